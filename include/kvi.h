@@ -583,6 +583,149 @@ KVI_API kvi_status kvi_store_file_info_read(const char *path, kvi_store_file_inf
 KVI_API kvi_status kvi_store_load(const char *path, void *kv, float *emb, int64_t *fact_start,
                                   int32_t *fact_len, uint32_t flags);
 
+/* Attention over the injected memory.
+ *
+ * Section 3.4's premise is that the engine runs its forward pass over blocks
+ * that already hold the memory prefix; these calls are that pass's attention.
+ * Query heads are grouped over KV heads: query head h reads KV head
+ * h / (q_heads / kv_heads).  Scores are scale * <q, k>, softmax statistics
+ * and sums are float32. */
+#define KVI_MAX_ATTN_HEAD_DIM 256 /* D, a multiple of 16 (4-bit cache: of 32) */
+#define KVI_MAX_ATTN_GROUP 128    /* q_heads / kv_heads */
+typedef struct {
+    int32_t q_heads;  /* Hq, a multiple of kv_heads */
+    int32_t kv_heads; /* H */
+    int32_t head_dim; /* D */
+    float scale;      /* of the scores, finite and > 0 (usually D^-0.5) */
+} kvi_attention;
+
+/* Device scratch bytes of kvi_attn_prompt for these sizes (as there); 0 for
+ * invalid ones. */
+KVI_API size_t kvi_attn_prompt_workspace_bytes(const kvi_attention *a, int32_t R, int32_t total_q,
+                                               int32_t max_q, int32_t max_ctx);
+
+/* Causal attention of R packed prompts over the paged bf16 cache (Section
+ * 3.4: the forward pass over the injected prefix).  Request r owns the query
+ * rows d_q_start[r] .. d_q_start[r+1]-1 (n of them, possibly none) and
+ * ctx = d_ctx_lens[r] keys: positions 0 .. ctx-1 of block table row r, the
+ * injected memory first and the prompt's own K/V last.  Its row i sees the
+ * positions <= ctx - n + i (so ctx == n is a whole prompt without memory, and
+ * n == 1 a decoding step).  A row that sees nothing gives zeros, and minus
+ * infinity in d_lse.  Keys and values that a row does not see have no effect
+ * on it, whatever they hold.
+ *   d_q      bf16 [total_q][Hq][D], rows q_row_stride elements apart
+ *   d_out    bf16 likewise, rows out_row_stride elements apart
+ *   d_lse    float32 [total_q][Hq] natural log of the sum of exp(score), or NULL
+ *   max_q, max_ctx   host upper bounds of every n and ctx
+ *   layer    which of cache->layer_base
+ * Pointers and rows of q and out are 16-byte aligned.  d_ws: >=
+ * kvi_attn_prompt_workspace_bytes, 256-byte aligned, no initialisation.
+ * Device-side errors (*d_status): KVI_ERR_OUT_OF_RANGE for a request whose
+ * rows lie outside [0, total_q), exceed max_q or whose ctx is negative or
+ * exceeds max_ctx or its block table (its outputs are not written), and for
+ * a block id outside the pool (that block's keys are left out);
+ * KVI_ERR_TIMEOUT when a wait for the kernel's own copies gave up.
+ * Errors: KVI_ERR_INVALID_ARG, KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const void *d_q,
+                                   int64_t q_row_stride, const int32_t *d_q_start, int32_t total_q,
+                                   int32_t max_q, const int32_t *d_ctx_lens, int32_t max_ctx,
+                                   const int32_t *d_block_tables, int32_t max_blocks,
+                                   const kvi_paged_cache *cache, int32_t layer, void *d_out,
+                                   int64_t out_row_stride, float *d_lse, void *d_ws, size_t ws_bytes,
+                                   int32_t *d_status, kvi_stream_t stream);
+
+/* The 4-bit cache: a paged pool at 4.5 bits per element instead of 16.  It is
+ * described by a kvi_paged_cache whose block_size is a multiple of 16 and
+ * whose layer_base buffers each hold [num_blocks][H] pages of
+ * kvi_cache4_layer_bytes / (num_blocks * H) bytes.  A row of D channels is
+ * kept as D / 32 groups, each with a bf16 step = bf16(max |x| / 7) and codes
+ * round(x / step) in [-7, 7] (ties to even); a group whose step is zero holds
+ * zeros, and one with an infinity or NaN reads back as NaN.  With G = D / 32
+ * and B = block_size a page is, back to back:
+ *   K codes [B][4][G] 32-bit words: word (t, g) has the channels
+ *           32 g + 8 t + n in nibble n = 0..7 (bits 4 n ..), as code + 8
+ *   V codes [B/2][8][G] words: word (s, g) has the channels 32 g + 4 s + j of
+ *           token 2 i in nibble j and of token 2 i + 1 in nibble 4 + j
+ *   K steps [B][G] bf16     V steps [B/2][G][2] bf16 (tokens 2 i, 2 i + 1)
+ * Returns 0 for invalid sizes (D not a multiple of 32 up to
+ * KVI_MAX_ATTN_HEAD_DIM, block_size not a multiple of 16, counts < 1). */
+KVI_API size_t kvi_cache4_layer_bytes(int32_t kv_heads, int32_t head_dim, int32_t num_blocks,
+                                      int32_t block_size);
+
+/* Store T rows into the 4-bit cache (Section 3.4's scatter-copy, into pages
+ * of another type): row t of d_k and d_v (bf16 [T][H][D], rows
+ * k_row_stride / v_row_stride elements apart) goes to slot d_slots[t] =
+ * block * block_size + offset; a negative slot skips the row.  The rows may be
+ * a step's new K/V, or the planes of a bf16 pool (T = num_blocks *
+ * block_size rows), which converts it.  No slot may appear twice.  Row
+ * pointers and strides are 16-byte aligned.  Device-side error:
+ * KVI_ERR_OUT_OF_RANGE (slot beyond the pool; row skipped).
+ * Errors: KVI_ERR_INVALID_ARG, KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_cache4_write(int32_t kv_heads, int32_t head_dim, const kvi_paged_cache *cache,
+                                    int32_t layer, int64_t T, const void *d_k, int64_t k_row_stride,
+                                    const void *d_v, int64_t v_row_stride, const int64_t *d_slots,
+                                    int32_t *d_status, kvi_stream_t stream);
+
+/* Read T rows back as bf16 (step * code, rounded to nearest even), the
+ * counterpart of kvi_cache4_write: rows with a negative slot, or (recorded)
+ * one beyond the pool, are left as they are. */
+KVI_API kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const kvi_paged_cache *cache,
+                                   int32_t layer, int64_t T, const int64_t *d_slots, void *d_k,
+                                   int64_t k_row_stride, void *d_v, int64_t v_row_stride,
+                                   int32_t *d_status, kvi_stream_t stream);
+
+/* Device scratch bytes of kvi_attn_decode4 for these sizes (weights != 0: with
+ * accumulated weights); 0 for invalid ones. */
+KVI_API size_t kvi_attn_decode4_workspace_bytes(const kvi_attention *a, int32_t R, int32_t max_ctx,
+                                                int32_t weights);
+
+/* One decoding step of R requests over the 4-bit cache: row r of d_q (bf16
+ * [R][Hq][D], rows q_row_stride elements apart) attends to the slots
+ * 0 .. d_ctx_lens[r]-1 of block table row r.  d_out as d_q.  With d_weights
+ * (float32 [R][H][weights_stride]) the softmax weight of every slot, summed
+ * over the query heads of its KV head, is added to d_weights[r][h][slot]:
+ * the score kvi_cache4_evict ranks by.  d_ws and the device-side errors are as
+ * for kvi_attn_prompt.  Errors: KVI_ERR_INVALID_ARG (also weights_stride <
+ * max_ctx), KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const void *d_q,
+                                    int64_t q_row_stride, const int32_t *d_ctx_lens, int32_t max_ctx,
+                                    const int32_t *d_block_tables, int32_t max_blocks,
+                                    const kvi_paged_cache *cache, int32_t layer, void *d_out,
+                                    int64_t out_row_stride, float *d_weights, int64_t weights_stride,
+                                    void *d_ws, size_t ws_bytes, int32_t *d_status,
+                                    kvi_stream_t stream);
+
+/* Device scratch bytes of kvi_cache4_evict; 0 for invalid sizes. */
+KVI_API size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int32_t max_ctx);
+
+/* Cut each request's 4-bit cache of one layer back to at most `budget` slots,
+ * head by head.  Kept are, in this order until the budget is full: the slots
+ * whose position d_pos is < sink or among the newest (> the head's largest
+ * position - recent), then those with the largest accumulated weight; ties
+ * go to the lower slot, NaN weights count above infinity.  Kept rows at slots >= budget move
+ * into the freed slots below it (the i-th freed slot takes the i-th such
+ * row); the others stay where they are, so attention over the slots
+ * 0 .. min(ctx, budget)-1 sees exactly the kept keys (their rotary positions
+ * are in the keys already).  Rows at slots >= budget are read, never written.
+ *   d_weights, d_pos          float32 / int32 [R][H][stride], read
+ *   d_weights_out, d_pos_out  likewise, written for slots < ctx: those of the
+ *                             kept rows, then 0 and -1; other buffers than
+ *                             the inputs
+ *   d_ctx_out                 [R] min(ctx, budget); another buffer than d_ctx_lens
+ * 1 <= budget, 0 <= sink, recent, sink + recent <= budget, stride >= max_ctx.
+ * Device-side errors: KVI_ERR_OUT_OF_RANGE for a ctx that is negative or
+ * exceeds max_ctx or its block table (the request is left as it is, its
+ * outputs unwritten), and for a block id outside the pool (its rows are not
+ * moved).  Errors: KVI_ERR_INVALID_ARG, KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_cache4_evict(int32_t kv_heads, int32_t head_dim, int32_t R,
+                                    const kvi_paged_cache *cache, int32_t layer,
+                                    const int32_t *d_ctx_lens, int32_t max_ctx,
+                                    const int32_t *d_block_tables, int32_t max_blocks, int32_t budget,
+                                    int32_t sink, int32_t recent, const float *d_weights,
+                                    const int32_t *d_pos, int64_t stride, float *d_weights_out,
+                                    int32_t *d_pos_out, int32_t *d_ctx_out, void *d_ws,
+                                    size_t ws_bytes, int32_t *d_status, kvi_stream_t stream);
+
 /* Diagnostic: one warp waits on a shared-memory barrier that nothing
  * completes, with the bounded wait every staging kernel of this library
  * uses; after limit_ns (1 us .. 1 s) of %globaltimer it gives up, records

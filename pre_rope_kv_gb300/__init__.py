@@ -28,4 +28,8 @@ from ._binding import (  # noqa: F401
     kvi_graph_search, graph_search_params, kvi_graph_retrieve_and_inject_workspace_bytes,
     kvi_graph_retrieve_and_inject, kvi_selftest_bounded_wait, open_library, use_library,
     kvi_debug_stall_scorer_row, kvi_debug_stall_coarse_chunk, kvi_selftest_stream_read,
+    MAX_ATTN_HEAD_DIM, MAX_ATTN_GROUP, Attention, attention, cache4, kvi_attn_prompt_workspace_bytes,
+    kvi_attn_prompt, kvi_cache4_layer_bytes, kvi_cache4_write, kvi_cache4_read,
+    kvi_attn_decode4_workspace_bytes, kvi_attn_decode4, kvi_cache4_evict_workspace_bytes,
+    kvi_cache4_evict,
 )

@@ -40,8 +40,13 @@ EXPORTED_SYMBOLS = (
     "kvi_store_file_info_read", "kvi_store_load", "kvi_graph_build_workspace_bytes",
     "kvi_graph_build", "kvi_graph_search_workspace_bytes", "kvi_graph_search",
     "kvi_graph_retrieve_and_inject_workspace_bytes", "kvi_graph_retrieve_and_inject",
-    "kvi_selftest_bounded_wait", "kvi_selftest_stream_read",
+    "kvi_selftest_bounded_wait", "kvi_selftest_stream_read", "kvi_attn_prompt_workspace_bytes",
+    "kvi_attn_prompt", "kvi_cache4_layer_bytes", "kvi_cache4_write", "kvi_cache4_read",
+    "kvi_attn_decode4_workspace_bytes", "kvi_attn_decode4", "kvi_cache4_evict_workspace_bytes",
+    "kvi_cache4_evict",
 )
+MAX_ATTN_HEAD_DIM = 256
+MAX_ATTN_GROUP = 128
 MAX_GRAPH_DEGREE = 128
 MAX_GRAPH_BEAM = 256
 MAX_GRAPH_FRONTIER = 512
@@ -97,6 +102,12 @@ class StoreFileInfo(ctypes.Structure):
 class GraphSearchParams(ctypes.Structure):
     _fields_ = [("beam", ctypes.c_int32), ("width", ctypes.c_int32), ("max_iters", ctypes.c_int32),
                 ("n_seeds", ctypes.c_int32)]
+
+
+class Attention(ctypes.Structure):
+    """kvi_attention: grouped heads and the scale of the scores."""
+    _fields_ = [("q_heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class PagedCache(ctypes.Structure):
@@ -172,6 +183,20 @@ def open_library(path: str):
                                               P, P, sz, P, P]),
         "kvi_selftest_bounded_wait": (S, [ctypes.c_uint64, P, P, P]),
         "kvi_selftest_stream_read": (S, [P, sz, i32, P, P]),
+        "kvi_attn_prompt_workspace_bytes": (sz, [ctypes.POINTER(Attention), i32, i32, i32, i32]),
+        "kvi_attn_prompt": (S, [ctypes.POINTER(Attention), i32, P, i64, P, i32, i32, P, i32, P, i32,
+                                ctypes.POINTER(PagedCache), i32, P, i64, P, P, sz, P, P]),
+        "kvi_cache4_layer_bytes": (sz, [i32, i32, i32, i32]),
+        "kvi_cache4_write": (S, [i32, i32, ctypes.POINTER(PagedCache), i32, i64, P, i64, P, i64, P,
+                                 P, P]),
+        "kvi_cache4_read": (S, [i32, i32, ctypes.POINTER(PagedCache), i32, i64, P, P, i64, P, i64,
+                                P, P]),
+        "kvi_attn_decode4_workspace_bytes": (sz, [ctypes.POINTER(Attention), i32, i32, i32]),
+        "kvi_attn_decode4": (S, [ctypes.POINTER(Attention), i32, P, i64, P, i32, P, i32,
+                                 ctypes.POINTER(PagedCache), i32, P, i64, P, i64, P, sz, P, P]),
+        "kvi_cache4_evict_workspace_bytes": (sz, [i32, i32, i32]),
+        "kvi_cache4_evict": (S, [i32, i32, i32, ctypes.POINTER(PagedCache), i32, P, i32, P, i32, i32,
+                                 i32, i32, P, P, i64, P, P, P, P, sz, P, P]),
         "kvi_status_str": (ctypes.c_char_p, [S]),
         "kvi_last_error": (ctypes.c_char_p, []),
     }
@@ -565,6 +590,153 @@ def kvi_graph_retrieve_and_inject(store: StoreView, graph, degree: int, R: int, 
         int(max_blocks), ctypes.byref(c), ctypes.byref(rope), _ptr(ids), _ptr(scores), _ptr(pos),
         _ptr(ws), ws.numel() * ws.element_size(), _ptr(status), _stream(stream)),
         "kvi_graph_retrieve_and_inject")
+
+
+# ------------------------------------------- attention over the cached memory
+
+def attention(q_heads: int, kv_heads: int, head_dim: int, scale: float | None = None) -> Attention:
+    """A kvi_attention; scale defaults to head_dim ** -0.5."""
+    return Attention(int(q_heads), int(kv_heads), int(head_dim),
+                     float(head_dim) ** -0.5 if scale is None else float(scale))
+
+
+class _Cache4:
+    """A 4-bit pool and the heads its pages are laid out for."""
+
+    def __init__(self, layer_tensors, block_size: int, kv_heads: int, head_dim: int):
+        one = load_library().kvi_cache4_layer_bytes(int(kv_heads), int(head_dim), 1, int(block_size))
+        blocks = (layer_tensors[0].numel() * layer_tensors[0].element_size()) // one if one else 0
+        for t in layer_tensors:
+            if one and t.numel() * t.element_size() != blocks * one:
+                raise ValueError(f"every layer of a 4-bit cache holds the same number of blocks of {one} bytes")
+        ptrs = [t.data_ptr() for t in layer_tensors]
+        self._arr = (ctypes.c_void_p * len(ptrs))(*ptrs)
+        self.struct = PagedCache(ctypes.cast(self._arr, ctypes.POINTER(ctypes.c_void_p)),
+                                 len(ptrs), blocks, int(block_size))
+        self.layer_tensors = list(layer_tensors)
+        self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
+
+
+def cache4(layer_tensors, block_size: int, kv_heads: int, head_dim: int) -> _Cache4:
+    """Describe a 4-bit pool: one uint8 tensor per layer, of
+    kvi_cache4_layer_bytes(kv_heads, head_dim, num_blocks, block_size) bytes
+    (any shape, e.g. [num_blocks][H][page bytes])."""
+    return _Cache4(layer_tensors, block_size, kv_heads, head_dim)
+
+
+def _rows(t, heads: int, head_dim: int, name: str):
+    """Address and row stride of bf16 rows [n][heads][head_dim] (a row may be
+    part of a wider one, e.g. of a fused projection)."""
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+        raise ValueError(f"{name} must be bfloat16 [rows][{heads}][{head_dim}]")
+    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+        raise ValueError(f"the rows of {name} must be contiguous")
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * head_dim)
+
+
+def _same_rows(n: int, name: str, t):
+    if t.shape[0] != n:
+        raise ValueError(f"{name} has {t.shape[0]} rows, {n} are needed")
+
+
+def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
+    return load_library().kvi_attn_prompt_workspace_bytes(ctypes.byref(a), int(R), int(total_q),
+                                                          int(max_q), int(max_ctx))
+
+
+def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int, block_tables, cache,
+                    layer: int, out, ws, status, lse=None, stream=None) -> None:
+    """Causal attention of packed prompts over the paged bf16 cache: q and out
+    [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
+    int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
+    c = cache.struct if hasattr(cache, "struct") else cache
+    qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
+    op, os_ = _rows(out, a.q_heads, a.head_dim, "out")
+    _same_rows(q.shape[0], "out", out)
+    _check(load_library().kvi_attn_prompt(
+        ctypes.byref(a), ctx_lens.shape[0], qp, qs, _ptr(q_start), q.shape[0], int(max_q),
+        _ptr(ctx_lens), int(max_ctx), _ptr(block_tables), block_tables.shape[1], ctypes.byref(c),
+        int(layer), op, os_, _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
+        _stream(stream)), "kvi_attn_prompt")
+
+
+def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:
+    return load_library().kvi_cache4_layer_bytes(int(kv_heads), int(head_dim), int(num_blocks),
+                                                 int(block_size))
+
+
+def kvi_cache4_write(cache: _Cache4, layer: int, k, v, slots, status, stream=None) -> None:
+    """Store rows k, v [T][H][D] bf16 at slots int64 [T] (negative: skipped)."""
+    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v")
+    _same_rows(slots.shape[0], "k", k)
+    _same_rows(slots.shape[0], "v", v)
+    _check(load_library().kvi_cache4_write(
+        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), slots.shape[0], kp, ks,
+        vp, vs, _ptr(slots), _ptr(status), _stream(stream)), "kvi_cache4_write")
+
+
+def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None) -> None:
+    """Read the rows at slots int64 [T] back into k, v [T][H][D] bf16."""
+    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k")
+    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v")
+    _same_rows(slots.shape[0], "k", k)
+    _same_rows(slots.shape[0], "v", v)
+    _check(load_library().kvi_cache4_read(
+        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), slots.shape[0],
+        _ptr(slots), kp, ks, vp, vs, _ptr(status), _stream(stream)), "kvi_cache4_read")
+
+
+def kvi_attn_decode4_workspace_bytes(a: Attention, R: int, max_ctx: int, weights: bool) -> int:
+    return load_library().kvi_attn_decode4_workspace_bytes(ctypes.byref(a), int(R), int(max_ctx),
+                                                           1 if weights else 0)
+
+
+def _weights(t, R: int, H: int, name: str):
+    if t.dim() != 3 or tuple(t.shape[:2]) != (R, H) or not t.is_contiguous() or t.element_size() != 4:
+        raise ValueError(f"{name} must be contiguous [{R}][{H}][slots] of 4-byte elements")
+    return t.data_ptr()
+
+
+def kvi_attn_decode4(a: Attention, q, ctx_lens, max_ctx: int, block_tables, cache: _Cache4, layer: int,
+                     out, ws, status, weights=None, stream=None) -> None:
+    """One decoding step over the 4-bit cache: q and out [R][Hq][D] bf16;
+    weights float32 [R][H][slots] accumulates each slot's softmax weight."""
+    if (a.kv_heads, a.head_dim) != (cache.kv_heads, cache.head_dim):
+        raise ValueError("the attention and the 4-bit cache have different heads")
+    R = ctx_lens.shape[0]
+    qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
+    op, os_ = _rows(out, a.q_heads, a.head_dim, "out")
+    _same_rows(R, "q", q)
+    _same_rows(R, "out", out)
+    wp = None if weights is None else _weights(weights, R, a.kv_heads, "weights")
+    _check(load_library().kvi_attn_decode4(
+        ctypes.byref(a), R, qp, qs, _ptr(ctx_lens), int(max_ctx), _ptr(block_tables),
+        block_tables.shape[1], ctypes.byref(cache.struct), int(layer), op, os_, wp,
+        0 if weights is None else weights.shape[2], _ptr(ws), ws.numel() * ws.element_size(),
+        _ptr(status), _stream(stream)), "kvi_attn_decode4")
+
+
+def kvi_cache4_evict_workspace_bytes(kv_heads: int, R: int, max_ctx: int) -> int:
+    return load_library().kvi_cache4_evict_workspace_bytes(int(kv_heads), int(R), int(max_ctx))
+
+
+def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_tables, budget: int,
+                     sink: int, recent: int, weights, pos, weights_out, pos_out, ctx_out, ws, status,
+                     stream=None) -> None:
+    """Cut a layer of the 4-bit cache back to `budget` slots per request and
+    head by accumulated weight (weights float32, pos int32: [R][H][slots])."""
+    R, H = ctx_lens.shape[0], cache.kv_heads
+    ptrs = [_weights(t, R, H, n) for t, n in ((weights, "weights"), (pos, "pos"),
+                                              (weights_out, "weights_out"), (pos_out, "pos_out"))]
+    if len({t.shape[2] for t in (weights, pos, weights_out, pos_out)}) > 1:
+        raise ValueError("weights and positions, in and out, must have the same number of slots")
+    _check(load_library().kvi_cache4_evict(
+        H, cache.head_dim, R, ctypes.byref(cache.struct), int(layer), _ptr(ctx_lens), int(max_ctx),
+        _ptr(block_tables), block_tables.shape[1], int(budget), int(sink), int(recent), ptrs[0], ptrs[1],
+        weights.shape[2], ptrs[2], ptrs[3], _ptr(ctx_out), _ptr(ws), ws.numel() * ws.element_size(),
+        _ptr(status), _stream(stream)), "kvi_cache4_evict")
 
 
 def kvi_selftest_bounded_wait(limit_ns: int, status, elapsed_ns=None, stream=None) -> None:

@@ -1,0 +1,148 @@
+// kvi_attn.cuh -- shared by the attention kernels (kvi_attn_prompt.cu,
+// kvi_attn_decode4.cu) and the 4-bit cache (kvi_cache4.cu): the tensor-core
+// and conversion helpers, the 4-bit page layout, and the join of partial
+// results of work split over a long axis.  Not part of the public ABI.
+//
+// Softmax in pieces.  With s_p = scale <q, k_p> in units of log2 (scale
+// times log2 e), a piece of the keys is summed up by (m, l, o): m a number no
+// smaller than max s_p - kLazy, l = sum 2^(s_p - m) and o = sum 2^(s_p - m)
+// v_p, all float32.  Pieces join by M = max m: l = sum l_i 2^(m_i - M), o
+// likewise; the output is o / l and the log of the sum (M + log2 l) ln 2.
+// A piece no key of which is visible has m = -inf and l = 0, o = 0.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kvi_internal.cuh"
+
+namespace kvi {
+
+// ------------------------------------------------------- 4-bit page layout
+//
+// One page holds B tokens (a multiple of 16) of one KV head: the codes of K
+// and V, then their steps; G = D / 32 groups of 32 channels.  The order
+// inside follows the matrix instruction's fragments, so that a lane's share
+// of 16 tokens is a few wide loads and needs no shuffle:
+//   K codes  [B][4][G] words: word (t, g) = channels 32 g + 8 t + n, nibble n
+//   V codes  [B/2][8][G] words: word (s, g) = channels 32 g + 4 s + j of token
+//            2 i (nibble j) and of token 2 i + 1 (nibble 4 + j)
+//   K steps  [B][G] bf16            V steps  [B/2][G][2] bf16
+// An element is step * (nibble - 8).
+struct Page4 {
+    int32_t B, D;
+    __host__ __device__ int groups() const { return D / 32; }
+    __host__ __device__ int64_t bytes() const { return (int64_t)B * D + (int64_t)B * groups() * 4; }
+    __host__ __device__ int64_t v_codes() const { return (int64_t)B * D / 2; }
+    __host__ __device__ int64_t k_steps() const { return (int64_t)B * D; }
+    __host__ __device__ int64_t v_steps() const { return (int64_t)B * D + (int64_t)B * groups() * 2; }
+};
+
+// ------------------------------------------------------------------ joining
+
+struct JoinParams {
+    const float *po;         // [rows][S][D]
+    const float2 *ml;        // [rows][S] (m in log2 units, l)
+    int32_t S, span;         // splits, keys per split
+    int32_t R, q_heads, D;
+    const int32_t *q_start;  // [R + 1] or null: one row per request
+    int32_t total_q, max_q;
+    const int32_t *ctx_lens;  // [R]
+    int32_t max_ctx, max_blocks, block_size;
+    __nv_bfloat16 *out;
+    int64_t out_stride;
+    float *lse;              // [total_q][q_heads] or null
+};
+cudaError_t launch_join(const JoinParams &p, cudaStream_t s);
+
+// The checks of the attention calls' shared arguments (a message is recorded).
+kvi_status check_attention(const kvi_attention *a);
+kvi_status check_pages(const kvi_paged_cache *c, int32_t layer, int32_t R, int32_t max_blocks,
+                       const void *block_tables);
+kvi_status cache4_check(int32_t kv_heads, int32_t head_dim, const kvi_paged_cache *c, int32_t layer);
+// Record the message as KVI_ERR_INVALID_ARG; a CUDA error as KVI_ERR_CUDA.
+kvi_status arg_error(const char *fmt, ...);
+// Whether a pointer is NULL or not aligned to `a` bytes.
+inline bool unusable(const void *p, uintptr_t a) { return !p || reinterpret_cast<uintptr_t>(p) % a != 0; }
+kvi_status cuda_status(cudaError_t e, const char *where);
+
+#ifdef __CUDACC__
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The reference m of a running softmax moves only when a score passes it by
+// more than 2^kLazy: sums and outputs then stay below 2^kLazy per key, far
+// inside float32, and the accumulators are rescaled a few times per row
+// instead of once per tile.
+constexpr float kLazy = 8.0f;
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xff800000u); }
+
+// 2^x (the hardware's approximation, 2 ulp; -inf gives 0)
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// D (16x8, float32) += A (16x16 bf16, row) B (16x8 bf16, col)
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// An 8x8 matrix of 16-bit elements (row = lane / 4, a pair of columns per
+// lane) transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+}  // namespace
+
+// The rows and keys of request r, or false when its lengths are not usable.
+struct RequestSpan {
+    int32_t q0, n_q, ctx;
+};
+__device__ __forceinline__ bool request_span(int r, const int32_t *q_start, int total_q, int max_q,
+                                             const int32_t *ctx_lens, int max_ctx, int max_blocks, int block_size,
+                                             RequestSpan &o)
+{
+    o.q0 = q_start ? q_start[r] : r;
+    const int q1 = q_start ? q_start[r + 1] : r + 1;
+    o.ctx = ctx_lens[r];
+    o.n_q = q1 - o.q0;
+    return o.q0 >= 0 && q1 >= o.q0 && q1 <= total_q && o.n_q <= max_q && o.ctx >= 0 && o.ctx <= max_ctx &&
+           (int64_t)o.ctx <= (int64_t)max_blocks * block_size;
+}
+
+#endif  // __CUDACC__
+
+}  // namespace kvi
