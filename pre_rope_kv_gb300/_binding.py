@@ -273,10 +273,20 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_current = None  # (torch.cuda.current_device, raw handle of a device's current stream)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current
+        if _current is None:
+            import torch
+            # the handle itself, where this torch offers it: a Stream object
+            # built for every call costs more than the call's launch
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            _current = (torch.cuda.current_device,
+                        raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+        return _current[1](_current[0]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -624,20 +634,25 @@ def cache4(layer_tensors, block_size: int, kv_heads: int, head_dim: int) -> _Cac
     return _Cache4(layer_tensors, block_size, kv_heads, head_dim)
 
 
-def _rows(t, heads: int, head_dim: int, name: str):
+_bf16 = None  # torch.bfloat16, once a call has needed it
+
+
+def _rows(t, heads: int, head_dim: int, name: str, n: int = -1):
     """Address and row stride of bf16 rows [n][heads][head_dim] (a row may be
-    part of a wider one, e.g. of a fused projection)."""
-    import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or tuple(t.shape[1:]) != (heads, head_dim):
+    part of a wider one, e.g. of a fused projection); n < 0: any number."""
+    global _bf16
+    if _bf16 is None:
+        import torch
+        _bf16 = torch.bfloat16
+    shape = t.shape
+    if t.dtype is not _bf16 or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError(f"{name} must be bfloat16 [rows][{heads}][{head_dim}]")
-    if t.shape[0] and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)):
+    if n >= 0 and shape[0] != n:
+        raise ValueError(f"{name} has {shape[0]} rows, {n} are needed")
+    row, head, one = t.stride()
+    if shape[0] and (one != 1 or (heads > 1 and head != head_dim)):
         raise ValueError(f"the rows of {name} must be contiguous")
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else heads * head_dim)
-
-
-def _same_rows(n: int, name: str, t):
-    if t.shape[0] != n:
-        raise ValueError(f"{name} has {t.shape[0]} rows, {n} are needed")
+    return t.data_ptr(), (row if shape[0] > 1 else heads * head_dim)
 
 
 def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
@@ -651,11 +666,11 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
     [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
     int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
     c = cache.struct if hasattr(cache, "struct") else cache
+    total = q.shape[0]
     qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
-    op, os_ = _rows(out, a.q_heads, a.head_dim, "out")
-    _same_rows(q.shape[0], "out", out)
+    op, os_ = _rows(out, a.q_heads, a.head_dim, "out", total)
     _check(load_library().kvi_attn_prompt(
-        ctypes.byref(a), ctx_lens.shape[0], qp, qs, _ptr(q_start), q.shape[0], int(max_q),
+        ctypes.byref(a), ctx_lens.shape[0], qp, qs, _ptr(q_start), total, int(max_q),
         _ptr(ctx_lens), int(max_ctx), _ptr(block_tables), block_tables.shape[1], ctypes.byref(c),
         int(layer), op, os_, _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
         _stream(stream)), "kvi_attn_prompt")
@@ -668,23 +683,21 @@ def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_
 
 def kvi_cache4_write(cache: _Cache4, layer: int, k, v, slots, status, stream=None) -> None:
     """Store rows k, v [T][H][D] bf16 at slots int64 [T] (negative: skipped)."""
-    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v")
-    _same_rows(slots.shape[0], "k", k)
-    _same_rows(slots.shape[0], "v", v)
+    T = slots.shape[0]
+    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k", T)
+    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_write(
-        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), slots.shape[0], kp, ks,
-        vp, vs, _ptr(slots), _ptr(status), _stream(stream)), "kvi_cache4_write")
+        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), T, kp, ks, vp, vs,
+        _ptr(slots), _ptr(status), _stream(stream)), "kvi_cache4_write")
 
 
 def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None) -> None:
     """Read the rows at slots int64 [T] back into k, v [T][H][D] bf16."""
-    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k")
-    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v")
-    _same_rows(slots.shape[0], "k", k)
-    _same_rows(slots.shape[0], "v", v)
+    T = slots.shape[0]
+    kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k", T)
+    vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_read(
-        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), slots.shape[0],
+        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), T,
         _ptr(slots), kp, ks, vp, vs, _ptr(status), _stream(stream)), "kvi_cache4_read")
 
 
@@ -694,7 +707,8 @@ def kvi_attn_decode4_workspace_bytes(a: Attention, R: int, max_ctx: int, weights
 
 
 def _weights(t, R: int, H: int, name: str):
-    if t.dim() != 3 or tuple(t.shape[:2]) != (R, H) or not t.is_contiguous() or t.element_size() != 4:
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != R or shape[1] != H or not t.is_contiguous() or t.element_size() != 4:
         raise ValueError(f"{name} must be contiguous [{R}][{H}][slots] of 4-byte elements")
     return t.data_ptr()
 
@@ -706,10 +720,8 @@ def kvi_attn_decode4(a: Attention, q, ctx_lens, max_ctx: int, block_tables, cach
     if (a.kv_heads, a.head_dim) != (cache.kv_heads, cache.head_dim):
         raise ValueError("the attention and the 4-bit cache have different heads")
     R = ctx_lens.shape[0]
-    qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
-    op, os_ = _rows(out, a.q_heads, a.head_dim, "out")
-    _same_rows(R, "q", q)
-    _same_rows(R, "out", out)
+    qp, qs = _rows(q, a.q_heads, a.head_dim, "q", R)
+    op, os_ = _rows(out, a.q_heads, a.head_dim, "out", R)
     wp = None if weights is None else _weights(weights, R, a.kv_heads, "weights")
     _check(load_library().kvi_attn_decode4(
         ctypes.byref(a), R, qp, qs, _ptr(ctx_lens), int(max_ctx), _ptr(block_tables),

@@ -115,10 +115,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+// (hi + lo) * s of two bf16 numbers each, lo no larger than hi's rounding: one
+// rounding of the product to bf16 (lo * s rounds far below it)
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t hi, uint32_t lo, uint32_t s)
 {
-    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&hi);
+    const __nv_bfloat162 l = *reinterpret_cast<const __nv_bfloat162 *>(&lo);
+    const __nv_bfloat162 f = *reinterpret_cast<const __nv_bfloat162 *>(&s);
+    const __nv_bfloat162 v = __hfma2(h, f, __hmul2(l, f));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 

@@ -9,29 +9,32 @@
 // its group), so the products are taken as S^T = K Q^T (16 keys x 8 heads)
 // and O^T = V^T P^T (16 channels x 8 heads): up to 8 heads fill N without
 // padding, half of what heads on M = 16 would pad to.  The page layout is
-// this instruction's fragment order, so a lane loads its share of 16 tokens
-// with a few wide loads straight into registers.
+// this instruction's fragment order, so a lane reads its share of 16 tokens
+// with a few wide loads.
 //   K: a group's product is taken of the bare codes and then scaled by the
 //      key's step in float32 (step * code has 12 significant bits and would
 //      not fit a bf16 operand).
-//   V: the step belongs to (key, group), and a key is summed over, so P is
-//      scaled: P and P * step round to bf16, as any P on tensor cores does.
+//   V: the step belongs to (key, group), and a key is summed over, so it is P
+//      that is scaled; P * step rounds to bf16, as any P on tensor cores does.
 //   A code c in the low nibble of a 16-bit half, or'ed with 0x4300, is the
 //      bf16 number 128 + c; 136 is subtracted exactly.
-// A warp takes tiles of 16 keys in turn with a softmax of its own; the warps of
-// a block join at the end, and blocks that share a request's keys join in a
+// A warp takes tiles of 16 keys in turn, from a ring of its own that bulk copies
+// fill four tiles ahead, with a softmax of its own; the warps of a block join at the end, and blocks that share a request's keys join in a
 // second kernel.
 #include <cuda_runtime.h>
 
 #include <algorithm>
 
 #include "kvi_attn.cuh"
+#include "kvi_sync.cuh"
 
 namespace kvi {
 
 namespace {
 
 constexpr int kWarps4 = 4;
+constexpr int kStages4 = 4;  // tiles of 16 keys that a warp has in flight
+constexpr uint64_t kWait4Ns = 1000000000ull;
 constexpr int kPlanSms = 152;
 
 struct Decode4Params {
@@ -56,15 +59,15 @@ struct Decode4Params {
     int32_t *status;
 };
 
-// N 32-bit words from p, with the widest loads their count allows (p is
-// aligned to that width).
+// N 32-bit words from shared memory, with the widest loads their count allows
+// (p is aligned to that width).
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
 {
     if constexpr (N % 4 == 0) {
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
             w[4 * i] = v.x;
             w[4 * i + 1] = v.y;
             w[4 * i + 2] = v.z;
@@ -73,13 +76,13 @@ __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t *p)
     } else if constexpr (N % 2 == 0) {
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p) + i);
+            const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
             w[2 * i] = v.x;
             w[2 * i + 1] = v.y;
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = __ldg(reinterpret_cast<const uint32_t *>(p) + i);
+        for (int i = 0; i < N; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
     }
 }
 
@@ -93,65 +96,48 @@ __device__ __forceinline__ void load_halves(uint32_t (&w)[(N + 1) / 2], const ui
         const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
 #pragma unroll
         for (int i = 0; i < (N + 1) / 2; ++i)
-            w[i] = (uint32_t)__ldg(h + 2 * i) | (2 * i + 1 < N ? (uint32_t)__ldg(h + 2 * i + 1) << 16 : 0u);
+            w[i] = (uint32_t)h[2 * i] | (2 * i + 1 < N ? (uint32_t)h[2 * i + 1] << 16 : 0u);
     }
 }
 
-// The codes in nibbles 0 and 4 of w as two bf16 numbers
+// The codes in nibbles 0 and 4 of w as two bf16 numbers, plus 128 + 8
+__device__ __forceinline__ uint32_t codes_plus136(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
+
 __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w)
 {
-    const uint32_t b = (w & 0x000f000fu) | 0x43004300u;
+    const uint32_t b = codes_plus136(w);
     const uint32_t off = 0x43084308u;  // 136, 136
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&off));
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// This lane's share of 16 tokens of a page.
-template <int NG>
-struct Tile4 {
-    uint32_t kc[2][NG];            // keys lane / 4 and + 8
-    uint32_t ks[2][(NG + 1) / 2];  // their steps
-    uint32_t vc[2][NG];            // token pairs lane % 4 and + 4
-    uint32_t vs[2][NG];            // their steps (both tokens of the pair)
-    bool live;                     // false: nothing was read (bad block)
-};
-
-template <int NG>
-__device__ __forceinline__ void load_tile(Tile4<NG> &x, const Decode4Params &p, const int32_t *table, int h, int tile)
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t *src, uint32_t bytes, uint32_t bar)
 {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int k0 = tile * 16;
-    const int b = table[k0 / p.page.B];
-    x.live = b >= 0 && b < p.num_blocks;
-    if (!x.live) {
-        if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-#pragma unroll
-            for (int j = 0; j < NG; ++j) x.kc[i][j] = x.vc[i][j] = x.vs[i][j] = 0;
-#pragma unroll
-            for (int j = 0; j < (NG + 1) / 2; ++j) x.ks[i][j] = 0;
-        }
-        return;
-    }
-    const uint8_t *page = p.pool + ((int64_t)b * p.H + h) * p.page.bytes();
-    const int off = k0 % p.page.B;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int key = off + g + 8 * i, pair = off / 2 + t + 4 * i;
-        load_words<NG>(x.kc[i], page + (int64_t)key * (NG * 16) + t * (NG * 4));
-        load_words<NG>(x.vc[i], page + p.page.v_codes() + (int64_t)pair * (NG * 32) + g * (NG * 4));
-        load_halves<NG>(x.ks[i], page + p.page.k_steps() + (int64_t)key * (NG * 2));
-        load_words<NG>(x.vs[i], page + p.page.v_steps() + (int64_t)pair * (NG * 4));
-    }
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
 }
 
+// Shared memory of a block: each warp's ring of 16-token stages (the order of
+// a page of 16 tokens: K codes, V codes, K steps, V steps), reused for the join.
 template <int NG, int NT>
-__global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_constant__ Decode4Params p)
+struct Smem4 {
+    static constexpr int kCodes = 256 * NG, kSteps = 32 * NG;
+    static constexpr int kStage = 2 * kCodes + 2 * kSteps;
+    static constexpr int kRing = kStages4 * kStage;
+    static constexpr int kJoin = kWarps4 * 8 * NT * (32 * NG + 4) * 4;
+    static constexpr int kBytes = kWarps4 * kRing > kJoin ? kWarps4 * kRing : kJoin;
+};
+
+template <int NG, int NT>
+__global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? 4 : NG * NT <= 6 ? 3 : 2)
+decode4_kernel(const __grid_constant__ Decode4Params p)
 {
+    using Sm = Smem4<NG, NT>;
     constexpr int D = NG * 32;
-    __shared__ float s_o[kWarps4][8 * NT][D + 4];
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t s_bar[kWarps4][kStages4];
     __shared__ float s_m[kWarps4][8 * NT], s_l[kWarps4][8 * NT];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x;
@@ -165,6 +151,62 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
     const int from = split * p.span, to = min(rq.ctx, from + p.span);
     if (from >= to && split > 0) return;  // split 0 writes the zeros of an empty cache
     const bool whole = rq.ctx <= p.span;
+
+    // ---- this warp's tiles: from / 16 + warp, + kWarps4, ...; a stage each
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kStages4; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    uint8_t *ring = smem + warp * Sm::kRing;
+    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+    const int t1 = (to + 15) / 16, tile0 = from / 16 + warp;
+    const int per_page = p.page.B / 16;
+    const int64_t page_bytes = p.page.bytes(), block_bytes = page_bytes * p.H;
+    const uint8_t *pool = p.pool + h * page_bytes;
+    // the next tile to copy: its place in the table and in its page, stepped
+    // by kWarps4 tiles without a division; its block is read a tile ahead, so
+    // that the two latencies do not add up
+    int c_tile = tile0, c_page = tile0 / per_page, c_sub = tile0 % per_page;
+    const int d_page = kWarps4 / per_page, d_sub = kWarps4 % per_page;
+    int c_block = c_tile < t1 ? __ldg(table + c_page) : 0;
+    uint32_t dead = 0;  // stages that hold nothing (a block outside the pool)
+    auto issue = [&](int stage) {
+        if (c_tile < t1) {
+            const bool live = c_block >= 0 && c_block < p.num_blocks;
+            dead = live ? dead & ~(1u << stage) : dead | (1u << stage);
+            if (lane == 0) {
+                const uint32_t bar = smem_u32(&s_bar[warp][stage]), dst = smem_u32(ring + stage * Sm::kStage);
+                if (live) {
+                    const uint8_t *page = pool + c_block * block_bytes;
+                    mbar_expect_tx(bar, Sm::kStage);
+                    if (per_page == 1) {
+                        bulk_copy(dst, page, Sm::kStage, bar);
+                    } else {
+                        bulk_copy(dst, page + c_sub * Sm::kCodes, Sm::kCodes, bar);
+                        bulk_copy(dst + Sm::kCodes, page + p.page.v_codes() + c_sub * Sm::kCodes, Sm::kCodes, bar);
+                        bulk_copy(dst + 2 * Sm::kCodes, page + p.page.k_steps() + c_sub * Sm::kSteps, Sm::kSteps, bar);
+                        bulk_copy(dst + 2 * Sm::kCodes + Sm::kSteps, page + p.page.v_steps() + c_sub * Sm::kSteps,
+                                  Sm::kSteps, bar);
+                    }
+                } else {
+                    record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+                    mbar_arrive(bar);
+                }
+            }
+            c_tile += kWarps4;
+            c_page += d_page;
+            c_sub += d_sub;
+            if (c_sub >= per_page) {
+                c_sub -= per_page;
+                ++c_page;
+            }
+            c_block = c_tile < t1 ? __ldg(table + c_page) : 0;
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kStages4; ++i) issue(i);
 
     // Q as B fragments: word (a, b) of group j is channels 32 j + 8 t + 2 a + b
     // and + 4, the order of the codes' nibbles
@@ -185,26 +227,38 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
         }
     }
     float o[NT][2 * NG][4];
-    float m[NT][2], l[NT][2];
+    // per column (head): the reference m in the scores' own units, the score
+    // that moves it, m as the exponent's offset (0 while nothing is seen), and
+    // this lane's share of the sum
+    float m[NT][2], limit[NT][2], ref[NT][2], l[NT][2];
+    const float lazy = kLazy / p.scale;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-        m[nt][0] = m[nt][1] = neg_inf();
-        l[nt][0] = l[nt][1] = 0.f;
+        m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = neg_inf();
+        ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.f;
     }
 
-    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
-    const int t1 = (to + 15) / 16;
-    int tile = from / 16 + warp;
-    Tile4<NG> x;
-    if (tile < t1) load_tile<NG>(x, p, table, h, tile);
-    for (; tile < t1; tile += kWarps4) {
-        Tile4<NG> y;
-        if (tile + kWarps4 < t1) load_tile<NG>(y, p, table, h, tile + kWarps4);
-        // ---- scores: rows g and g + 8 of the tile, heads 2 t and 2 t + 1
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int tile = tile0; tile < t1; tile += kWarps4) {
+        if (!mbar_wait(smem_u32(&s_bar[warp][stage]), phase, kWait4Ns)) {
+            record_status(p.status, KVI_ERR_TIMEOUT);
+            break;
+        }
+        const uint8_t *st = ring + stage * Sm::kStage;
+        const int end = (dead >> stage) & 1u ? 0 : to;  // keys at and past it are not there
+        const bool partly = tile * 16 + 16 > end;
+        uint32_t kc[2][NG], ks[2][(NG + 1) / 2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            load_words<NG>(kc[i], st + (g + 8 * i) * (NG * 16) + t * (NG * 4));
+            load_halves<NG>(ks[i], st + 2 * Sm::kCodes + (g + 8 * i) * (NG * 2));
+        }
+        // ---- scores: keys g and g + 8 of the tile, heads 2 t and 2 t + 1
         float s[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -212,8 +266,8 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
             for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            const float k0 = (j & 1) ? bf16_hi(x.ks[0][j / 2]) : bf16_lo(x.ks[0][j / 2]);
-            const float k1 = (j & 1) ? bf16_hi(x.ks[1][j / 2]) : bf16_lo(x.ks[1][j / 2]);
+            const float k0 = (j & 1) ? bf16_hi(ks[0][j / 2]) : bf16_lo(ks[0][j / 2]);
+            const float k1 = (j & 1) ? bf16_hi(ks[1][j / 2]) : bf16_lo(ks[1][j / 2]);
             float part[NT][4];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -221,8 +275,8 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
                 for (int i = 0; i < 4; ++i) part[nt][i] = 0.f;
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                const uint32_t a0 = codes_bf16x2(x.kc[0][j] >> (8 * a)), a1 = codes_bf16x2(x.kc[1][j] >> (8 * a));
-                const uint32_t a2 = codes_bf16x2(x.kc[0][j] >> (8 * a + 4)), a3 = codes_bf16x2(x.kc[1][j] >> (8 * a + 4));
+                const uint32_t a0 = codes_bf16x2(kc[0][j] >> (8 * a)), a1 = codes_bf16x2(kc[1][j] >> (8 * a));
+                const uint32_t a2 = codes_bf16x2(kc[0][j] >> (8 * a + 4)), a3 = codes_bf16x2(kc[1][j] >> (8 * a + 4));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
                     mma16816(part[nt], a0, a1, a2, a3, qf[nt][2 * j + a][0], qf[nt][2 * j + a][1]);
@@ -236,23 +290,28 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
             }
         }
         const int key = tile * 16 + g;
-        const bool in0 = x.live && key < to, in1 = x.live && key + 8 < to;
+        if (partly) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (key + (i >> 1) * 8 >= end) s[nt][i] = neg_inf();
+        }
         bool move = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] = (i < 2 ? in0 : in1) ? s[nt][i] * p.scale : neg_inf();
-            move |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kLazy || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kLazy;
-        }
+        for (int nt = 0; nt < NT; ++nt)
+            move |= fmaxf(s[nt][0], s[nt][2]) > limit[nt][0] || fmaxf(s[nt][1], s[nt][3]) > limit[nt][1];
         if (p.scores) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int head = c0 + 8 * nt + 2 * t;
                 float *sc = p.scores + (((int64_t)r * p.H + h) * p.max_ctx + key) * p.score_stride + head;
                 if (head < p.score_stride) {
-                    if (key < to) *reinterpret_cast<float2 *>(sc) = make_float2(s[nt][0], s[nt][1]);
+                    if (key < to)
+                        *reinterpret_cast<float2 *>(sc) = make_float2(s[nt][0] * p.scale, s[nt][1] * p.scale);
                     if (key + 8 < to)
-                        *reinterpret_cast<float2 *>(sc + 8 * p.score_stride) = make_float2(s[nt][2], s[nt][3]);
+                        *reinterpret_cast<float2 *>(sc + 8 * p.score_stride) =
+                            make_float2(s[nt][2] * p.scale, s[nt][3] * p.scale);
                 }
             }
         }
@@ -265,9 +324,11 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     // each column goes by its own scores alone
-                    if (!(top > m[nt][c] + kLazy)) continue;
-                    const float f = exp2_fast(m[nt][c] - top);
+                    if (!(top > limit[nt][c])) continue;
+                    const float f = exp2_fast((m[nt][c] - top) * p.scale);
                     m[nt][c] = top;
+                    limit[nt][c] = top + lazy;
+                    ref[nt][c] = top * p.scale;
                     l[nt][c] *= f;
 #pragma unroll
                     for (int i = 0; i < 2 * NG; ++i) {
@@ -276,48 +337,79 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
                     }
                 }
         }
-        // ---- weights, as B fragments: keys 2 t, 2 t + 1 (and + 8) of head g
-        uint32_t b0[NT], b1[NT];
+        // ---- weights, as B fragments: keys 2 t, 2 t + 1 (and + 8) of head g,
+        // in two parts, P = hi + lo, so that P * step rounds to bf16 once
+        uint32_t b0[NT], b1[NT], r0[NT], r1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = m[nt][0] == neg_inf() ? 0.f : m[nt][0], m1 = m[nt][1] == neg_inf() ? 0.f : m[nt][1];
-            const float p0 = exp2_fast(s[nt][0] - m0), p1 = exp2_fast(s[nt][1] - m1);
-            const float p2 = exp2_fast(s[nt][2] - m0), p3 = exp2_fast(s[nt][3] - m1);
+            const float p0 = exp2_fast(fmaf(s[nt][0], p.scale, -ref[nt][0]));
+            const float p1 = exp2_fast(fmaf(s[nt][1], p.scale, -ref[nt][1]));
+            const float p2 = exp2_fast(fmaf(s[nt][2], p.scale, -ref[nt][0]));
+            const float p3 = exp2_fast(fmaf(s[nt][3], p.scale, -ref[nt][1]));
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
-            b0[nt] = transpose8x8(pack_bf16(p0, p1));
-            b1[nt] = transpose8x8(pack_bf16(p2, p3));
+            const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
+            b0[nt] = transpose8x8(h0);
+            b1[nt] = transpose8x8(h1);
+            r0[nt] = transpose8x8(pack_bf16(p0 - bf16_lo(h0), p1 - bf16_hi(h0)));
+            r1[nt] = transpose8x8(pack_bf16(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
+        }
+        uint32_t vc[2][NG], vs[2][NG];  // token pairs t and t + 4
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            load_words<NG>(vc[i], st + Sm::kCodes + (t + 4 * i) * (NG * 32) + g * (NG * 4));
+            load_words<NG>(vs[i], st + 2 * Sm::kCodes + Sm::kSteps + (t + 4 * i) * (NG * 4));
         }
         // slots past the end have weight 0, but their steps may hold anything
-        if (tile * 16 + 16 > to) {
-            const uint32_t lo = tile * 16 + 2 * t < to ? 0x0000ffffu : 0u, hi = tile * 16 + 2 * t + 1 < to ? 0xffff0000u : 0u;
-            const uint32_t lo8 = tile * 16 + 2 * t + 8 < to ? 0x0000ffffu : 0u;
-            const uint32_t hi8 = tile * 16 + 2 * t + 9 < to ? 0xffff0000u : 0u;
+        if (partly) {
+            const int k = tile * 16 + 2 * t;
+            const uint32_t keep0 = (k < end ? 0x0000ffffu : 0u) | (k + 1 < end ? 0xffff0000u : 0u);
+            const uint32_t keep1 = (k + 8 < end ? 0x0000ffffu : 0u) | (k + 9 < end ? 0xffff0000u : 0u);
 #pragma unroll
             for (int j = 0; j < NG; ++j) {
-                x.vs[0][j] &= lo | hi;
-                x.vs[1][j] &= lo8 | hi8;
+                vs[0][j] &= keep0;
+                vs[1][j] &= keep1;
             }
         }
+        __syncwarp();  // the stage is in registers
+        issue(stage);
         // ---- output: channels 32 j + 4 g + 2 a (+ 1), heads 2 t and 2 t + 1
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             uint32_t w0[NT], w1[NT];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                w0[nt] = mul_bf16x2(b0[nt], x.vs[0][j]);
-                w1[nt] = mul_bf16x2(b1[nt], x.vs[1][j]);
+                w0[nt] = scale_bf16x2(b0[nt], r0[nt], vs[0][j]);
+                w1[nt] = scale_bf16x2(b1[nt], r1[nt], vs[1][j]);
             }
 #pragma unroll
             for (int a = 0; a < 2; ++a) {
-                const uint32_t a0 = codes_bf16x2(x.vc[0][j] >> (8 * a)), a1 = codes_bf16x2(x.vc[0][j] >> (8 * a + 4));
-                const uint32_t a2 = codes_bf16x2(x.vc[1][j] >> (8 * a)), a3 = codes_bf16x2(x.vc[1][j] >> (8 * a + 4));
+                const uint32_t a0 = codes_bf16x2(vc[0][j] >> (8 * a)), a1 = codes_bf16x2(vc[0][j] >> (8 * a + 4));
+                const uint32_t a2 = codes_bf16x2(vc[1][j] >> (8 * a)), a3 = codes_bf16x2(vc[1][j] >> (8 * a + 4));
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * j + a], a0, a1, a2, a3, w0[nt], w1[nt]);
             }
         }
-        x = y;
+        if (++stage == kStages4) {
+            stage = 0;
+            phase ^= 1u;
+        }
     }
+    // after a wait that gave up: no copy may still be writing when the rings
+    // are reused (bounded; the outputs are not valid, as the status says)
+    if (c_tile > tile0) {
+        const int issued = (c_tile - tile0) / kWarps4;
+        if (lane < kStages4 && lane < issued) {
+            const int last = (issued - 1 - lane) / kStages4;
+            if (!mbar_wait(smem_u32(&s_bar[warp][lane]), (uint32_t)(last & 1), kWait4Ns))
+                record_status(p.status, KVI_ERR_TIMEOUT);
+        }
+    }
+    __syncthreads();
+    float *s_o = reinterpret_cast<float *>(smem);
+    constexpr int kO = D + 4;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) m[nt][0] *= p.scale, m[nt][1] *= p.scale;
 
     // ---- the block's warps join
 #pragma unroll
@@ -333,7 +425,7 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
             }
 #pragma unroll
             for (int j = 0; j < NG; ++j)
-                *reinterpret_cast<float4 *>(&s_o[warp][n][32 * j + 4 * g]) =
+                *reinterpret_cast<float4 *>(s_o + (warp * 8 * NT + n) * kO + 32 * j + 4 * g) =
                     make_float4(o[nt][2 * j][c], o[nt][2 * j][c + 2], o[nt][2 * j + 1][c], o[nt][2 * j + 1][c + 2]);
         }
     }
@@ -351,8 +443,9 @@ __global__ void __launch_bounds__(kWarps4 * 32) decode4_kernel(const __grid_cons
         for (int w = 0; w < kWarps4; ++w) {
             const float f = exp2_fast(s_m[w][n] - ref);
             L += s_l[w][n] * f;
-            acc.x += s_o[w][n][d] * f;
-            acc.y += s_o[w][n][d + 1] * f;
+            const float *src = s_o + (w * 8 * NT + n) * kO + d;
+            acc.x += src[0] * f;
+            acc.y += src[1] * f;
         }
         const int64_t row = (int64_t)r * p.Hq + (int64_t)h * p.G + c0 + n;
         if (whole) {
@@ -447,7 +540,12 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
 template <int NG, int NT>
 cudaError_t run4(const Decode4Params &p, int32_t R, cudaStream_t s)
 {
-    decode4_kernel<NG, NT><<<dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R), kWarps4 * 32, 0, s>>>(p);
+    constexpr int bytes = Smem4<NG, NT>::kBytes;
+    if (bytes > 48 * 1024) {
+        const cudaError_t e = smem_opt_in(decode4_kernel<NG, NT>, bytes);
+        if (e != cudaSuccess) return e;
+    }
+    decode4_kernel<NG, NT><<<dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R), kWarps4 * 32, bytes, s>>>(p);
     return cudaGetLastError();
 }
 

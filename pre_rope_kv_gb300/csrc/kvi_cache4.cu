@@ -154,8 +154,8 @@ __global__ void __launch_bounds__(kRowThreads) cache4_read_kernel(const RowParam
 
 // ----------------------------------------------------------------- eviction
 //
-// Per request and head: the budget-th largest rank is found byte by byte
-// (four counting passes over the ranks), then one ordered pass marks the kept
+// Per request and head: the budget-th largest rank is found 11 bits at a time
+// (three counting passes over the ranks), then one ordered pass marks the kept
 // slots (ties in slot order) and lists the freed slots below the budget and
 // the kept ones above it.  Both lists have the same length; the second
 // kernel copies row for row.
@@ -177,11 +177,14 @@ struct EvictParams {
     int32_t *holes, *tails;  // [R][H][most] slots
     int32_t *moves;          // [R][H]
     int32_t most;            // moves a row can need
+    int32_t cap;             // ranks kept in shared memory
     int32_t *status;
 };
 
 constexpr int kEvictThreads = 1024;
 constexpr int kMoveThreads = 256;
+constexpr int kBins = 2048;           // two per thread
+constexpr int kRankCap = 24 * 1024;   // ranks kept in shared memory (two blocks fit an SM)
 
 // Rank order of a slot as an unsigned number: protected slots first, then
 // by weight (-0 as 0, NaN above infinity).
@@ -191,6 +194,23 @@ __device__ __forceinline__ uint32_t evict_rank(float w, int pos, int sink, int64
     if (w != w) return 0xfffffffeu;
     const uint32_t b = __float_as_uint(w + 0.0f);
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// Sum of v over the threads before this one.
+__device__ __forceinline__ int block_sum_before(int v, int *warp_sums)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int sum = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += u;
+    }
+    if (lane == 31) warp_sums[warp] = sum;
+    __syncthreads();
+    int before = lane < warp ? warp_sums[lane] : 0;
+    before = __reduce_add_sync(0xffffffffu, before);
+    return before + sum - v;
 }
 
 // Exclusive prefix sum over the block of a 0/1 flag; `total` for everybody.
@@ -219,8 +239,9 @@ __device__ __forceinline__ int block_rank(bool flag, int *warp_sums, int &total)
 
 __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictParams p)
 {
+    extern __shared__ uint32_t s_rank[];  // of the first p.cap slots
     __shared__ int s_warp[33];
-    __shared__ int s_hist[256];
+    __shared__ int s_hist[kBins];
     __shared__ int s_newest, s_digit, s_left;
     const int h = blockIdx.x % p.H, r = blockIdx.x / p.H, tid = threadIdx.x;
     const int64_t row = (int64_t)blockIdx.x;
@@ -229,6 +250,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     float *w_out = p.w_out + row * p.stride;
     int32_t *pos_out = p.pos_out + row * p.stride;
     const int n = p.ctx_lens[r];
+    pdl_launch_dependents();
     if (n < 0 || n > p.max_ctx || (int64_t)n > (int64_t)p.max_blocks * p.page.B) {
         if (tid == 0) {
             record_status(p.status, KVI_ERR_OUT_OF_RANGE);
@@ -247,29 +269,44 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
         return;
     }
     if (tid == 0) s_newest = INT32_MIN;
+    for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = 0;
     __syncthreads();
     int newest = INT32_MIN;
     for (int i = tid; i < n; i += kEvictThreads) newest = max(newest, pos[i]);
-    atomicMax(&s_newest, newest);
+    newest = __reduce_max_sync(0xffffffffu, newest);
+    if ((tid & 31) == 0) atomicMax(&s_newest, newest);
     __syncthreads();
     const int64_t from = (int64_t)s_newest - p.recent + 1;
+    auto rank_of = [&](int i) { return i < p.cap ? s_rank[i] : evict_rank(w[i], pos[i], p.sink, from); };
 
-    // the budget-th largest rank, from its highest byte down
+    // the budget-th largest rank, 11, 11 and 10 bits at a time from the top
     uint32_t found = 0;
-    int want = p.budget;  // of the slots that share the bytes found so far
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) s_hist[tid] = 0;
-        __syncthreads();
+    int want = p.budget;  // of the slots that share the bits found so far
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
         for (int i = tid; i < n; i += kEvictThreads) {
-            const uint32_t k = evict_rank(w[i], pos[i], p.sink, from);
-            if (shift == 24 || (k >> (shift + 8)) == (found >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255u], 1);
+            uint32_t k;
+            if (pass == 0) {
+                k = evict_rank(w[i], pos[i], p.sink, from);
+                if (i < p.cap) s_rank[i] = k;
+            } else {
+                k = rank_of(i);
+                if ((k ^ found) >> (pass == 1 ? 21 : 10)) continue;
+            }
+            atomicAdd(&s_hist[(k >> shift) & mask], 1);
         }
         __syncthreads();
-        if (tid == 0) {
-            int d = 255, c = want;
-            while (d > 0 && s_hist[d] < c) c -= s_hist[d--];
-            s_digit = d;
-            s_left = c;
+        // from the top bin down, two bins a thread: the one where the count
+        // passes `want`
+        const int hi = kBins - 1 - 2 * tid;
+        const int a = s_hist[hi], b = s_hist[hi - 1];
+        s_hist[hi] = s_hist[hi - 1] = 0;
+        const int above = block_sum_before(a + b, s_warp);
+        if (above < want && above + a + b >= want) {
+            s_digit = above + a >= want ? hi : hi - 1;
+            s_left = want - above - (above + a >= want ? 0 : a);
         }
         __syncthreads();
         found |= (uint32_t)s_digit << shift;
@@ -281,24 +318,27 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
         const int i = i0 + tid;
         const bool in = i < n;
-        const float wi = in ? w[i] : 0.f;
-        const int pi = in ? pos[i] : 0;
-        const uint32_t k = in ? evict_rank(wi, pi, p.sink, from) : 0u;
+        const uint32_t k = in ? rank_of(i) : 0u;
         const bool tie = in && k == found;
         int c;
         const int rank = ties + block_rank(tie, s_warp, c);
         ties += c;
         const bool keep = in && (k > found || (tie && rank < want));
         const bool hole = in && i < left && !keep, tail = keep && i >= left;
-        const int a = n_holes + block_rank(hole, s_warp, c);
-        n_holes += c;
-        if (hole) holes[a] = i;
-        const int b = n_tails + block_rank(tail, s_warp, c);
-        n_tails += c;
-        if (tail) tails[b] = i;
+        // a block's slots lie below the budget, above it, or (once) across it
+        if (i0 < left) {
+            const int at = n_holes + block_rank(hole, s_warp, c);
+            n_holes += c;
+            if (hole) holes[at] = i;
+        }
+        if (i0 + kEvictThreads > left) {
+            const int at = n_tails + block_rank(tail, s_warp, c);
+            n_tails += c;
+            if (tail) tails[at] = i;
+        }
         if (in && !hole) {
-            w_out[i] = i < left ? wi : 0.f;
-            pos_out[i] = i < left ? pi : -1;
+            w_out[i] = i < left ? w[i] : 0.f;
+            pos_out[i] = i < left ? pos[i] : -1;
         }
     }
     __syncthreads();
@@ -503,7 +543,10 @@ extern "C" kvi_status kvi_cache4_evict(int32_t kv_heads, int32_t head_dim, int32
     p.tails = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + list);
     p.moves = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + 2 * list);
     p.status = d_status;
-    evict_select_kernel<<<(unsigned)(R * kv_heads), kEvictThreads, 0, stream>>>(p);
+    p.cap = std::min(max_ctx, kRankCap);
+    cudaError_t e = smem_opt_in(evict_select_kernel, kRankCap * 4);
+    if (e != cudaSuccess) return cuda_status(e, "kvi_cache4_evict");
+    evict_select_kernel<<<(unsigned)(R * kv_heads), kEvictThreads, (size_t)p.cap * 4, stream>>>(p);
     st = cuda_status(cudaGetLastError(), "kvi_cache4_evict");
     if (st != KVI_OK || max_ctx <= budget) return st;  // nothing can move
     // enough warps that none copies more than a few rows, without a grid of
@@ -511,6 +554,15 @@ extern "C" kvi_status kvi_cache4_evict(int32_t kv_heads, int32_t head_dim, int32
     const int rows = std::min(p.most, budget);
     const int want = std::max(1, 4096 / (R * kv_heads));
     const unsigned gx = (unsigned)std::min((rows + kMoveThreads / 32 - 1) / (kMoveThreads / 32), want);
-    evict_move_kernel<<<dim3(gx, (unsigned)(R * kv_heads)), kMoveThreads, 0, stream>>>(p);
-    return cuda_status(cudaGetLastError(), "kvi_cache4_evict");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(gx, (unsigned)(R * kv_heads));
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
+    return cuda_status(e != cudaSuccess ? e : cudaGetLastError(), "kvi_cache4_evict");
 }
