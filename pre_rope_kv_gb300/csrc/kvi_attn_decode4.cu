@@ -18,9 +18,18 @@
 //      that is scaled; P * step rounds to bf16, as any P on tensor cores does.
 //   A code c in the low nibble of a 16-bit half, or'ed with 0x4300, is the
 //      bf16 number 128 + c; 136 is subtracted exactly.
-// A warp takes tiles of 16 keys in turn, from a ring of its own that bulk copies
-// fill four tiles ahead, with a softmax of its own; the warps of a block join at the end, and blocks that share a request's keys join in a
-// second kernel.
+// A warp takes pairs of tiles of 16 keys in turn, from a ring of its own that
+// bulk copies fill ahead of it, with a softmax of its own; the warps of a block
+// join at the end, and blocks that share a request's keys in a second kernel.
+//
+// What bounds it is the issue of the decoding instructions, not the bytes: 14
+// integer operations and 8 subtractions per 16 codes, with the softmax, make about 400 warp
+// instructions per tile of 2304 bytes (D = 128), where HBM delivers a tile in
+// the time of 390.  Two tiles an iteration share the bookkeeping and run
+// independently of one another (16 requests x 28 k keys, D = 128, 8 KV heads:
+// 152 us one tile at a time, 140 us two; 12 warps an SM instead of 16: 148 us;
+// shifts as multiplications: 166 us; the offset of V's codes taken off by a
+// second matrix product instead of a subtraction: 155 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -33,7 +42,7 @@ namespace kvi {
 namespace {
 
 constexpr int kWarps4 = 4;
-constexpr int kStages4 = 4;  // tiles of 16 keys that a warp has in flight
+constexpr int kStages4 = 2;  // pairs of tiles of 16 keys that a warp has in flight
 constexpr uint64_t kWait4Ns = 1000000000ull;
 constexpr int kPlanSms = 152;
 
@@ -100,12 +109,12 @@ __device__ __forceinline__ void load_halves(uint32_t (&w)[(N + 1) / 2], const ui
     }
 }
 
-// The codes in nibbles 0 and 4 of w as two bf16 numbers, plus 128 + 8
-__device__ __forceinline__ uint32_t codes_plus136(uint32_t w) { return (w & 0x000f000fu) | 0x43004300u; }
-
+// The codes in nibbles 0 and 4 of w as two bf16 numbers (one and-or, one
+// subtraction of 136)
 __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w)
 {
-    const uint32_t b = codes_plus136(w);
+    uint32_t b;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
     const uint32_t off = 0x43084308u;  // 136, 136
     const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b),
                                      *reinterpret_cast<const __nv_bfloat162 *>(&off));
@@ -119,12 +128,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t *src, uint
                  : "memory");
 }
 
-// Shared memory of a block: each warp's ring of 16-token stages (the order of
-// a page of 16 tokens: K codes, V codes, K steps, V steps), reused for the join.
+// Shared memory of a block: each warp's ring of stages, two tiles of 16 tokens
+// each (a tile in the order of a page of 16 tokens: K codes, V codes, K steps,
+// V steps), reused for the join.
 template <int NG, int NT>
 struct Smem4 {
     static constexpr int kCodes = 256 * NG, kSteps = 32 * NG;
-    static constexpr int kStage = 2 * kCodes + 2 * kSteps;
+    static constexpr int kTile = 2 * kCodes + 2 * kSteps;
+    static constexpr int kStage = 2 * kTile;
     static constexpr int kRing = kStages4 * kStage;
     static constexpr int kJoin = kWarps4 * 8 * NT * (32 * NG + 4) * 4;
     static constexpr int kBytes = kWarps4 * kRing > kJoin ? kWarps4 * kRing : kJoin;
@@ -152,7 +163,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     if (from >= to && split > 0) return;  // split 0 writes the zeros of an empty cache
     const bool whole = rq.ctx <= p.span;
 
-    // ---- this warp's tiles: from / 16 + warp, + kWarps4, ...; a stage each
+    // ---- this warp's pairs of tiles: from / 32 + warp, + kWarps4, ...; a stage each
     if (lane == 0) {
 #pragma unroll
         for (int i = 0; i < kStages4; ++i) mbar_init(smem_u32(&s_bar[warp][i]), 1);
@@ -161,52 +172,56 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     __syncwarp();
     uint8_t *ring = smem + warp * Sm::kRing;
     const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
-    const int t1 = (to + 15) / 16, tile0 = from / 16 + warp;
+    const int t1 = (to + 15) / 16, pair0 = from / 32 + warp;
     const int per_page = p.page.B / 16;
     const int64_t page_bytes = p.page.bytes(), block_bytes = page_bytes * p.H;
-    const uint8_t *pool = p.pool + h * page_bytes;
-    // the next tile to copy: its place in the table and in its page, stepped
-    // by kWarps4 tiles without a division; its block is read a tile ahead, so
-    // that the two latencies do not add up
-    int c_tile = tile0, c_page = tile0 / per_page, c_sub = tile0 % per_page;
-    const int d_page = kWarps4 / per_page, d_sub = kWarps4 % per_page;
-    int c_block = c_tile < t1 ? __ldg(table + c_page) : 0;
-    uint32_t dead = 0;  // stages that hold nothing (a block outside the pool)
+    // The copies of a stage, one lane each: lane % 4 is the part of the tile
+    // (K codes, V codes, K steps, V steps; a page of 16 tokens is one part) and
+    // lane / 4 the tile.  Each lane keeps its next tile's place in the table and in
+    // its page, stepped by a division made once, and reads the tile's block
+    // an iteration ahead, so that the two latencies do not add up.
+    const int part = lane & 3;
+    const bool copies = lane < 8 && (part == 0 || per_page > 1);
+    const uint32_t part_bytes = per_page == 1 ? Sm::kTile : part < 2 ? Sm::kCodes : Sm::kSteps;
+    const uint32_t part_dst = smem_u32(ring) + ((lane >> 2) & 1) * Sm::kTile +
+                              (part < 2 ? part * Sm::kCodes : 2 * Sm::kCodes + (part - 2) * Sm::kSteps);
+    const uint8_t *part_src = p.pool + h * page_bytes +
+                              (part == 0 ? 0 : part == 1 ? p.page.v_codes() : part == 2 ? p.page.k_steps() : p.page.v_steps());
+    int c_tile = 2 * pair0 + ((lane >> 2) & 1), c_page = c_tile / per_page, c_sub = c_tile % per_page;
+    const int d_page = 2 * kWarps4 / per_page, d_sub = 2 * kWarps4 % per_page;
+    int c_block = c_tile < t1 ? __ldg(table + c_page) : -1;
+    int issued = 0;     // stages that copies went out for
+    uint32_t dead = 0;  // bits 2 stage, + 1: a tile whose block lies outside the pool
     auto issue = [&](int stage) {
-        if (c_tile < t1) {
-            const bool live = c_block >= 0 && c_block < p.num_blocks;
-            dead = live ? dead & ~(1u << stage) : dead | (1u << stage);
-            if (lane == 0) {
-                const uint32_t bar = smem_u32(&s_bar[warp][stage]), dst = smem_u32(ring + stage * Sm::kStage);
-                if (live) {
-                    const uint8_t *page = pool + c_block * block_bytes;
-                    mbar_expect_tx(bar, Sm::kStage);
-                    if (per_page == 1) {
-                        bulk_copy(dst, page, Sm::kStage, bar);
-                    } else {
-                        bulk_copy(dst, page + c_sub * Sm::kCodes, Sm::kCodes, bar);
-                        bulk_copy(dst + Sm::kCodes, page + p.page.v_codes() + c_sub * Sm::kCodes, Sm::kCodes, bar);
-                        bulk_copy(dst + 2 * Sm::kCodes, page + p.page.k_steps() + c_sub * Sm::kSteps, Sm::kSteps, bar);
-                        bulk_copy(dst + 2 * Sm::kCodes + Sm::kSteps, page + p.page.v_steps() + c_sub * Sm::kSteps,
-                                  Sm::kSteps, bar);
-                    }
-                } else {
-                    record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-                    mbar_arrive(bar);
-                }
-            }
-            c_tile += kWarps4;
-            c_page += d_page;
-            c_sub += d_sub;
-            if (c_sub >= per_page) {
-                c_sub -= per_page;
-                ++c_page;
-            }
-            c_block = c_tile < t1 ? __ldg(table + c_page) : 0;
+        // a tile past the end is not copied: its keys are masked
+        const bool live = (uint32_t)c_block < (uint32_t)p.num_blocks;
+        const uint32_t lives = __ballot_sync(0xffffffffu, live) & 0x11u;
+        const uint32_t bar = smem_u32(&s_bar[warp][stage]);
+        if (lives != 0x11u) {
+            const uint32_t lost = __ballot_sync(0xffffffffu, !live && c_tile < t1) & 0x11u;
+            if (lost && lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+            dead = (dead & ~(3u << (2 * stage))) | (((lost & 1u) | (lost >> 3)) << (2 * stage));
+        } else if (dead) {
+            dead &= ~(3u << (2 * stage));
         }
+        if (lane == 0) mbar_expect_tx(bar, __popc(lives) * Sm::kTile);
+        __syncwarp();
+        if (copies && live)
+            bulk_copy(part_dst + stage * Sm::kStage, part_src + c_block * block_bytes + c_sub * part_bytes, part_bytes, bar);
+        ++issued;
+        c_tile += 2 * kWarps4;
+        c_page += d_page;
+        c_sub += d_sub;
+        if (c_sub >= per_page) {
+            c_sub -= per_page;
+            ++c_page;
+        }
+        c_block = c_tile < t1 ? __ldg(table + c_page) : -1;
     };
+    const int pairs = max(0, ((t1 + 1) / 2 - pair0 + kWarps4 - 1) / kWarps4);  // of this warp
 #pragma unroll
-    for (int i = 0; i < kStages4; ++i) issue(i);
+    for (int i = 0; i < kStages4; ++i)
+        if (i < pairs) issue(i);
 
     // Q as B fragments: word (a, b) of group j is channels 32 j + 8 t + 2 a + b
     // and + 4, the order of the codes' nibbles
@@ -244,83 +259,88 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
 
     int stage = 0;
     uint32_t phase = 0;
-    for (int tile = tile0; tile < t1; tile += kWarps4) {
+    for (int it = 0; it < pairs; ++it) {
         if (!mbar_wait(smem_u32(&s_bar[warp][stage]), phase, kWait4Ns)) {
             record_status(p.status, KVI_ERR_TIMEOUT);
             break;
         }
         const uint8_t *st = ring + stage * Sm::kStage;
-        const int end = (dead >> stage) & 1u ? 0 : to;  // keys at and past it are not there
-        const bool partly = tile * 16 + 16 > end;
-        uint32_t kc[2][NG], ks[2][(NG + 1) / 2];
+        const int k0 = (pair0 + it * kWarps4) * 32;  // the pair's first key
+        const uint32_t lost = dead >> (2 * stage);
+        const bool partly = k0 + 32 > to || (lost & 3u);
+        // keys of tile f: there are those below `to`, unless the tile is lost
+        const int end[2] = {lost & 1u ? 0 : to, lost & 2u ? 0 : to};
+        // ---- scores: keys g and g + 8 of each tile, heads 2 t and 2 t + 1
+        float s[2][NT][4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            load_words<NG>(kc[i], st + (g + 8 * i) * (NG * 16) + t * (NG * 4));
-            load_halves<NG>(ks[i], st + 2 * Sm::kCodes + (g + 8 * i) * (NG * 2));
-        }
-        // ---- scores: keys g and g + 8 of the tile, heads 2 t and 2 t + 1
-        float s[NT][4];
+        for (int f = 0; f < 2; ++f) {
+            uint32_t kc[2][NG], ks[2][(NG + 1) / 2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < 2; ++i) {
+                load_words<NG>(kc[i], st + f * Sm::kTile + (g + 8 * i) * (NG * 16) + t * (NG * 4));
+                load_halves<NG>(ks[i], st + f * Sm::kTile + 2 * Sm::kCodes + (g + 8 * i) * (NG * 2));
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][i] = 0.f;
+            for (int j = 0; j < NG; ++j) {
+                const float s0 = (j & 1) ? bf16_hi(ks[0][j / 2]) : bf16_lo(ks[0][j / 2]);
+                const float s1 = (j & 1) ? bf16_hi(ks[1][j / 2]) : bf16_lo(ks[1][j / 2]);
+                float sum[NT][4];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            const float k0 = (j & 1) ? bf16_hi(ks[0][j / 2]) : bf16_lo(ks[0][j / 2]);
-            const float k1 = (j & 1) ? bf16_hi(ks[1][j / 2]) : bf16_lo(ks[1][j / 2]);
-            float part[NT][4];
+                for (int a = 0; a < 2; ++a) {
+                    const uint32_t a0 = codes_bf16x2(kc[0][j] >> (8 * a)), a1 = codes_bf16x2(kc[1][j] >> (8 * a));
+                    const uint32_t a2 = codes_bf16x2(kc[0][j] >> (8 * a + 4)), a3 = codes_bf16x2(kc[1][j] >> (8 * a + 4));
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) part[nt][i] = 0.f;
-#pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const uint32_t a0 = codes_bf16x2(kc[0][j] >> (8 * a)), a1 = codes_bf16x2(kc[1][j] >> (8 * a));
-                const uint32_t a2 = codes_bf16x2(kc[0][j] >> (8 * a + 4)), a3 = codes_bf16x2(kc[1][j] >> (8 * a + 4));
+                    for (int nt = 0; nt < NT; ++nt) {
+                        if (a == 0)
+                            mma16816_first(sum[nt], a0, a1, a2, a3, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                        else
+                            mma16816(sum[nt], a0, a1, a2, a3, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                    }
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
-                    mma16816(part[nt], a0, a1, a2, a3, qf[nt][2 * j + a][0], qf[nt][2 * j + a][1]);
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                s[nt][0] = fmaf(k0, part[nt][0], s[nt][0]);
-                s[nt][1] = fmaf(k0, part[nt][1], s[nt][1]);
-                s[nt][2] = fmaf(k1, part[nt][2], s[nt][2]);
-                s[nt][3] = fmaf(k1, part[nt][3], s[nt][3]);
+                    for (int i = 0; i < 4; ++i)
+                        s[f][nt][i] = j ? fmaf(i < 2 ? s0 : s1, sum[nt][i], s[f][nt][i]) : (i < 2 ? s0 : s1) * sum[nt][i];
             }
         }
-        const int key = tile * 16 + g;
         if (partly) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int f = 0; f < 2; ++f)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (key + (i >> 1) * 8 >= end) s[nt][i] = neg_inf();
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (k0 + 16 * f + g + (i >> 1) * 8 >= end[f]) s[f][nt][i] = neg_inf();
         }
         bool move = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            move |= fmaxf(s[nt][0], s[nt][2]) > limit[nt][0] || fmaxf(s[nt][1], s[nt][3]) > limit[nt][1];
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+                move |= fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) > limit[nt][c];
         if (p.scores) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int head = c0 + 8 * nt + 2 * t;
-                float *sc = p.scores + (((int64_t)r * p.H + h) * p.max_ctx + key) * p.score_stride + head;
-                if (head < p.score_stride) {
-                    if (key < to)
-                        *reinterpret_cast<float2 *>(sc) = make_float2(s[nt][0] * p.scale, s[nt][1] * p.scale);
-                    if (key + 8 < to)
-                        *reinterpret_cast<float2 *>(sc + 8 * p.score_stride) =
-                            make_float2(s[nt][2] * p.scale, s[nt][3] * p.scale);
+            for (int f = 0; f < 2; ++f)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int head = c0 + 8 * nt + 2 * t, key = k0 + 16 * f + g;
+                    float *sc = p.scores + (((int64_t)r * p.H + h) * p.max_ctx + key) * p.score_stride + head;
+                    if (head < p.score_stride) {
+                        if (key < to)
+                            *reinterpret_cast<float2 *>(sc) = make_float2(s[f][nt][0] * p.scale, s[f][nt][1] * p.scale);
+                        if (key + 8 < to)
+                            *reinterpret_cast<float2 *>(sc + 8 * p.score_stride) =
+                                make_float2(s[f][nt][2] * p.scale, s[f][nt][3] * p.scale);
+                    }
                 }
-            }
         }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float top = fmaxf(s[nt][c], s[nt][c + 2]);
+                    float top = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
 #pragma unroll
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     // each column goes by its own scores alone
@@ -339,55 +359,62 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
         }
         // ---- weights, as B fragments: keys 2 t, 2 t + 1 (and + 8) of head g,
         // in two parts, P = hi + lo, so that P * step rounds to bf16 once
-        uint32_t b0[NT], b1[NT], r0[NT], r1[NT];
+        uint32_t b0[2][NT], b1[2][NT], r0[2][NT], r1[2][NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float p0 = exp2_fast(fmaf(s[nt][0], p.scale, -ref[nt][0]));
-            const float p1 = exp2_fast(fmaf(s[nt][1], p.scale, -ref[nt][1]));
-            const float p2 = exp2_fast(fmaf(s[nt][2], p.scale, -ref[nt][0]));
-            const float p3 = exp2_fast(fmaf(s[nt][3], p.scale, -ref[nt][1]));
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
-            b0[nt] = transpose8x8(h0);
-            b1[nt] = transpose8x8(h1);
-            r0[nt] = transpose8x8(pack_bf16(p0 - bf16_lo(h0), p1 - bf16_hi(h0)));
-            r1[nt] = transpose8x8(pack_bf16(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
-        }
-        uint32_t vc[2][NG], vs[2][NG];  // token pairs t and t + 4
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            load_words<NG>(vc[i], st + Sm::kCodes + (t + 4 * i) * (NG * 32) + g * (NG * 4));
-            load_words<NG>(vs[i], st + 2 * Sm::kCodes + Sm::kSteps + (t + 4 * i) * (NG * 4));
-        }
-        // slots past the end have weight 0, but their steps may hold anything
-        if (partly) {
-            const int k = tile * 16 + 2 * t;
-            const uint32_t keep0 = (k < end ? 0x0000ffffu : 0u) | (k + 1 < end ? 0xffff0000u : 0u);
-            const uint32_t keep1 = (k + 8 < end ? 0x0000ffffu : 0u) | (k + 9 < end ? 0xffff0000u : 0u);
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                vs[0][j] &= keep0;
-                vs[1][j] &= keep1;
-            }
-        }
-        __syncwarp();  // the stage is in registers
-        issue(stage);
-        // ---- output: channels 32 j + 4 g + 2 a (+ 1), heads 2 t and 2 t + 1
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            uint32_t w0[NT], w1[NT];
+        for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                w0[nt] = scale_bf16x2(b0[nt], r0[nt], vs[0][j]);
-                w1[nt] = scale_bf16x2(b1[nt], r1[nt], vs[1][j]);
+                const float p0 = exp2_fast(fmaf(s[f][nt][0], p.scale, -ref[nt][0]));
+                const float p1 = exp2_fast(fmaf(s[f][nt][1], p.scale, -ref[nt][1]));
+                const float p2 = exp2_fast(fmaf(s[f][nt][2], p.scale, -ref[nt][0]));
+                const float p3 = exp2_fast(fmaf(s[f][nt][3], p.scale, -ref[nt][1]));
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
+                b0[f][nt] = transpose8x8(h0);
+                b1[f][nt] = transpose8x8(h1);
+                r0[f][nt] = transpose8x8(pack_bf16(p0 - bf16_lo(h0), p1 - bf16_hi(h0)));
+                r1[f][nt] = transpose8x8(pack_bf16(p2 - bf16_lo(h1), p3 - bf16_hi(h1)));
+            }
+        // ---- output: channels 32 j + 4 g + 2 a (+ 1), heads 2 t and 2 t + 1
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            uint32_t vc[2][NG], vs[2][NG];  // token pairs t and t + 4
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                load_words<NG>(vc[i], st + f * Sm::kTile + Sm::kCodes + (t + 4 * i) * (NG * 32) + g * (NG * 4));
+                load_words<NG>(vs[i], st + f * Sm::kTile + 2 * Sm::kCodes + Sm::kSteps + (t + 4 * i) * (NG * 4));
+            }
+            // slots past the end have weight 0, but their steps may hold anything
+            if (partly) {
+                const int k = k0 + 16 * f + 2 * t;
+                const uint32_t keep0 = (k < end[f] ? 0x0000ffffu : 0u) | (k + 1 < end[f] ? 0xffff0000u : 0u);
+                const uint32_t keep1 = (k + 8 < end[f] ? 0x0000ffffu : 0u) | (k + 9 < end[f] ? 0xffff0000u : 0u);
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    vs[0][j] &= keep0;
+                    vs[1][j] &= keep1;
+                }
+            }
+            if (f == 1) {
+                __syncwarp();  // the stage is in registers
+                if (it + kStages4 < pairs) issue(stage);
             }
 #pragma unroll
-            for (int a = 0; a < 2; ++a) {
-                const uint32_t a0 = codes_bf16x2(vc[0][j] >> (8 * a)), a1 = codes_bf16x2(vc[0][j] >> (8 * a + 4));
-                const uint32_t a2 = codes_bf16x2(vc[1][j] >> (8 * a)), a3 = codes_bf16x2(vc[1][j] >> (8 * a + 4));
+            for (int j = 0; j < NG; ++j) {
+                uint32_t w0[NT], w1[NT];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * j + a], a0, a1, a2, a3, w0[nt], w1[nt]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    w0[nt] = scale_bf16x2(b0[f][nt], r0[f][nt], vs[0][j]);
+                    w1[nt] = scale_bf16x2(b1[f][nt], r1[f][nt], vs[1][j]);
+                }
+#pragma unroll
+                for (int a = 0; a < 2; ++a) {
+                    const uint32_t a0 = codes_bf16x2(vc[0][j] >> (8 * a)), a1 = codes_bf16x2(vc[0][j] >> (8 * a + 4));
+                    const uint32_t a2 = codes_bf16x2(vc[1][j] >> (8 * a)), a3 = codes_bf16x2(vc[1][j] >> (8 * a + 4));
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * j + a], a0, a1, a2, a3, w0[nt], w1[nt]);
+                }
             }
         }
         if (++stage == kStages4) {
@@ -397,13 +424,10 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     }
     // after a wait that gave up: no copy may still be writing when the rings
     // are reused (bounded; the outputs are not valid, as the status says)
-    if (c_tile > tile0) {
-        const int issued = (c_tile - tile0) / kWarps4;
-        if (lane < kStages4 && lane < issued) {
-            const int last = (issued - 1 - lane) / kStages4;
-            if (!mbar_wait(smem_u32(&s_bar[warp][lane]), (uint32_t)(last & 1), kWait4Ns))
-                record_status(p.status, KVI_ERR_TIMEOUT);
-        }
+    if (lane < kStages4 && lane < issued) {
+        const int last = (issued - 1 - lane) / kStages4;
+        if (!mbar_wait(smem_u32(&s_bar[warp][lane]), (uint32_t)(last & 1), kWait4Ns))
+            record_status(p.status, KVI_ERR_TIMEOUT);
     }
     __syncthreads();
     float *s_o = reinterpret_cast<float *>(smem);
@@ -522,11 +546,12 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     // two blocks of 8 heads share each decoded tile where registers allow
     pl.nt = G > 8 && a.head_dim <= 128 ? 2 : 1;
     pl.chunks = (G + 8 * pl.nt - 1) / (8 * pl.nt);
-    // enough blocks for four on every SM, but none below 256 keys (four tiles a warp)
+    // enough blocks for four on every SM, twice, but none below 256 keys (two pairs
+    // of tiles a warp)
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
     const int64_t want = std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
     int64_t span = (max_ctx + want - 1) / want;
-    span = std::max<int64_t>(256, (span + 63) / 64 * 64);
+    span = std::max<int64_t>(256, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
     pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
     const size_t rq = (size_t)R * a.q_heads;
