@@ -11,6 +11,7 @@
 // A piece no key of which is visible has m = -inf and l = 0, o = 0.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -56,6 +57,40 @@ struct JoinParams {
     float *lse;              // [total_q][q_heads] or null
 };
 cudaError_t launch_join(const JoinParams &p, cudaStream_t s);
+
+// ------------------------------------------------------- attention of prompts
+
+struct PromptParams {
+    const __nv_bfloat16 *q;
+    int64_t q_stride;
+    const int32_t *q_start;
+    int32_t total_q, max_q;
+    const int32_t *ctx_lens;
+    int32_t max_ctx, max_blocks;
+    const int32_t *block_tables;
+    int32_t num_blocks, B;
+    int32_t H, Hq, G, D;
+    const __nv_bfloat16 *pool;  // [2][num_blocks][B][H][D]
+    float scale;                // times log2 e
+    __nv_bfloat16 *out;
+    int64_t out_stride;
+    float *lse;
+    int32_t chunks;             // row chunks per request and KV head
+    int32_t S, span;
+    float *po;
+    float2 *ml;
+    int32_t *status;
+};
+
+// The tensor-core form (kvi_attn_tile.cu): two tiles of 128 rows a block.
+// Tokens that a tile holds, and the launch (p.chunks = tile pairs).
+inline int tile_tokens(int G) { return 128 / G; }
+cudaError_t launch_tiles(const PromptParams &p, int32_t R, cudaStream_t s);
+
+// A tensor map of bf16 boxes with the 128-byte swizzle (rank <= 5; pitches in
+// bytes of the dimensions past the first); out-of-range elements read as 0.
+cudaError_t tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *pitches,
+                            const uint32_t *box);
 
 // The checks of the attention calls' shared arguments (a message is recorded).
 kvi_status check_attention(const kvi_attention *a);

@@ -4,7 +4,8 @@
 // A KV head's query rows are its group's heads for every token, token first:
 // row = token * G + head, so the rows that read the same keys share a tile.
 //
-// rows_kernel takes 8 or 16 rows per block and any page size and head size.
+// Long prompts run on the tensor cores' tiles (kvi_attn_tile.cu).  rows_kernel
+// here is for few rows, and for any page size and head size: it takes 8 or 16 rows per block and any page size and head size.
 // Its products are S^T = K Q^T (16 keys x 8 rows) and O^T = V^T P^T, as with few
 // rows it is K and V that fill the matrix instruction's M.  Each warp streams
 // its own tiles of 16 keys (16-byte asynchronous copies into a ring of its own,
@@ -25,28 +26,6 @@ namespace {
 constexpr int kRowWarps = 4;
 constexpr int kRowStages = 3;
 constexpr int kPlanSms = 152;
-
-struct PromptParams {
-    const __nv_bfloat16 *q;
-    int64_t q_stride;
-    const int32_t *q_start;
-    int32_t total_q, max_q;
-    const int32_t *ctx_lens;
-    int32_t max_ctx, max_blocks;
-    const int32_t *block_tables;
-    int32_t num_blocks, B;
-    int32_t H, Hq, G, D;
-    const __nv_bfloat16 *pool;  // [2][num_blocks][B][H][D]
-    float scale;                // times log2 e
-    __nv_bfloat16 *out;
-    int64_t out_stride;
-    float *lse;
-    int32_t chunks;             // row chunks per request and KV head
-    int32_t S, span;
-    float *po;
-    float2 *ml;
-    int32_t *status;
-};
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
@@ -364,13 +343,28 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct PromptPlan {
+    bool tiles;  // the form of kvi_attn_tile.cu
     int dp, nt;
     int64_t chunks;
     int S, span;
     size_t ml, total;
 };
 
-PromptPlan prompt_plan(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
+// `splits` pieces of the keys are wanted, none below `least` keys
+void plan_split(PromptPlan &pl, const kvi_attention &a, int32_t total_q, int32_t max_ctx, int64_t splits, int least)
+{
+    int64_t span = (max_ctx + splits - 1) / splits;
+    span = std::max<int64_t>(least, (span + 127) / 128 * 128);
+    pl.span = (int)std::min<int64_t>(span, 1 << 30);
+    pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
+    if (pl.S > 1) {
+        const size_t n_rows = (size_t)total_q * a.q_heads;
+        pl.ml = up256(n_rows * pl.S * a.head_dim * 4);
+        pl.total = pl.ml + up256(n_rows * pl.S * 8);
+    }
+}
+
+PromptPlan plan_rows(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
 {
     PromptPlan pl{};
     const int G = a.q_heads / a.kv_heads;
@@ -380,17 +374,38 @@ PromptPlan prompt_plan(const kvi_attention &a, int32_t R, int32_t total_q, int32
     pl.chunks = std::max<int64_t>(1, (rows + 8 * pl.nt - 1) / (8 * pl.nt));
     // blocks for four on every SM, none below 256 keys (four tiles a warp)
     const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
-    const int64_t want = std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n);
-    int64_t span = (max_ctx + want - 1) / want;
-    span = std::max<int64_t>(256, (span + 63) / 64 * 64);
-    pl.span = (int)std::min<int64_t>(span, 1 << 30);
-    pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
-    if (pl.S > 1) {
-        const size_t n_rows = (size_t)total_q * a.q_heads;
-        pl.ml = up256(n_rows * pl.S * a.head_dim * 4);
-        pl.total = pl.ml + up256(n_rows * pl.S * 8);
-    }
+    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n), 256);
     return pl;
+}
+
+PromptPlan plan_tiles(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
+{
+    PromptPlan pl{};
+    pl.tiles = true;
+    const int per = 2 * tile_tokens(a.q_heads / a.kv_heads);
+    pl.chunks = std::max<int64_t>(1, ((int64_t)max_q + per - 1) / per);
+    // a block for every SM, none below 256 keys
+    const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
+    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 256);
+    return pl;
+}
+
+// The tensor-core tiles want 16-byte channels in boxes of 8 tokens and up to
+// 128 channels, and pay once a request has more rows than the other form
+// keeps in one or a few blocks.
+constexpr int kRowsMost = 64;
+bool tiles_fit(const kvi_attention &a, int32_t max_q, int32_t num_blocks, int32_t block_size)
+{
+    return a.head_dim <= 128 && block_size % 8 == 0 && num_blocks <= (1 << 29) &&
+           (int64_t)max_q * (a.q_heads / a.kv_heads) > kRowsMost;
+}
+
+// Workspace for whichever form the cache's pages decide on.
+size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
+{
+    size_t n = std::max<size_t>(256, plan_rows(a, R, total_q, max_q, max_ctx).total);
+    if (tiles_fit(a, max_q, 1, 8)) n = std::max(n, plan_tiles(a, R, total_q, max_q, max_ctx).total);
+    return n;
 }
 
 template <int DP, int NT>
@@ -428,7 +443,7 @@ extern "C" size_t kvi_attn_prompt_workspace_bytes(const kvi_attention *a, int32_
                                                   int32_t max_ctx)
 {
     if (check_attention(a) != KVI_OK || !sizes_ok(R, total_q, max_q, max_ctx)) return 0;
-    return std::max<size_t>(256, prompt_plan(*a, R, total_q, max_q, max_ctx).total);
+    return prompt_bytes(*a, R, total_q, max_q, max_ctx);
 }
 
 extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,
@@ -451,12 +466,14 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     if (reinterpret_cast<uintptr_t>(d_q) % 16 || reinterpret_cast<uintptr_t>(d_out) % 16 || q_row_stride % 8 ||
         out_row_stride % 8 || q_row_stride < wide || out_row_stride < wide)
         return arg_error("q and out rows must be 16-byte aligned, with strides of at least q_heads * head_dim elements");
-    const PromptPlan pl = prompt_plan(*a, R, total_q, max_q, max_ctx);
+    const PromptPlan pl = tiles_fit(*a, max_q, cache->num_blocks, cache->block_size)
+                              ? plan_tiles(*a, R, total_q, max_q, max_ctx)
+                              : plan_rows(*a, R, total_q, max_q, max_ctx);
+    const size_t need = prompt_bytes(*a, R, total_q, max_q, max_ctx);
     if (pl.chunks * pl.S * a->kv_heads > 0x7fffffff || (int64_t)max_q * (a->q_heads / a->kv_heads) > (1 << 30))
         return arg_error("max_q=%d is too large for this call", max_q);
-    if (!d_ws || ws_bytes < std::max<size_t>(256, pl.total) || reinterpret_cast<uintptr_t>(d_ws) % 256)
-        return arg_error("workspace of %zu bytes (256-byte aligned) needed, %zu given", std::max<size_t>(256, pl.total),
-                         ws_bytes);
+    if (!d_ws || ws_bytes < need || reinterpret_cast<uintptr_t>(d_ws) % 256)
+        return arg_error("workspace of %zu bytes (256-byte aligned) needed, %zu given", need, ws_bytes);
     uint8_t *ws = static_cast<uint8_t *>(d_ws);
     PromptParams p{};
     p.q = static_cast<const __nv_bfloat16 *>(d_q);
@@ -485,8 +502,9 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.po = reinterpret_cast<float *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
     p.status = d_status;
-    st = cuda_status(launch_rows(p, pl, R, stream), "kvi_attn_prompt");
-    if (st != KVI_OK || pl.S == 1 || max_q == 0) return st;
+    if (max_q == 0) return KVI_OK;  // no rows
+    st = cuda_status(pl.tiles ? launch_tiles(p, R, stream) : launch_rows(p, pl, R, stream), "kvi_attn_prompt");
+    if (st != KVI_OK || pl.S == 1) return st;
     JoinParams j{};
     j.po = p.po;
     j.ml = p.ml;

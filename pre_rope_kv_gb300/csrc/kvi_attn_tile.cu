@@ -1,0 +1,606 @@
+// kvi_attn_tile.cu -- causal attention of prompts on the 5th-generation tensor
+// cores: the form of kvi_attn_prompt for long prompts.
+//
+// A block takes two tiles of up to 128 query rows of one request and KV head
+// (row = token * G + head of the group, so that all heads that read the same
+// keys share them) and walks over tiles of 128 keys:
+//   S = Q K^T      tcgen05.mma, Q and K in shared memory, S in tensor memory
+//   P = 2^(S - m)  a thread per row reads its 128 scores, keeps the running
+//                  sum, and writes P in bf16 over S
+//   O += P V       tcgen05.mma, P from tensor memory, V in shared memory
+//                  as it lies in the cache (channels contiguous)
+// The two tiles alternate: while one tile's scores go through the softmax the
+// tensor cores work on the other's products.  One warp copies (one box of K or
+// V per lane: a piece of a cache page, 64 channels wide), one issues the
+// matrix instructions, four per tile do the softmax.
+//
+// The running reference m moves only when a score passes it by 2^kLazy (O is
+// rescaled in tensor memory then, which a row needs a few times in all).
+// It may move at once: the matrix instructions run in the order of their issue
+// and S of a tile is issued after the O of the tile before, so a tile's S
+// being there means that its O is at rest.
+//
+// Keys that only some rows see, or that lie past the end, are masked in S.
+// Their values must not reach the output either (0 * inf is NaN), so in the
+// few tiles that have such keys V is looked over in shared memory first: rows
+// past the end become zero, and an infinity or NaN is replaced by zero and
+// added, at the end, to the rows that see it.
+//
+// What bounds it: the matrix products (4 D flops per pair of row and key) for
+// long prompts; measured figures are at the launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "kvi_attn.cuh"
+#include "kvi_sync.cuh"
+
+namespace kvi {
+
+namespace {
+
+constexpr int kM = 128;           // rows of a tile, keys of a tile
+constexpr int kCopyWarp = 8, kMmaWarp = 9;  // after four softmax warps per tile; two warps idle
+constexpr int kTileThreads = 12 * 32;
+// Registers: the launch gives 168 a thread (65536 / 384); the third warpgroup
+// keeps 72 of them, so that the softmax's hold a row of scores: 2 * 216 + 72 =
+// 3 * 168.
+constexpr int kRegsSoft = 216, kRegsRest = 72;
+constexpr uint64_t kTileWaitNs = 1000000000ull;
+constexpr int kHalf = kM * 128;   // bytes of 128 rows of 64 channels
+
+template <int DP>
+struct TileSmem {
+    static constexpr int kHalves = DP / 64;
+    static constexpr int kTile = kHalves * kHalf;  // Q, K or V of 128 rows
+    static constexpr int kStages = DP == 128 ? 4 : 6;
+    static constexpr int kQ = 0, kRing = 2 * kTile, kTail = kRing + kStages * kTile;
+};
+
+template <int DP>
+struct TileTail {
+    uint64_t q_full;
+    uint64_t full[TileSmem<DP>::kStages], empty[TileSmem<DP>::kStages];
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t v_fixed;
+    uint64_t drained;
+    uint32_t tmem;
+    int32_t odd;            // `first` holds something
+    int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
+};
+
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Shared-memory descriptors, 128-byte swizzle: rows of 128 bytes in groups of
+// 8 (1024 bytes).  K-major (Q, K): the stride offset is the group's; MN-major
+// (V): 64 channels of 8 keys are a group, the next 64 channels lie `half` on.
+__device__ __forceinline__ uint64_t desc_k(uint32_t a)
+{
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+           ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t a)
+{
+    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(kHalf >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+// Instruction descriptor: D float32, A and B bf16, M = 128, N, B K- or MN-major
+__device__ __forceinline__ uint32_t bf16_idesc(int n, bool b_mn)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+           ((uint32_t)(kM >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+{
+    asm volatile(
+        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+// 32 columns of this warp's 32 lanes (no wait)
+__device__ __forceinline__ void tmem_load32(uint32_t a, float *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,"
+        "%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(a)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store32(uint32_t a, const float *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"f"(v[0]),
+        "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+        "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]), "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]),
+        "f"(v[20]), "f"(v[21]), "f"(v[22]), "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]),
+        "f"(v[29]), "f"(v[30]), "f"(v[31]), "r"(a)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t a, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(
+            v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(a)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ void box3(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void box4(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+// V of one tile before the products: thread `kr` of 128 looks over key kr's
+// row.  Values of keys that are not there become zero; an infinity or NaN too,
+// noted with its key for the rows that see it.
+template <int DP>
+__device__ __forceinline__ void fix_values(uint8_t *v, int kr, int key, int ctx, TileTail<DP> &tl)
+{
+#pragma unroll 4
+    for (int i = 0; i < DP / 8; ++i) {  // 16-byte chunks of 8 channels
+        uint4 *at = reinterpret_cast<uint4 *>(v + (i >> 3) * kHalf + kr * 128 + (((i & 7) ^ (kr & 7)) << 4));
+        if (key >= ctx) {
+            *at = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 x = *at;
+        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) any |= ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        if (any) {
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                if ((b & 0x7f80u) != 0x7f80u) continue;
+                atomicMin(&tl.first[b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2][8 * i + e], key);
+                w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+            }
+            tl.odd = 1;
+            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kTileThreads, 1)
+tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
+            const __grid_constant__ PromptParams p, int box_keys)
+{
+    using Sm = TileSmem<DP>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    TileTail<DP> &tl = *reinterpret_cast<TileTail<DP> *>(base + Sm::kTail);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // ---- the block's rows and keys (heaviest prompts' ends first)
+    const int split = blockIdx.x % p.S, h = (blockIdx.x / p.S) % p.H, pair = p.chunks - 1 - blockIdx.x / p.S / p.H;
+    const int r = blockIdx.y;
+    RequestSpan rq;
+    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
+        if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        return;
+    }
+    const int per = kM / p.G;         // tokens of a tile
+    const int tok0 = pair * 2 * per;  // the block's first token
+    if (tok0 >= rq.n_q) return;
+    const int pieces = max(1, (rq.ctx + p.span - 1) / p.span);
+    if (split >= pieces) return;
+    const bool whole = pieces == 1;
+    const int seen0 = rq.ctx - rq.n_q;  // last position that token 0 sees
+    const int from = split * p.span;    // a multiple of 128
+    // tiles of keys that each row tile walks over; token t sees up to seen0 + t
+    int n_tiles[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int t0 = tok0 + i * per, t1 = min(rq.n_q, t0 + per);
+        const int end = t0 < rq.n_q ? min(seen0 + t1, from + p.span) : 0;
+        n_tiles[i] = max(0, (end - from + kM - 1) / kM);
+    }
+    const int n = max(n_tiles[0], n_tiles[1]);
+    const int sure = seen0 + tok0 + 1;  // keys below it are seen by every row
+    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+
+    if (tid == 0) {
+        mbar_init(smem_u32(&tl.q_full), 1);
+        for (int s = 0; s < Sm::kStages; ++s) {
+            mbar_init(smem_u32(&tl.full[s]), 1);
+            mbar_init(smem_u32(&tl.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&tl.s_full[i]), 1);
+            mbar_init(smem_u32(&tl.p_full[i]), kM);
+            mbar_init(smem_u32(&tl.o_full[i]), 1);
+        }
+        mbar_init(smem_u32(&tl.v_fixed), kM);
+        mbar_init(smem_u32(&tl.drained), 1);
+        tl.odd = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tl.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    for (int i = tid; i < 3 * DP; i += kTileThreads) (&tl.first[0][0])[i] = INT32_MAX;
+    bool lost = false;  // a block of this range lies outside the pool
+    for (int b = from / p.B + tid; (int64_t)b * p.B < min(rq.ctx, from + n * kM); b += kTileThreads)
+        lost |= (uint32_t)table[b] >= (uint32_t)p.num_blocks;
+    fence_before();
+    lost = __syncthreads_or(lost);
+    fence_after();
+    if (lost && tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+    const uint32_t tmem = tl.tmem;
+    // tensor memory: S (and P) of the two tiles, then their O
+    constexpr int kColO = 2 * kM;
+
+    if (warp >= kCopyWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kCopyWarp) {
+        // ------------------------------------------------------------ copies
+        if (lane < 2 && n > 0) {
+            const int t0 = tok0 + lane * per;
+            const uint32_t bar = smem_u32(&tl.q_full);
+            // rows past the tile's tokens keep what the memory held: their scores
+            // are computed and not used
+            if (lane == 0)
+                mbar_expect_tx(bar, (n_tiles[1] > 0 ? 2 : 1) * Sm::kHalves * per * p.G * 128);
+            __syncwarp(3u);
+            if (lane == 0 || n_tiles[1] > 0)
+                for (int x = 0; x < Sm::kHalves; ++x)
+                    box3(smem_u32(base + Sm::kQ + lane * Sm::kTile + x * kHalf), &tm_q, 64 * x, h * p.G, rq.q0 + t0, bar);
+        }
+        __syncwarp();
+        const int boxes = kM / box_keys;
+        const int half = lane / boxes, box = lane % boxes;  // 32 lanes cover two halves of 16 boxes
+        int stage = 0;
+        uint32_t phase = 1;  // an unused stage is empty
+        bool ok = true;
+        int slots = 0;
+        for (int j = 0; j < n && ok; ++j) {
+            const int key = from + j * kM + box * box_keys;
+            int block = key < rq.ctx ? table[key / p.B] : -1;
+            // a piece past the end, or of a block that is not there, reads as
+            // zeros from past a page's last token
+            const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
+            const int y = there ? key % p.B : p.B;
+            if (!there) block = 0;
+            for (int plane = 0; plane < 2; ++plane) {
+                bool got = true;
+                if (lane == 0) got = mbar_wait(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
+                if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
+                    if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                    ok = false;
+                    break;
+                }
+                const uint32_t bar = smem_u32(&tl.full[stage]);
+                if (lane == 0) mbar_expect_tx(bar, Sm::kTile);
+                __syncwarp();
+                if (half < Sm::kHalves)
+                    box4(smem_u32(base + Sm::kRing + stage * Sm::kTile + half * kHalf + box * box_keys * 128), &tm_kv,
+                         64 * half, h, y, plane * p.num_blocks + block, bar);
+                ++slots;
+                if (++stage == Sm::kStages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        // no copy may still be writing when the block ends
+        if (!ok) {
+            if (lane < Sm::kStages && lane < slots) {
+                const int last = (slots - 1 - lane) / Sm::kStages;
+                (void)mbar_wait(smem_u32(&tl.full[lane]), (uint32_t)(last & 1), kTileWaitNs);
+            }
+            if (lane == 0 && n > 0) (void)mbar_wait(smem_u32(&tl.q_full), 0, kTileWaitNs);
+        }
+    } else if (warp == kMmaWarp) {
+        // -------------------------------------------------- matrix products
+        if (lane == 0 && n > 0) {
+            const uint32_t id_s = bf16_idesc(kM, false), id_o = bf16_idesc(DP, true);
+            bool ok = mbar_wait(smem_u32(&tl.q_full), 0, kTileWaitNs);
+            auto wait_slot = [&](int slot) {
+                return mbar_wait(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+            };
+            auto stage_at = [&](int slot) { return smem_u32(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile); };
+            auto free_slot = [&](int slot) { mma_commit(smem_u32(&tl.empty[slot % Sm::kStages])); };
+            auto scores = [&](int i, int j) {
+                const uint32_t a = smem_u32(base + Sm::kQ + i * Sm::kTile), b = stage_at(2 * j);
+#pragma unroll
+                for (int k = 0; k < DP / 16; ++k) {
+                    const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
+                    mma_ss(tmem + i * kM, desc_k(a + at), desc_k(b + at), id_s, k > 0);
+                }
+                mma_commit(smem_u32(&tl.s_full[i]));
+            };
+            auto values = [&](int i, int j) {
+                const uint32_t b = stage_at(2 * j + 1);
+#pragma unroll
+                for (int k = 0; k < kM / 16; ++k)
+                    mma_ts(tmem + kColO + i * DP, tmem + i * kM + 8 * k, desc_mn(b + k * 2048), id_o, j > 0 || k > 0);
+            };
+            uint32_t fixes = 0;
+            ok = ok && wait_slot(0);
+            if (ok) {
+                fence_after();
+                for (int i = 0; i < 2; ++i)
+                    if (n_tiles[i] > 0) scores(i, 0);
+                free_slot(0);
+            }
+            for (int j = 0; j < n && ok; ++j) {
+                ok = wait_slot(2 * j + 1);
+                if (ok && from + (j + 1) * kM > sure) ok = mbar_wait(smem_u32(&tl.v_fixed), fixes++ & 1u, kTileWaitNs);
+                for (int i = 0; i < 2 && ok; ++i) {
+                    if (j < n_tiles[i]) {
+                        ok = mbar_wait(smem_u32(&tl.p_full[i]), (uint32_t)(j & 1), kTileWaitNs);
+                        if (!ok) break;
+                        fence_after();
+                        values(i, j);
+                        if (j + 1 == n_tiles[i]) mma_commit(smem_u32(&tl.o_full[i]));
+                    }
+                    if (i == 1) free_slot(2 * j + 1);
+                    if (j + 1 < n_tiles[i]) {
+                        ok = wait_slot(2 * j + 2);
+                        if (!ok) break;
+                        fence_after();
+                        scores(i, j + 1);
+                    }
+                    if (i == 1 && j + 1 < n) free_slot(2 * j + 2);
+                }
+            }
+            if (!ok) record_status(p.status, KVI_ERR_TIMEOUT);
+            // whatever ended the loop, no product may still run when tensor
+            // memory is given back
+            mma_commit(smem_u32(&tl.drained));
+            if (!mbar_wait(smem_u32(&tl.drained), 0, kTileWaitNs)) record_status(p.status, KVI_ERR_TIMEOUT);
+        }
+        __syncwarp();
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
+        // ----------------------------------------------------------- softmax
+        const int i = warp >> 2, row = tid & (kM - 1);
+        const int my = n_tiles[i];
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // this warp's part of tensor memory
+        const uint32_t t_s = tmem + lanes + i * kM, t_o = tmem + lanes + kColO + i * DP;
+        const int token = tok0 + i * per + row / p.G;
+        const bool real = row < per * p.G && token < rq.n_q;
+        const int last = seen0 + token;
+        float m = neg_inf(), limit = real ? neg_inf() : __int_as_float(0x7f800000), ref = 0.f, sum = 0.f;
+        const float lazy = kLazy / p.scale;
+        bool ok = true;
+        for (int j = 0; j < my; ++j) {
+            const int key0 = from + j * kM;
+            const bool partly = key0 + kM > sure;
+            if (partly && i == (j < n_tiles[1] ? 1 : 0)) {
+                const int slot = 2 * j + 1;
+                ok = ok && mbar_wait(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+                if (ok) fix_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, row, key0 + row, rq.ctx, tl);
+                mbar_arrive(smem_u32(&tl.v_fixed));
+            }
+            ok = ok && mbar_wait(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                ok = false;
+                break;
+            }
+            fence_after();
+            float s[kM];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_load32(t_s + 32 * c, s + 32 * c);
+            tmem_wait_ld();
+            if (partly) {
+                const int vis = last + 1 - key0;
+#pragma unroll
+                for (int c = 0; c < kM; ++c) s[c] = c < vis ? s[c] : neg_inf();
+            }
+            if (lost) {
+                uint32_t gone[4] = {0, 0, 0, 0};
+                for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
+                    if ((uint32_t)table[(key0 + c) / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
+#pragma unroll
+                for (int c = 0; c < kM; ++c)
+                    if ((gone[c >> 5] >> (c & 31)) & 1u) s[c] = neg_inf();
+            }
+            float top = max3(s[0], s[1], s[2]), top2 = max3(s[3], s[4], s[5]);
+#pragma unroll
+            for (int c = 6; c < kM - 2; c += 4) {
+                top = max3(top, s[c], s[c + 1]);
+                top2 = max3(top2, s[c + 2], s[c + 3]);
+            }
+            top = fmaxf(max3(top, s[kM - 2], s[kM - 1]), top2);
+            const bool move = top > limit;
+            if (__any_sync(0xffffffffu, move)) {
+                const float f = move ? exp2_fast((m - top) * p.scale) : 1.f;
+                if (move) {
+                    m = top;
+                    limit = top + lazy;
+                    ref = top * p.scale;
+                    sum *= f;
+                }
+                if (j > 0) {
+#pragma unroll
+                    for (int c = 0; c < DP; c += 32) {
+                        float v[32];
+                        tmem_load32(t_o + c, v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] *= f;
+                        tmem_store32(t_o + c, v);
+                    }
+                }
+            }
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int c = 0; c < kM; c += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    const float p0 = exp2_fast(fmaf(s[c + e], p.scale, -ref));
+                    const float p1 = exp2_fast(fmaf(s[c + e + 1], p.scale, -ref));
+                    part[e & 2] += p0;
+                    part[(e & 2) + 1] += p1;
+                    w[e / 2] = pack_bf16(p0, p1);
+                }
+                tmem_store16(t_s + c / 2, w);
+            }
+            sum += (part[0] + part[1]) + (part[2] + part[3]);
+            tmem_wait_st();
+            fence_before();
+            mbar_arrive(smem_u32(&tl.p_full[i]));
+        }
+        // ---- the rows' results; both tiles' warps have looked over their values
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (my > 0 && ok) {
+            ok = mbar_wait(smem_u32(&tl.o_full[i]), 0, kTileWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                ok = false;
+            }
+            fence_after();
+        }
+        if (ok) {
+            const int head = h * p.G + row % p.G;
+            const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
+            const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
+            const bool odd = tl.odd != 0;
+#pragma unroll 1
+            for (int c = 0; c < DP; c += 32) {
+                __syncwarp();
+                float v[32];
+                if (my > 0) {
+                    tmem_load32(t_o + c, v);
+                    tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (!real || c >= p.D) continue;
+                if (odd) {
+                    const float inf = __int_as_float(0x7f800000);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (tl.first[0][c + e] <= last) v[e] += inf;
+                        if (tl.first[1][c + e] <= last) v[e] -= inf;
+                        if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                    }
+                }
+                if (whole) {
+                    __nv_bfloat16 *out = p.out + tok * p.out_stride + (int64_t)head * p.D + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        if (c + e < p.D)
+                            *reinterpret_cast<uint4 *>(out + e) =
+                                make_uint4(pack_bf16(v[e] * inv, v[e + 1] * inv), pack_bf16(v[e + 2] * inv, v[e + 3] * inv),
+                                           pack_bf16(v[e + 4] * inv, v[e + 5] * inv), pack_bf16(v[e + 6] * inv, v[e + 7] * inv));
+                } else {
+                    float *out = p.po + (at * p.S + split) * p.D + c;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        if (c + e < p.D) *reinterpret_cast<float4 *>(out + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+            if (real) {
+                const float M = m * p.scale;
+                if (!whole)
+                    p.ml[at * p.S + split] = make_float2(M, sum);
+                else if (p.lse)
+                    p.lse[at] = sum == 0.f ? neg_inf() : (M + log2f(sum)) * kLn2;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+}  // namespace
+
+template <int DP>
+static cudaError_t run_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
+{
+    CUtensorMap tq, tkv;
+    const uint32_t per = (uint32_t)tile_tokens(p.G);
+    const uint64_t qd[3] = {(uint64_t)p.D, (uint64_t)p.Hq, (uint64_t)p.total_q};
+    const uint64_t qp[2] = {(uint64_t)p.D * 2, (uint64_t)p.q_stride * 2};
+    const uint32_t qb[3] = {64, (uint32_t)p.G, per};
+    cudaError_t e = tensor_map_bf16(&tq, p.q, 3, qd, qp, qb);
+    if (e != cudaSuccess) return e;
+    // K and V pieces: channels, heads, tokens of a page, pages (K's, then V's)
+    int box = 8;
+    while (box < kM && p.B % (2 * box) == 0) box *= 2;
+    const uint64_t row = (uint64_t)p.H * p.D * 2;
+    const uint64_t kd[4] = {(uint64_t)p.D, (uint64_t)p.H, (uint64_t)p.B, 2 * (uint64_t)p.num_blocks};
+    const uint64_t kp[3] = {(uint64_t)p.D * 2, row, row * p.B};
+    const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
+    e = tensor_map_bf16(&tkv, p.pool, 4, kd, kp, kb);
+    if (e != cudaSuccess) return e;
+    constexpr int bytes = TileSmem<DP>::kTail + (int)sizeof(TileTail<DP>) + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory");
+    e = smem_opt_in(tile_kernel<DP>, bytes);
+    if (e != cudaSuccess) return e;
+    tile_kernel<DP><<<dim3((unsigned)(p.S * p.H * p.chunks), (unsigned)R), kTileThreads, bytes, s>>>(tq, tkv, p, box);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
+{
+    return p.D <= 64 ? run_tiles<64>(p, R, s) : run_tiles<128>(p, R, s);
+}
+
+}  // namespace kvi

@@ -43,6 +43,7 @@
 #include <mutex>
 #include <tuple>
 
+#include "kvi_attn.cuh"
 #include "kvi_internal.cuh"
 
 namespace kvi {
@@ -970,6 +971,26 @@ cudaError_t launch_coarse_split(CoarseParams p, const float *emb, int64_t n_fact
 }
 
 }  // namespace
+
+cudaError_t tensor_map_bf16(CUtensorMap *map, const void *ptr, int rank, const uint64_t *dims, const uint64_t *pitches,
+                            const uint32_t *box)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc;
+    const cudaError_t e = encoder(&enc);
+    if (e != cudaSuccess) return e;
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    cuuint64_t d[5], s[4];
+    cuuint32_t b[5];
+    for (int i = 0; i < rank; ++i) {
+        d[i] = dims[i];
+        b[i] = box[i];
+        if (i) s[i - 1] = pitches[i - 1];
+    }
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void *>(ptr), d, s, b,
+                           estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 int coarse_stages(int Rp, int mt)
 {
