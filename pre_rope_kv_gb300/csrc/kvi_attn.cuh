@@ -16,6 +16,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "kvi_internal.cuh"
 
@@ -105,6 +106,28 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 
 #ifdef __CUDACC__
 
+// Every kernel of these calls may begin while the previous kernel of the
+// stream drains, waits for it before it touches memory (pdl_wait), and lets
+// the next one begin (pdl_launch_dependents): what a launch costs is hidden
+// behind the work before it.
+template <typename P, typename... Args>
+inline cudaError_t launch_chained(void (*kernel)(P, Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+                                  const std::decay_t<P> &p, const std::decay_t<Args> &...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, args...);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -161,6 +184,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&v);
 }
 
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    const __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// The codes in nibbles 0 and 4 of w as two bf16 numbers (one and-or, one
+// subtraction of 136)
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w)
+{
+    uint32_t b;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
+    const uint32_t off = 0x43084308u;  // 136, 136
+    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&off));
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
 // (hi + lo) * s of two bf16 numbers each, lo no larger than hi's rounding: one
 // rounding of the product to bf16 (lo * s rounds far below it)
 __device__ __forceinline__ uint32_t scale_bf16x2(uint32_t hi, uint32_t lo, uint32_t s)
@@ -192,6 +234,73 @@ __device__ __forceinline__ bool request_span(int r, const int32_t *q_start, int 
     return o.q0 >= 0 && q1 >= o.q0 && q1 <= total_q && o.n_q <= max_q && o.ctx >= 0 && o.ctx <= max_ctx &&
            (int64_t)o.ctx <= (int64_t)max_blocks * block_size;
 }
+
+namespace {
+
+constexpr int kJoinWarps = 4;
+
+// Block x of request r: its warps' (query row, head) rows.
+__device__ __forceinline__ void join_rows(const JoinParams &p, int x, int r)
+{
+    const int lane = threadIdx.x & 31;
+    RequestSpan q;
+    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q)) return;
+    const int pieces = (q.ctx + p.span - 1) / p.span;
+    if (pieces <= 1) return;
+    const int64_t i = (int64_t)x * kJoinWarps + (threadIdx.x >> 5);
+    if (i >= (int64_t)q.n_q * p.q_heads) return;
+    const int64_t row = (int64_t)q.q0 * p.q_heads + i;
+    const float2 *ml = p.ml + row * p.S;
+    const float *po = p.po + row * p.S * p.D;
+    const int d0 = 4 * lane;
+    // eight pieces' outputs are asked for before the sums are known
+    constexpr int kAhead = 8;
+    float4 v[kAhead];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s)
+        if (s < pieces && d0 < p.D) v[s] = *reinterpret_cast<const float4 *>(po + (int64_t)s * p.D + d0);
+    const float2 mine = lane < pieces ? ml[lane] : make_float2(neg_inf(), 0.f);  // of piece `lane`
+    float M = mine.x;
+    for (int s = lane + 32; s < pieces; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float ref = M == neg_inf() ? 0.f : M;
+    const float f0 = exp2_fast(mine.x - ref);
+    float L = mine.y * f0;
+    for (int s = lane + 32; s < pieces; s += 32) L += ml[s].y * exp2_fast(ml[s].x - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    __nv_bfloat16 *out = p.out + (row / p.q_heads) * p.out_stride + (row % p.q_heads) * p.D;
+    for (int d = d0; d - d0 < p.D; d += 128) {
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int b = 0; b < pieces; b += kAhead) {
+            if (b > 0 || d > d0) {
+#pragma unroll
+                for (int s = 0; s < kAhead; ++s)
+                    if (b + s < pieces && d < p.D) v[s] = *reinterpret_cast<const float4 *>(po + (int64_t)(b + s) * p.D + d);
+            }
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s) {
+                float f = __shfl_sync(0xffffffffu, f0, (b + s) & 31);
+                if (b + s >= 32) f = b + s < pieces ? exp2_fast(ml[b + s].x - ref) : 0.f;
+                // a piece without a visible key adds nothing (its output may be anything)
+                if (b + s < pieces && d < p.D && f != 0.f) {
+                    acc.x = fmaf(f, v[s].x, acc.x);
+                    acc.y = fmaf(f, v[s].y, acc.y);
+                    acc.z = fmaf(f, v[s].z, acc.z);
+                    acc.w = fmaf(f, v[s].w, acc.w);
+                }
+            }
+        }
+        if (d < p.D)
+            *reinterpret_cast<uint2 *>(out + d) =
+                make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    }
+    if (p.lse && lane == 0) p.lse[row] = L == 0.f ? neg_inf() : (M + log2f(L)) * kLn2;
+}
+
+}  // namespace
 
 #endif  // __CUDACC__
 

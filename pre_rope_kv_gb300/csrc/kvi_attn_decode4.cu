@@ -109,18 +109,6 @@ __device__ __forceinline__ void load_halves(uint32_t (&w)[(N + 1) / 2], const ui
     }
 }
 
-// The codes in nibbles 0 and 4 of w as two bf16 numbers (one and-or, one
-// subtraction of 136)
-__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t w)
-{
-    uint32_t b;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(b) : "r"(w), "r"(0x000f000fu), "r"(0x43004300u));
-    const uint32_t off = 0x43084308u;  // 136, 136
-    const __nv_bfloat162 v = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&b),
-                                     *reinterpret_cast<const __nv_bfloat162 *>(&off));
-    return *reinterpret_cast<const uint32_t *>(&v);
-}
-
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -154,6 +142,8 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     const int split = blockIdx.x;
     const int h = blockIdx.y / p.chunks, c0 = (blockIdx.y % p.chunks) * 8 * NT;  // first head of the group
     const int r = blockIdx.z;
+    pdl_wait();
+    pdl_launch_dependents();
     RequestSpan rq;
     if (!request_span(r, nullptr, (int)gridDim.z, 1, p.ctx_lens, p.max_ctx, p.max_blocks, p.page.B, rq)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
@@ -486,47 +476,88 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
 // ------------------------------------------------------ accumulated weights
 
 struct WeightParams {
+    JoinParams join;
+    int32_t join_blocks;  // 0: every request has a single piece
+    int32_t key_blocks;   // per KV head
     const float *scores;
     int32_t score_stride;
-    const float2 *ml;
-    int32_t S, span;
-    int32_t H, Hq, G;
-    const int32_t *ctx_lens;
-    int32_t max_ctx, max_blocks, block_size;
+    int32_t H, G;
     float *w;
     int64_t stride;
 };
 
-constexpr int kWeightThreads = 256;
+constexpr int kKeysThread = 2;
+constexpr int kKeysBlock = kKeysThread * kJoinWarps * 32;
 
-// weights[r][h][p] += sum over the group's heads of 2^(s_p - M) / L
-__global__ void __launch_bounds__(kWeightThreads) weight_kernel(const WeightParams p)
+// After the attention, per request: blocks that join its pieces' outputs, and
+// blocks that add weights[r][h][p] += sum over the group's heads of
+// 2^(s_p - M) / L, from the scores that the attention left.
+__global__ void __launch_bounds__(kJoinWarps * 32) finish_kernel(const __grid_constant__ WeightParams p)
 {
     __shared__ float s_ref[KVI_MAX_ATTN_GROUP], s_inv[KVI_MAX_ATTN_GROUP];
     pdl_wait();
-    const int h = blockIdx.y, r = blockIdx.z, tid = threadIdx.x;
+    pdl_launch_dependents();
+    const JoinParams &jp = p.join;
+    const int r = blockIdx.y, tid = threadIdx.x;
+    if ((int)blockIdx.x < p.join_blocks) {
+        join_rows(jp, blockIdx.x, r);
+        return;
+    }
+    const int x = blockIdx.x - p.join_blocks, h = x / p.key_blocks;
     RequestSpan rq;
-    if (!request_span(r, nullptr, (int)gridDim.z, 1, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, rq)) return;
-    if ((int64_t)blockIdx.x * kWeightThreads >= rq.ctx) return;
-    const int pieces = (rq.ctx + p.span - 1) / p.span;
-    for (int g = tid; g < p.G; g += kWeightThreads) {
-        const float2 *ml = p.ml + ((int64_t)r * p.Hq + (int64_t)h * p.G + g) * p.S;
+    if (!request_span(r, nullptr, jp.total_q, 1, jp.ctx_lens, jp.max_ctx, jp.max_blocks, jp.block_size, rq)) return;
+    const int key0 = (x % p.key_blocks) * kKeysBlock;
+    if (key0 >= rq.ctx) return;
+    // the scores of two keys and up to eight heads are asked for before the sums
+    // that they are measured against
+    const float *sc = p.scores + ((int64_t)r * p.H + h) * jp.max_ctx * p.score_stride;
+    float *w = p.w + ((int64_t)r * p.H + h) * p.stride;
+    constexpr int kAhead = 4;
+    float2 ahead[kKeysThread][kAhead];
+    float old[kKeysThread];
+#pragma unroll
+    for (int e = 0; e < kKeysThread; ++e) {
+        const int key = key0 + e * kJoinWarps * 32 + tid;
+        if (key >= rq.ctx) continue;
+        old[e] = w[key];
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g)
+            if (2 * g < p.G) ahead[e][g] = *reinterpret_cast<const float2 *>(sc + (int64_t)key * p.score_stride + 2 * g);
+    }
+    const int pieces = (rq.ctx + jp.span - 1) / jp.span;
+    // a warp per head
+    for (int g = tid >> 5; g < p.G; g += kJoinWarps) {
+        const int lane = tid & 31;
+        const float2 *ml = jp.ml + ((int64_t)r * jp.q_heads + (int64_t)h * p.G + g) * jp.S;
         float M = neg_inf();
-        for (int s = 0; s < pieces; ++s) M = fmaxf(M, ml[s].x);
+        for (int s = lane; s < pieces; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float ref = M == neg_inf() ? 0.f : M;
         float L = 0.f;
-        for (int s = 0; s < pieces; ++s) L += ml[s].y * exp2_fast(ml[s].x - ref);
-        s_ref[g] = ref;
-        s_inv[g] = L == 0.f ? 0.f : 1.f / L;
+        for (int s = lane; s < pieces; s += 32) L += ml[s].y * exp2_fast(ml[s].x - ref);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) {
+            s_ref[g] = ref;
+            s_inv[g] = L == 0.f ? 0.f : 1.f / L;
+        }
     }
     __syncthreads();
-    const int key = blockIdx.x * kWeightThreads + tid;
-    if (key >= rq.ctx) return;
-    const float *s = p.scores + (((int64_t)r * p.H + h) * p.max_ctx + key) * p.score_stride;
-    float sum = 0.f;
-    for (int g = 0; g < p.G; ++g) sum += exp2_fast(s[g] - s_ref[g]) * s_inv[g];
-    float *w = p.w + ((int64_t)r * p.H + h) * p.stride + key;
-    *w += sum;
+#pragma unroll
+    for (int e = 0; e < kKeysThread; ++e) {
+        const int key = key0 + e * kJoinWarps * 32 + tid;
+        if (key >= rq.ctx) break;
+        const float *s = sc + (int64_t)key * p.score_stride;
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < kAhead; ++g) {
+            if (2 * g < p.G) sum += exp2_fast(ahead[e][g].x - s_ref[2 * g]) * s_inv[2 * g];
+            if (2 * g + 1 < p.G) sum += exp2_fast(ahead[e][g].y - s_ref[2 * g + 1]) * s_inv[2 * g + 1];
+        }
+        for (int g = 2 * kAhead; g < p.G; ++g) sum += exp2_fast(s[g] - s_ref[g]) * s_inv[g];
+        w[key] = old[e] + sum;
+    }
 }
 
 // -------------------------------------------------------------------- host
@@ -546,12 +577,12 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     // two blocks of 8 heads share each decoded tile where registers allow
     pl.nt = G > 8 && a.head_dim <= 128 ? 2 : 1;
     pl.chunks = (G + 8 * pl.nt - 1) / (8 * pl.nt);
-    // enough blocks for four on every SM, twice, but none below 256 keys (two pairs
+    // enough blocks for four on every SM, twice, but none below 128 keys (a pair
     // of tiles a warp)
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
     const int64_t want = std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
     int64_t span = (max_ctx + want - 1) / want;
-    span = std::max<int64_t>(256, (span + 127) / 128 * 128);
+    span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
     pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
     const size_t rq = (size_t)R * a.q_heads;
@@ -570,8 +601,8 @@ cudaError_t run4(const Decode4Params &p, int32_t R, cudaStream_t s)
         const cudaError_t e = smem_opt_in(decode4_kernel<NG, NT>, bytes);
         if (e != cudaSuccess) return e;
     }
-    decode4_kernel<NG, NT><<<dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R), kWarps4 * 32, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(decode4_kernel<NG, NT>, dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R),
+                          kWarps4 * 32, bytes, s, p);
 }
 
 cudaError_t launch_decode4(const Decode4Params &p, int nt, int32_t R, cudaStream_t s)
@@ -657,45 +688,33 @@ extern "C" kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const 
     p.status = d_status;
     st = cuda_status(launch_decode4(p, pl.nt, R, stream), "kvi_attn_decode4");
     if (st != KVI_OK) return st;
-    if (pl.S > 1) {
-        JoinParams j{};
-        j.po = p.po;
-        j.ml = p.ml;
-        j.S = pl.S;
-        j.span = pl.span;
-        j.R = R;
-        j.q_heads = a->q_heads;
-        j.D = a->head_dim;
-        j.total_q = R;
-        j.max_q = 1;
-        j.ctx_lens = d_ctx_lens;
-        j.max_ctx = max_ctx;
-        j.max_blocks = max_blocks;
-        j.block_size = cache->block_size;
-        j.out = p.out;
-        j.out_stride = out_row_stride;
-        st = cuda_status(launch_join(j, stream), "kvi_attn_decode4");
-        if (st != KVI_OK) return st;
-    }
-    if (d_weights && max_ctx > 0) {
-        WeightParams w{};
-        w.scores = p.scores;
-        w.score_stride = pl.score_stride;
-        w.ml = p.ml;
-        w.S = pl.S;
-        w.span = pl.span;
-        w.H = p.H;
-        w.Hq = p.Hq;
-        w.G = p.G;
-        w.ctx_lens = d_ctx_lens;
-        w.max_ctx = max_ctx;
-        w.max_blocks = max_blocks;
-        w.block_size = cache->block_size;
-        w.w = d_weights;
-        w.stride = weights_stride;
-        weight_kernel<<<dim3((unsigned)((max_ctx + kWeightThreads - 1) / kWeightThreads), (unsigned)p.H, (unsigned)R),
-                        kWeightThreads, 0, stream>>>(w);
-        st = cuda_status(cudaGetLastError(), "kvi_attn_decode4");
-    }
-    return st;
+    if (pl.S == 1 && (!d_weights || max_ctx == 0)) return st;
+    WeightParams w{};
+    JoinParams &j = w.join;
+    j.po = p.po;
+    j.ml = p.ml;
+    j.S = pl.S;
+    j.span = pl.span;
+    j.R = R;
+    j.q_heads = a->q_heads;
+    j.D = a->head_dim;
+    j.total_q = R;
+    j.max_q = 1;
+    j.ctx_lens = d_ctx_lens;
+    j.max_ctx = max_ctx;
+    j.max_blocks = max_blocks;
+    j.block_size = cache->block_size;
+    j.out = p.out;
+    j.out_stride = out_row_stride;
+    if (!d_weights) return cuda_status(launch_join(j, stream), "kvi_attn_decode4");
+    w.join_blocks = pl.S > 1 ? (a->q_heads + kJoinWarps - 1) / kJoinWarps : 0;
+    w.key_blocks = (max_ctx + kKeysBlock - 1) / kKeysBlock;
+    w.scores = p.scores;
+    w.score_stride = pl.score_stride;
+    w.H = p.H;
+    w.G = p.G;
+    w.w = d_weights;
+    w.stride = weights_stride;
+    const dim3 grid((unsigned)(w.join_blocks + (int64_t)w.key_blocks * w.H), (unsigned)R);
+    return cuda_status(launch_chained(finish_kernel, grid, kJoinWarps * 32, 0, stream, w), "kvi_attn_decode4");
 }

@@ -12,67 +12,23 @@ namespace kvi {
 
 namespace {
 
-constexpr int kJoinWarps = 4;
-
 // One warp per (query row, head): the pieces' (m, l) in one pass, then the
 // weighted sum of their outputs.  Rows of a request with a single piece were
 // written by the attention kernel itself.
-__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const JoinParams p)
+__global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const __grid_constant__ JoinParams p)
 {
     pdl_wait();
-    const int r = blockIdx.y, lane = threadIdx.x & 31;
-    RequestSpan q;
-    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q)) return;
-    const int pieces = (q.ctx + p.span - 1) / p.span;
-    if (pieces <= 1) return;
-    const int64_t i = (int64_t)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (i >= (int64_t)q.n_q * p.q_heads) return;
-    const int64_t row = (int64_t)q.q0 * p.q_heads + i;
-    const float2 *ml = p.ml + row * p.S;
-    float M = neg_inf();
-    for (int s = lane; s < pieces; s += 32) M = fmaxf(M, ml[s].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float ref = M == neg_inf() ? 0.f : M;
-    float L = 0.f;
-    for (int s = lane; s < pieces; s += 32) L += ml[s].y * exp2_fast(ml[s].x - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const float *po = p.po + row * p.S * p.D;
-    __nv_bfloat16 *out = p.out + (row / p.q_heads) * p.out_stride + (row % p.q_heads) * p.D;
-    for (int d = 2 * lane; d < p.D; d += 64) {
-        float2 acc = make_float2(0.f, 0.f);
-        for (int s = 0; s < pieces; ++s) {
-            const float f = exp2_fast(ml[s].x - ref);
-            const float2 v = *reinterpret_cast<const float2 *>(po + (int64_t)s * p.D + d);
-            if (f != 0.f) {  // a piece without a visible key adds nothing
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-            }
-        }
-        *reinterpret_cast<uint32_t *>(out + d) = pack_bf16(acc.x * inv, acc.y * inv);
-    }
-    if (p.lse && lane == 0) p.lse[row] = L == 0.f ? neg_inf() : (M + log2f(L)) * kLn2;
+    pdl_launch_dependents();
+    join_rows(p, blockIdx.x, blockIdx.y);
 }
 
 }  // namespace
 
 cudaError_t launch_join(const JoinParams &p, cudaStream_t s)
 {
-    cudaLaunchConfig_t cfg = {};
     const int64_t rows = (int64_t)p.max_q * p.q_heads;
-    cfg.gridDim = dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps), (unsigned)p.R);
-    cfg.blockDim = dim3(kJoinWarps * 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, join_kernel, p);
-    if (e != cudaSuccess) return e;
-    return cudaGetLastError();
+    return launch_chained(join_kernel, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps), (unsigned)p.R),
+                          kJoinWarps * 32, 0, s, p);
 }
 
 kvi_status arg_error(const char *fmt, ...)

@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
     const int r = blockIdx.y;
+    pdl_wait();
+    pdl_launch_dependents();
     RequestSpan rq;
     if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
@@ -384,9 +386,9 @@ PromptPlan plan_tiles(const kvi_attention &a, int32_t R, int32_t total_q, int32_
     pl.tiles = true;
     const int per = 2 * tile_tokens(a.q_heads / a.kv_heads);
     pl.chunks = std::max<int64_t>(1, ((int64_t)max_q + per - 1) / per);
-    // a block for every SM, none below 256 keys
+    // a block for every SM, none below a tile of keys
     const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
-    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 256);
+    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 128);
     return pl;
 }
 
@@ -414,8 +416,8 @@ cudaError_t run_rows(const PromptParams &p, int32_t R, cudaStream_t s)
     const int bytes = RowsSmem<DP, NT>::kBytes;
     const cudaError_t e = smem_opt_in(rows_kernel<DP, NT>, bytes);
     if (e != cudaSuccess) return e;
-    rows_kernel<DP, NT><<<dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes, s>>>(p);
-    return cudaGetLastError();
+    return launch_chained(rows_kernel<DP, NT>, dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes,
+                          s, p);
 }
 
 cudaError_t launch_rows(const PromptParams &p, const PromptPlan &pl, int32_t R, cudaStream_t s)

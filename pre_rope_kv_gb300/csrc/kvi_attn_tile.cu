@@ -228,6 +228,12 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // ---- the block's rows and keys (heaviest prompts' ends first)
     const int split = blockIdx.x % p.S, h = (blockIdx.x / p.S) % p.H, pair = p.chunks - 1 - blockIdx.x / p.S / p.H;
     const int r = blockIdx.y;
+    if (tid == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
+    }
+    pdl_wait();
+    pdl_launch_dependents();
     RequestSpan rq;
     if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
@@ -594,8 +600,8 @@ static cudaError_t run_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
     static_assert(bytes <= 227 * 1024, "shared memory");
     e = smem_opt_in(tile_kernel<DP>, bytes);
     if (e != cudaSuccess) return e;
-    tile_kernel<DP><<<dim3((unsigned)(p.S * p.H * p.chunks), (unsigned)R), kTileThreads, bytes, s>>>(tq, tkv, p, box);
-    return cudaGetLastError();
+    return launch_chained(tile_kernel<DP>, dim3((unsigned)(p.S * p.H * p.chunks), (unsigned)R), kTileThreads, bytes, s, tq,
+                          tkv, p, box);
 }
 
 cudaError_t launch_tiles(const PromptParams &p, int32_t R, cudaStream_t s)

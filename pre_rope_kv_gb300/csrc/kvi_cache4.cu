@@ -2,8 +2,8 @@
 // out (kvi_cache4_read) and the cut to a budget (kvi_cache4_evict).
 //
 // A row of one KV head is D / 32 groups of 32 channels: step = bf16(max |x| /
-// 7), code = x / step rounded to the nearest integer, ties to even.  Both
-// divisions are IEEE float32; step rounds once more, to bf16, because a
+// 7), code = x / step rounded to the nearest integer, ties to even.  The
+// first division is IEEE float32 and rounds once more, to bf16, because a
 // step of 16 bits per 32 codes is what makes the format 4.5 bits, and the
 // codes are taken against the rounded step, so that no error of it is left
 // in them.
@@ -21,9 +21,21 @@ namespace {
 
 // ------------------------------------------------------------ rows in and out
 //
-// A thread owns four neighbouring channels of one token and head: the four
-// nibbles of one 16-bit piece of both code layouts.  Eight neighbouring lanes
-// hold a group.
+// A thread owns eight neighbouring channels of one head of two rows, four
+// neighbouring lanes a group.  Two rows, because tokens 2 i and 2 i + 1 share
+// the words of V: where the two rows go to such a pair of slots, which is the
+// rule for rows of a prefix, every store is a whole word; any other two rows are
+// written piece by piece.
+//
+// Codes without a division.  x / step is wanted rounded to the nearest integer,
+// ties to even, and x and step have 8 significant bits each.  So |x / step| >=
+// 1/2 is either a half-integer exactly or at least 2^-10 from one: with x =
+// X 2^a, step = S 2^b (128 <= S < 256) and 2 X 2^a - h S 2^b != 0 for an odd h,
+// that difference is at least 2^(b - 1), and divided by 2 S 2^b at least 2^-10.
+// x * (1 / step) in float32 is off by less than 2^-20 here; rounded to
+// multiples of 2^-12 it is the half-integer again where the quotient is
+// one, and on the same side as the quotient everywhere else.  Steps too small
+// for their reciprocal take the division.
 
 struct RowParams {
     const __nv_bfloat16 *k_in, *v_in;
@@ -32,6 +44,8 @@ struct RowParams {
     const int64_t *slots;
     int64_t T, n_slots;
     int32_t H, D;
+    int32_t lanes;               // H * D / 8: threads of a pair of rows
+    int32_t pairs;               // pairs of rows per block (0: a pair takes several blocks)
     Page4 page;
     uint8_t *pool;
     int32_t *status;
@@ -57,99 +71,197 @@ __device__ __forceinline__ int64_t v_step_at(const Page4 &pg, int off, int g)
     return pg.v_steps() + (((int64_t)(off >> 1) * pg.groups() + g) * 2 + (off & 1)) * 2;
 }
 
-// Step and four codes of this lane's channels; the eight lanes of a group
-// agree on the step.
-__device__ __forceinline__ void quantise4(uint2 raw, uint16_t &step, uint16_t &codes)
+// Step and eight codes (channel n in nibble n) of this lane's channels; the
+// four lanes of a group agree on the step.
+__device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t &step)
 {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     // |x| as bf16 bits: their order is that of the values, infinities and
     // NaN at the top
-    uint32_t top = max(max(raw.x & 0x7fffu, (raw.x >> 16) & 0x7fffu), max(raw.y & 0x7fffu, (raw.y >> 16) & 0x7fffu));
+    uint32_t top = 0;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (top >= 0x7f80u) {  // not finite: the whole group reads back as NaN
         step = 0x7fff;
-        codes = 0x8888;
-        return;
+        return 0x88888888u;
     }
     const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.0f));
     step = __bfloat16_as_ushort(sb);
     const float sf = __bfloat162float(sb);
-    const float x[4] = {bf16_lo(raw.x), bf16_hi(raw.x), bf16_lo(raw.y), bf16_hi(raw.y)};
     uint32_t c = 0;
+    if (sf >= 1.1754944e-38f) {  // 1 / step is finite; |x / step| < 7.03
+        const float inv = __frcp_rn(sf);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        // sf == 0: 0 / 0 or x / 0 where x is too small for any bf16 step
-        float q = sf > 0.f ? rintf(__fdiv_rn(x[j], sf)) : 0.f;
-        // the step rounds down by at most 2^-9 of itself (less exactly for
-        // subnormal steps), so only there a quotient can pass 7
-        q = fminf(fmaxf(q, -7.f), 7.f);
-        c |= (uint32_t)((int)q + 8) << (4 * j);
+        for (int n = 7; n >= 0; --n) {
+            const float x = n & 1 ? bf16_hi(w[n >> 1]) : bf16_lo(w[n >> 1]);
+            const float q = __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 3072.f), -3072.f);  // multiples of 2^-12
+            // the integer in the low bits, plus 8
+            c = (c << 4) | (__float_as_uint(__fadd_rn(q, 12582920.f)) & 15u);
+        }
+    } else {
+#pragma unroll 1
+        for (int n = 7; n >= 0; --n) {
+            const float x = __uint_as_float((w[n >> 1] >> (16 * (n & 1))) << 16);
+            // a subnormal step can be well below max / 7
+            const float q = sf > 0.f ? fminf(fmaxf(rintf(__fdiv_rn(x, sf)), -7.f), 7.f) : 0.f;
+            c = (c << 4) | (uint32_t)((int)q + 8);
+        }
     }
-    codes = (uint16_t)c;
+    return c;
 }
 
-__global__ void __launch_bounds__(kRowThreads) cache4_write_kernel(const RowParams p)
+// step * code: eight channels from the codes in nibbles 0..7, as the four
+// words of a row.  The product has one rounding, to bf16.
+__device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t step)
 {
-    const int quads = p.D / 4;
-    const int64_t per_row = (int64_t)p.H * quads;  // a multiple of 8: a group never leaves its warp
-    const int64_t n = p.T * per_row;
-    const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-    const bool in = i < n;
-    const int64_t t = in ? i / per_row : 0;
-    const int rest = (int)(in ? i % per_row : 0);
-    const int h = rest / quads, q = rest % quads;
-    const int64_t slot = in ? p.slots[t] : -1;
-    const bool live = slot >= 0 && slot < p.n_slots;
-    if (slot >= p.n_slots && rest == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-    uint2 kr = make_uint2(0, 0), vr = make_uint2(0, 0);
-    if (live) {
-        kr = *reinterpret_cast<const uint2 *>(p.k_in + t * p.k_stride + (int64_t)h * p.D + 4 * q);
-        vr = *reinterpret_cast<const uint2 *>(p.v_in + t * p.v_stride + (int64_t)h * p.D + 4 * q);
-    }
-    uint16_t ks, kc, vs, vc;
-    quantise4(kr, ks, kc);
-    quantise4(vr, vs, vc);
-    if (!live) return;
-    const int off = (int)(slot % p.page.B), g = q >> 3, s = q & 7;
-    uint8_t *page = p.pool + ((slot / p.page.B) * p.H + h) * p.page.bytes();
-    *reinterpret_cast<uint16_t *>(page + k_piece(p.page, off, g, s)) = kc;
-    *reinterpret_cast<uint16_t *>(page + v_piece(p.page, off, g, s)) = vc;
-    if (s == 0) {
-        *reinterpret_cast<uint16_t *>(page + k_step_at(p.page, off, g)) = ks;
-        *reinterpret_cast<uint16_t *>(page + v_step_at(p.page, off, g)) = vs;
-    }
-}
-
-// step * code: exact in float32 (8 by 4 bits), rounded once to bf16
-__device__ __forceinline__ uint2 values4(uint16_t step, uint32_t codes)
-{
-    const float s = __uint_as_float((uint32_t)step << 16);
-    float x[4];
+    const uint32_t s2 = step | (step << 16);
+    uint32_t v[4];  // (j, j + 4)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = s * (float)((int)((codes >> (4 * j)) & 15u) - 8);
-    return make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
+    for (int j = 0; j < 4; ++j) v[j] = mul_bf16x2(codes_bf16x2(codes >> (4 * j)), s2);
+    return make_uint4(__byte_perm(v[0], v[1], 0x5410), __byte_perm(v[2], v[3], 0x5410), __byte_perm(v[0], v[1], 0x7632),
+                      __byte_perm(v[2], v[3], 0x7632));
 }
 
-__global__ void __launch_bounds__(kRowThreads) cache4_read_kernel(const RowParams p)
+// This thread's pair of rows and channels: rows 2 i - odd and + 1, where odd is
+// the first slot's parity, so that runs of consecutive slots pair up.
+struct RowWork {
+    int64_t row;       // the first row (it or the second may lie outside [0, T))
+    int32_t h, g, t;   // head, group, 8-channel part of the group
+    int64_t slot[2];   // -1: nothing to do
+    int64_t page[2];
+    int32_t off[2];
+    bool pair;         // slots 2 n and 2 n + 1 of one page
+};
+
+__device__ __forceinline__ bool row_work(const RowParams &p, RowWork &o)
 {
-    const int quads = p.D / 4;
-    const int64_t per_row = (int64_t)p.H * quads;
-    const int64_t i = (int64_t)blockIdx.x * kRowThreads + threadIdx.x;
-    if (i >= p.T * per_row) return;
-    const int64_t t = i / per_row;
-    const int rest = (int)(i % per_row);
-    const int h = rest / quads, q = rest % quads;
-    const int64_t slot = p.slots[t];
-    if (slot >= p.n_slots && rest == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-    if (slot < 0 || slot >= p.n_slots) return;
-    const int off = (int)(slot % p.page.B), g = q >> 3, s = q & 7;
-    const uint8_t *page = p.pool + ((slot / p.page.B) * p.H + h) * p.page.bytes();
-    const uint2 k = values4(*reinterpret_cast<const uint16_t *>(page + k_step_at(p.page, off, g)),
-                            *reinterpret_cast<const uint16_t *>(page + k_piece(p.page, off, g, s)));
-    const uint2 v = values4(*reinterpret_cast<const uint16_t *>(page + v_step_at(p.page, off, g)),
-                            *reinterpret_cast<const uint16_t *>(page + v_piece(p.page, off, g, s)));
-    *reinterpret_cast<uint2 *>(p.k_out + t * p.k_stride + (int64_t)h * p.D + 4 * q) = k;
-    *reinterpret_cast<uint2 *>(p.v_out + t * p.v_stride + (int64_t)h * p.D + 4 * q) = v;
+    const int tid = threadIdx.x;
+    int64_t i;
+    int lane;
+    if (p.pairs) {
+        const int at = tid / p.lanes;
+        lane = tid - at * p.lanes;
+        i = (int64_t)blockIdx.x * p.pairs + at;
+        if (at >= p.pairs) i = -1;
+    } else {
+        lane = blockIdx.y * kRowThreads + tid;
+        i = lane < p.lanes ? (int64_t)blockIdx.x : -1;
+    }
+    const int parts = p.D / 8;
+    o.h = lane / parts;
+    const int part = lane - o.h * parts;
+    o.g = part >> 2;
+    o.t = part & 3;
+    o.row = 2 * i - (p.slots[0] & 1);
+    o.slot[0] = o.slot[1] = -1;
+    if (i >= 0) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t r = o.row + e;
+            if (r < 0 || r >= p.T) continue;
+            const int64_t s = p.slots[r];
+            if (s >= p.n_slots) {
+                if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+            } else if (s >= 0) {
+                o.slot[e] = s;
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int64_t s = max((int64_t)0, o.slot[e]);
+        if (p.n_slots <= 0x7fffffff) {
+            o.page[e] = (int32_t)s / p.page.B;
+            o.off[e] = (int32_t)s % p.page.B;
+        } else {
+            o.page[e] = s / p.page.B;
+            o.off[e] = (int32_t)(s % p.page.B);
+        }
+    }
+    o.pair = o.slot[0] >= 0 && !(o.slot[0] & 1) && o.slot[1] == o.slot[0] + 1;  // (B is even: one page)
+    return o.slot[0] >= 0 || o.slot[1] >= 0;
+}
+
+__global__ void __launch_bounds__(kRowThreads) cache4_write_kernel(const __grid_constant__ RowParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    RowWork o;
+    row_work(p, o);
+    const int64_t col = (int64_t)o.h * p.D + 32 * o.g + 8 * o.t;
+    uint4 k[2], v[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        k[e] = v[e] = make_uint4(0, 0, 0, 0);
+        if (o.slot[e] >= 0) {
+            k[e] = *reinterpret_cast<const uint4 *>(p.k_in + (o.row + e) * p.k_stride + col);
+            v[e] = *reinterpret_cast<const uint4 *>(p.v_in + (o.row + e) * p.v_stride + col);
+        }
+    }
+    uint32_t ks[2], kc[2], vs[2], vc[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        kc[e] = quantise8(k[e], ks[e]);
+        vc[e] = quantise8(v[e], vs[e]);
+    }
+    const int64_t bytes = p.page.bytes();
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (o.slot[e] < 0) continue;
+        uint8_t *page = p.pool + (o.page[e] * p.H + o.h) * bytes;
+        *reinterpret_cast<uint32_t *>(page + k_piece(p.page, o.off[e], o.g, 2 * o.t)) = kc[e];
+        if (o.t == 0) *reinterpret_cast<uint16_t *>(page + k_step_at(p.page, o.off[e], o.g)) = (uint16_t)ks[e];
+        if (o.pair) continue;
+        *reinterpret_cast<uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t)) = (uint16_t)vc[e];
+        *reinterpret_cast<uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t + 1)) = (uint16_t)(vc[e] >> 16);
+        if (o.t == 0) *reinterpret_cast<uint16_t *>(page + v_step_at(p.page, o.off[e], o.g)) = (uint16_t)vs[e];
+    }
+    if (o.pair) {
+        uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
+        *reinterpret_cast<uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t)) = __byte_perm(vc[0], vc[1], 0x5410);
+        *reinterpret_cast<uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t + 1)) = __byte_perm(vc[0], vc[1], 0x7632);
+        if (o.t == 0) *reinterpret_cast<uint32_t *>(page + v_step_at(p.page, o.off[0], o.g)) = vs[0] | (vs[1] << 16);
+    }
+}
+
+__global__ void __launch_bounds__(kRowThreads) cache4_read_kernel(const __grid_constant__ RowParams p)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    RowWork o;
+    if (!row_work(p, o)) return;
+    const int64_t col = (int64_t)o.h * p.D + 32 * o.g + 8 * o.t, bytes = p.page.bytes();
+    uint32_t kc[2], ks[2], vc[2], vs[2];
+    if (o.pair) {
+        const uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
+        const uint32_t a = *reinterpret_cast<const uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t));
+        const uint32_t b = *reinterpret_cast<const uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t + 1));
+        const uint32_t s = *reinterpret_cast<const uint32_t *>(page + v_step_at(p.page, o.off[0], o.g));
+        vc[0] = __byte_perm(a, b, 0x5410);
+        vc[1] = __byte_perm(a, b, 0x7632);
+        vs[0] = s & 0xffffu;
+        vs[1] = s >> 16;
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (o.slot[e] < 0) continue;
+        const uint8_t *page = p.pool + (o.page[e] * p.H + o.h) * bytes;
+        kc[e] = *reinterpret_cast<const uint32_t *>(page + k_piece(p.page, o.off[e], o.g, 2 * o.t));
+        ks[e] = *reinterpret_cast<const uint16_t *>(page + k_step_at(p.page, o.off[e], o.g));
+        if (!o.pair) {
+            vc[e] = *reinterpret_cast<const uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t)) |
+                    (uint32_t)*reinterpret_cast<const uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t + 1)) << 16;
+            vs[e] = *reinterpret_cast<const uint16_t *>(page + v_step_at(p.page, o.off[e], o.g));
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        if (o.slot[e] < 0) continue;
+        *reinterpret_cast<uint4 *>(p.k_out + (o.row + e) * p.k_stride + col) = values8(kc[e], ks[e]);
+        *reinterpret_cast<uint4 *>(p.v_out + (o.row + e) * p.v_stride + col) = values8(vc[e], vs[e]);
+    }
 }
 
 // ----------------------------------------------------------------- eviction
@@ -181,10 +293,9 @@ struct EvictParams {
     int32_t *status;
 };
 
-constexpr int kEvictThreads = 1024;
 constexpr int kMoveThreads = 256;
-constexpr int kBins = 2048;           // two per thread
-constexpr int kRankCap = 24 * 1024;   // ranks kept in shared memory (two blocks fit an SM)
+constexpr int kBins = 2048;
+constexpr int kRankCap = 24 * 1024;   // ranks kept in shared memory
 
 // Rank order of a slot as an unsigned number: protected slots first, then
 // by weight (-0 as 0, NaN above infinity).
@@ -208,49 +319,44 @@ __device__ __forceinline__ int block_sum_before(int v, int *warp_sums)
     }
     if (lane == 31) warp_sums[warp] = sum;
     __syncthreads();
-    int before = lane < warp ? warp_sums[lane] : 0;
+    int before = lane < warp ? warp_sums[lane] : 0;  // warp < 32
     before = __reduce_add_sync(0xffffffffu, before);
     return before + sum - v;
 }
 
-// Exclusive prefix sum over the block of a 0/1 flag; `total` for everybody.
-__device__ __forceinline__ int block_rank(bool flag, int *warp_sums, int &total)
+// Sum of a warp's v over the warps before this one.
+__device__ __forceinline__ int warp_sum_before(int v, int *warp_sums)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t votes = __ballot_sync(0xffffffffu, flag);
     __syncthreads();  // the last call's sums have been read
-    if (lane == 0) warp_sums[warp] = __popc(votes);
+    if (lane == 0) warp_sums[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        const int v = warp_sums[lane];
-        int sum = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += u;
-        }
-        warp_sums[lane] = sum - v;
-        if (lane == 31) warp_sums[32] = sum;
-    }
-    __syncthreads();
-    total = warp_sums[32];
-    return warp_sums[warp] + __popc(votes & ((1u << lane) - 1u));
+    return __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const EvictParams p)
+// ITEMS > 0: a row of at most THREADS * ITEMS slots, each read once and kept in
+// registers; 0: a longer one, its ranks in shared memory (the first p.cap) and
+// recomputed past them.  A warp's slots are a run of consecutive ones either way.
+template <int THREADS, int ITEMS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_constant__ EvictParams p)
 {
-    extern __shared__ uint32_t s_rank[];  // of the first p.cap slots
-    __shared__ int s_warp[33];
+    extern __shared__ uint32_t s_rank[];
+    __shared__ int s_warp[32];
     __shared__ int s_hist[kBins];
     __shared__ int s_newest, s_digit, s_left;
-    const int h = blockIdx.x % p.H, r = blockIdx.x / p.H, tid = threadIdx.x;
+    constexpr int kKept = ITEMS > 0 ? ITEMS : 1;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int h = blockIdx.x % p.H, r = blockIdx.x / p.H;
     const int64_t row = (int64_t)blockIdx.x;
     const float *w = p.w + row * p.stride;
     const int32_t *pos = p.pos + row * p.stride;
     float *w_out = p.w_out + row * p.stride;
     int32_t *pos_out = p.pos_out + row * p.stride;
-    const int n = p.ctx_lens[r];
+    if (tid == 0) s_newest = INT32_MIN;
+    for (int i = tid; i < kBins; i += THREADS) s_hist[i] = 0;
+    pdl_wait();
     pdl_launch_dependents();
+    const int n = p.ctx_lens[r];
     if (n < 0 || n > p.max_ctx || (int64_t)n > (int64_t)p.max_blocks * p.page.B) {
         if (tid == 0) {
             record_status(p.status, KVI_ERR_OUT_OF_RANGE);
@@ -261,23 +367,58 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     const int left = min(n, p.budget);
     if (h == 0 && tid == 0) p.ctx_out[r] = left;
     if (n <= p.budget) {
-        for (int i = tid; i < n; i += kEvictThreads) {
+        for (int i = tid; i < n; i += THREADS) {
             w_out[i] = w[i];
             pos_out[i] = pos[i];
         }
         if (tid == 0) p.moves[row] = 0;
         return;
     }
-    if (tid == 0) s_newest = INT32_MIN;
-    for (int i = tid; i < kBins; i += kEvictThreads) s_hist[i] = 0;
-    __syncthreads();
+    const int run = ITEMS > 0 ? ITEMS * 32 : ((n + THREADS - 1) / THREADS) * 32;
+    const int i0 = warp * run, i1 = min(n, i0 + run);
+    float kw[kKept];
+    int kp[kKept];
+    uint32_t kr[kKept];
     int newest = INT32_MIN;
-    for (int i = tid; i < n; i += kEvictThreads) newest = max(newest, pos[i]);
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) {
+            const int i = i0 + 32 * e + lane;
+            kw[e] = i < i1 ? w[i] : 0.f;
+            kp[e] = i < i1 ? pos[i] : INT32_MIN;
+        }
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) newest = max(newest, kp[e]);
+    } else {
+#pragma unroll 8
+        for (int i = i0 + lane; i < i1; i += 32) newest = max(newest, pos[i]);
+    }
     newest = __reduce_max_sync(0xffffffffu, newest);
-    if ((tid & 31) == 0) atomicMax(&s_newest, newest);
+    __syncthreads();
+    if (lane == 0) atomicMax(&s_newest, newest);
     __syncthreads();
     const int64_t from = (int64_t)s_newest - p.recent + 1;
-    auto rank_of = [&](int i) { return i < p.cap ? s_rank[i] : evict_rank(w[i], pos[i], p.sink, from); };
+    if constexpr (ITEMS > 0) {
+#pragma unroll
+        for (int e = 0; e < ITEMS; ++e) kr[e] = evict_rank(kw[e], kp[e], p.sink, from);
+    } else {
+#pragma unroll 4
+        for (int i = i0 + lane; i < i1; i += 32)
+            if (i < p.cap) s_rank[i] = evict_rank(w[i], pos[i], p.sink, from);
+        __syncwarp();
+    }
+    // f(slot, rank) for each of the warp's slots, 32 at a time and in order
+    auto each = [&](auto &&f) {
+        if constexpr (ITEMS > 0) {
+#pragma unroll
+            for (int e = 0; e < ITEMS; ++e) f(e, i0 + 32 * e + lane, kr[e]);
+        } else {
+            for (int i = i0; i < i1; i += 32) {
+                const int at = i + lane;
+                f(0, at, at >= i1 ? 0u : at < p.cap ? s_rank[at] : evict_rank(w[at], pos[at], p.sink, from));
+            }
+        }
+    };
 
     // the budget-th largest rank, 11, 11 and 10 bits at a time from the top
     uint32_t found = 0;
@@ -286,103 +427,138 @@ __global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(const Evict
     for (int pass = 0; pass < 3; ++pass) {
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        for (int i = tid; i < n; i += kEvictThreads) {
-            uint32_t k;
-            if (pass == 0) {
-                k = evict_rank(w[i], pos[i], p.sink, from);
-                if (i < p.cap) s_rank[i] = k;
-            } else {
-                k = rank_of(i);
-                if ((k ^ found) >> (pass == 1 ? 21 : 10)) continue;
-            }
-            atomicAdd(&s_hist[(k >> shift) & mask], 1);
-        }
+        each([&](int, int i, uint32_t k) {
+            if (i < i1 && (pass == 0 || (k ^ found) >> (pass == 1 ? 21 : 10) == 0)) atomicAdd(&s_hist[(k >> shift) & mask], 1);
+        });
         __syncthreads();
-        // from the top bin down, two bins a thread: the one where the count
+        // from the top bin down, a few bins a thread: the one where the count
         // passes `want`
-        const int hi = kBins - 1 - 2 * tid;
-        const int a = s_hist[hi], b = s_hist[hi - 1];
-        s_hist[hi] = s_hist[hi - 1] = 0;
-        const int above = block_sum_before(a + b, s_warp);
-        if (above < want && above + a + b >= want) {
-            s_digit = above + a >= want ? hi : hi - 1;
-            s_left = want - above - (above + a >= want ? 0 : a);
+        constexpr int kOwn = kBins / THREADS;
+        const int hi = kBins - 1 - kOwn * tid;
+        int count[kOwn], all = 0;
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) {
+            count[e] = s_hist[hi - e];
+            s_hist[hi - e] = 0;
+            all += count[e];
+        }
+        int above = block_sum_before(all, s_warp);
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) {
+            if (above < want && above + count[e] >= want) {
+                s_digit = hi - e;
+                s_left = want - above;
+            }
+            above += count[e];
         }
         __syncthreads();
         found |= (uint32_t)s_digit << shift;
         want = s_left;
     }
-    // ranks above `found` stay, and the first `want` slots that equal it
-    int ties = 0, n_holes = 0, n_tails = 0;
+    // ranks above `found` stay, and the first `want` slots that equal it; each
+    // warp counts its run, and then knows its places in the lists
+    const uint32_t below = (1u << lane) - 1u;
     int32_t *holes = p.holes + row * p.most, *tails = p.tails + row * p.most;
-    for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
-        const int i = i0 + tid;
-        const bool in = i < n;
-        const uint32_t k = in ? rank_of(i) : 0u;
-        const bool tie = in && k == found;
-        int c;
-        const int rank = ties + block_rank(tie, s_warp, c);
-        ties += c;
-        const bool keep = in && (k > found || (tie && rank < want));
-        const bool hole = in && i < left && !keep, tail = keep && i >= left;
-        // a block's slots lie below the budget, above it, or (once) across it
-        if (i0 < left) {
-            const int at = n_holes + block_rank(hole, s_warp, c);
-            n_holes += c;
-            if (hole) holes[at] = i;
-        }
-        if (i0 + kEvictThreads > left) {
-            const int at = n_tails + block_rank(tail, s_warp, c);
-            n_tails += c;
-            if (tail) tails[at] = i;
-        }
-        if (in && !hole) {
-            w_out[i] = i < left ? w[i] : 0.f;
-            pos_out[i] = i < left ? pos[i] : -1;
+    int ties = 0;
+    each([&](int, int i, uint32_t k) { ties += __popc(__ballot_sync(0xffffffffu, i < i1 && k == found)); });
+    const int ties0 = warp_sum_before(ties, s_warp);
+    int hole_at = 0, tail_at = 0;
+#pragma unroll
+    for (int pass = 0; pass < 2; ++pass) {
+        int tie_at = ties0;
+        each([&](int e, int i, uint32_t k) {
+            const bool in = i < i1;
+            const uint32_t tie = __ballot_sync(0xffffffffu, in && k == found);
+            const bool keep = in && (k > found || (k == found && tie_at + __popc(tie & below) < want));
+            tie_at += __popc(tie);
+            const bool hole = in && i < left && !keep, tail = keep && i >= left;
+            const uint32_t hs = __ballot_sync(0xffffffffu, hole), ts = __ballot_sync(0xffffffffu, tail);
+            if (pass == 1) {
+                if (hole) holes[hole_at + __popc(hs & below)] = i;
+                if (tail) tails[tail_at + __popc(ts & below)] = i;
+                if (in && !hole) {
+                    w_out[i] = i >= left ? 0.f : ITEMS > 0 ? kw[e] : w[i];
+                    pos_out[i] = i >= left ? -1 : ITEMS > 0 ? kp[e] : pos[i];
+                }
+            }
+            hole_at += __popc(hs);
+            tail_at += __popc(ts);
+        });
+        if (pass == 0) {
+            hole_at = warp_sum_before(hole_at, s_warp);
+            tail_at = warp_sum_before(tail_at, s_warp);
+        } else if (tid == THREADS - 1) {
+            s_left = hole_at;  // all of them
         }
     }
     __syncthreads();
-    for (int i = tid; i < n_holes; i += kEvictThreads) {
-        w_out[holes[i]] = w[tails[i]];
-        pos_out[holes[i]] = pos[tails[i]];
+    const int n_holes = s_left;
+#pragma unroll 2
+    for (int i = tid; i < n_holes; i += THREADS) {
+        const int to = holes[i], at = tails[i];
+        w_out[to] = w[at];
+        pos_out[to] = pos[at];
     }
     if (tid == 0) p.moves[row] = n_holes;
 }
 
-// One warp per moved row: 16-bit pieces, as two tokens share each word of
-// the V codes and steps.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p)
+// Eight lanes per moved row, so that enough rows are in flight to hide a
+// chain of three latencies (list, table, page); 16-bit pieces, as two tokens
+// share each word of the V codes and steps.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p)
 {
     pdl_wait();
+    pdl_launch_dependents();
     const int64_t row = blockIdx.y;
-    const int h = (int)(row % p.H), r = (int)(row / p.H), lane = threadIdx.x & 31;
-    const int n = p.moves[row];
+    const int h = (int)(row % p.H), r = (int)(row / p.H), lane = threadIdx.x & 7;
+    const int i = blockIdx.x * (kMoveThreads / 8) + (threadIdx.x >> 3);
+    if (i >= p.moves[row]) return;
     const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
-    const int G = p.page.groups(), quads = p.page.D / 4;
-    const int warps = gridDim.x * (kMoveThreads / 32);
-    for (int i = blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); i < n; i += warps) {
-        const int dst = p.holes[row * p.most + i], src = p.tails[row * p.most + i];
-        const int db = table[dst / p.page.B], sb = table[src / p.page.B];
-        if (db < 0 || db >= p.num_blocks || sb < 0 || sb >= p.num_blocks) {
-            if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-            continue;
-        }
-        uint8_t *to = p.pool + ((int64_t)db * p.H + h) * p.page.bytes();
-        const uint8_t *fr = p.pool + ((int64_t)sb * p.H + h) * p.page.bytes();
-        const int d = dst % p.page.B, s = src % p.page.B;
-        for (int q = lane; q < quads; q += 32) {
-            *reinterpret_cast<uint16_t *>(to + k_piece(p.page, d, q >> 3, q & 7)) =
-                *reinterpret_cast<const uint16_t *>(fr + k_piece(p.page, s, q >> 3, q & 7));
-            *reinterpret_cast<uint16_t *>(to + v_piece(p.page, d, q >> 3, q & 7)) =
-                *reinterpret_cast<const uint16_t *>(fr + v_piece(p.page, s, q >> 3, q & 7));
-        }
-        if (lane < G) {
-            *reinterpret_cast<uint16_t *>(to + k_step_at(p.page, d, lane)) =
-                *reinterpret_cast<const uint16_t *>(fr + k_step_at(p.page, s, lane));
-            *reinterpret_cast<uint16_t *>(to + v_step_at(p.page, d, lane)) =
-                *reinterpret_cast<const uint16_t *>(fr + v_step_at(p.page, s, lane));
-        }
+    const int G = p.page.groups();
+    const int dst = p.holes[row * p.most + i], src = p.tails[row * p.most + i];
+    const int db = table[dst / p.page.B], sb = table[src / p.page.B];
+    if (db < 0 || db >= p.num_blocks || sb < 0 || sb >= p.num_blocks) {
+        if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        return;
     }
+    uint8_t *to = p.pool + ((int64_t)db * p.H + h) * p.page.bytes();
+    const uint8_t *fr = p.pool + ((int64_t)sb * p.H + h) * p.page.bytes();
+    const int d = dst % p.page.B, s = src % p.page.B;
+    constexpr int kMost = KVI_MAX_ATTN_HEAD_DIM / 32;
+    uint32_t k[kMost / 2];
+    uint16_t v[kMost], ks = 0, vs = 0;
+#pragma unroll
+    for (int g = 0; g < kMost; ++g) {
+        const int word = lane + 8 * g;  // of the row's 4 G words of K codes
+        if (g < kMost / 2 && word < 4 * G) k[g] = *reinterpret_cast<const uint32_t *>(fr + (int64_t)s * (p.page.D / 2) + 4 * word);
+        if (g < G) v[g] = *reinterpret_cast<const uint16_t *>(fr + v_piece(p.page, s, g, lane));
+    }
+    if (lane < G) {
+        ks = *reinterpret_cast<const uint16_t *>(fr + k_step_at(p.page, s, lane));
+        vs = *reinterpret_cast<const uint16_t *>(fr + v_step_at(p.page, s, lane));
+    }
+#pragma unroll
+    for (int g = 0; g < kMost; ++g) {
+        const int word = lane + 8 * g;
+        if (g < kMost / 2 && word < 4 * G) *reinterpret_cast<uint32_t *>(to + (int64_t)d * (p.page.D / 2) + 4 * word) = k[g];
+        if (g < G) *reinterpret_cast<uint16_t *>(to + v_piece(p.page, d, g, lane)) = v[g];
+    }
+    if (lane < G) {
+        *reinterpret_cast<uint16_t *>(to + k_step_at(p.page, d, lane)) = ks;
+        *reinterpret_cast<uint16_t *>(to + v_step_at(p.page, d, lane)) = vs;
+    }
+}
+
+// A block's threads and the slots a thread keeps, by the longest row.
+cudaError_t launch_select(EvictParams &p, unsigned rows, cudaStream_t s)
+{
+    if (p.max_ctx <= 2048) return launch_chained(evict_select_kernel<512, 4>, dim3(rows), 512, 0, s, p);
+    if (p.max_ctx <= 4096) return launch_chained(evict_select_kernel<512, 8>, dim3(rows), 512, 0, s, p);
+    if (p.max_ctx <= 8192) return launch_chained(evict_select_kernel<1024, 8>, dim3(rows), 1024, 0, s, p);
+    p.cap = std::min(p.max_ctx, kRankCap);
+    const cudaError_t e = smem_opt_in(evict_select_kernel<1024, 0>, kRankCap * 4);
+    if (e != cudaSuccess) return e;
+    return launch_chained(evict_select_kernel<1024, 0>, dim3(rows), 1024, (size_t)p.cap * 4, s, p);
 }
 
 bool aligned16(const void *p, int64_t stride) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride % 8 == 0; }
@@ -415,7 +591,7 @@ kvi_status rows_params(RowParams &p, int32_t H, int32_t D, const kvi_paged_cache
     if (T && (!k || !v || unusable(slots, 8))) return arg_error("d_k, d_v and d_slots are required");
     if (T && (!aligned16(k, ks) || !aligned16(v, vs) || ks < (int64_t)H * D || vs < (int64_t)H * D))
         return arg_error("rows must be 16-byte aligned, with strides of at least kv_heads * head_dim elements");
-    if (T * H * (D / 4) / kRowThreads >= 0x7fffffff) return arg_error("T=%lld rows are too many", (long long)T);
+    if (T >= 0xfffffff0ll) return arg_error("T=%lld rows are too many", (long long)T);
     p.k_stride = ks;
     p.v_stride = vs;
     p.slots = slots;
@@ -429,9 +605,15 @@ kvi_status rows_params(RowParams &p, int32_t H, int32_t D, const kvi_paged_cache
     return KVI_OK;
 }
 
-unsigned row_blocks(const RowParams &p)
+// Pairs of rows on x (one more than half the rows: pairs may start at row -1),
+// the parts of a wide pair on y.
+dim3 row_blocks(RowParams &p)
 {
-    return (unsigned)((p.T * p.H * (p.D / 4) + kRowThreads - 1) / kRowThreads);
+    p.lanes = p.H * (p.D / 8);
+    p.pairs = kRowThreads / p.lanes;
+    const int64_t pairs = p.T / 2 + 1;
+    if (p.pairs) return dim3((unsigned)((pairs + p.pairs - 1) / p.pairs));
+    return dim3((unsigned)pairs, (unsigned)((p.lanes + kRowThreads - 1) / kRowThreads));
 }
 
 size_t evict_bytes(int32_t H, int32_t R, int32_t max_ctx, int32_t *most)
@@ -469,8 +651,8 @@ extern "C" kvi_status kvi_cache4_write(int32_t kv_heads, int32_t head_dim, const
     if (st != KVI_OK || T == 0) return st;
     p.k_in = static_cast<const __nv_bfloat16 *>(d_k);
     p.v_in = static_cast<const __nv_bfloat16 *>(d_v);
-    cache4_write_kernel<<<row_blocks(p), kRowThreads, 0, stream>>>(p);
-    return cuda_status(cudaGetLastError(), "kvi_cache4_write");
+    const dim3 grid = row_blocks(p);
+    return cuda_status(launch_chained(cache4_write_kernel, grid, kRowThreads, 0, stream, p), "kvi_cache4_write");
 }
 
 extern "C" kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const kvi_paged_cache *cache, int32_t layer,
@@ -483,8 +665,8 @@ extern "C" kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const 
     if (st != KVI_OK || T == 0) return st;
     p.k_out = static_cast<__nv_bfloat16 *>(d_k);
     p.v_out = static_cast<__nv_bfloat16 *>(d_v);
-    cache4_read_kernel<<<row_blocks(p), kRowThreads, 0, stream>>>(p);
-    return cuda_status(cudaGetLastError(), "kvi_cache4_read");
+    const dim3 grid = row_blocks(p);
+    return cuda_status(launch_chained(cache4_read_kernel, grid, kRowThreads, 0, stream, p), "kvi_cache4_read");
 }
 
 extern "C" size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int32_t max_ctx)
@@ -543,26 +725,12 @@ extern "C" kvi_status kvi_cache4_evict(int32_t kv_heads, int32_t head_dim, int32
     p.tails = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + list);
     p.moves = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + 2 * list);
     p.status = d_status;
-    p.cap = std::min(max_ctx, kRankCap);
-    cudaError_t e = smem_opt_in(evict_select_kernel, kRankCap * 4);
-    if (e != cudaSuccess) return cuda_status(e, "kvi_cache4_evict");
-    evict_select_kernel<<<(unsigned)(R * kv_heads), kEvictThreads, (size_t)p.cap * 4, stream>>>(p);
-    st = cuda_status(cudaGetLastError(), "kvi_cache4_evict");
+    cudaError_t e = launch_select(p, (unsigned)(R * kv_heads), stream);
+    st = cuda_status(e, "kvi_cache4_evict");
     if (st != KVI_OK || max_ctx <= budget) return st;  // nothing can move
-    // enough warps that none copies more than a few rows, without a grid of
-    // mostly idle blocks where many heads share the GPU
-    const int rows = std::min(p.most, budget);
-    const int want = std::max(1, 4096 / (R * kv_heads));
-    const unsigned gx = (unsigned)std::min((rows + kMoveThreads / 32 - 1) / (kMoveThreads / 32), want);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(gx, (unsigned)(R * kv_heads));
-    cfg.blockDim = dim3(kMoveThreads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, evict_move_kernel, p);
-    return cuda_status(e != cudaSuccess ? e : cudaGetLastError(), "kvi_cache4_evict");
+    const int rows = std::min(budget, max_ctx - budget);  // a head moves at most so many
+    const unsigned gx = (unsigned)((rows + kMoveThreads / 8 - 1) / (kMoveThreads / 8));
+    const dim3 grid(gx, (unsigned)(R * kv_heads));
+    e = launch_chained(evict_move_kernel, grid, kMoveThreads, 0, stream, p);
+    return cuda_status(e, "kvi_cache4_evict");
 }

@@ -293,7 +293,8 @@ def run_evict(c, ctx, budget, sink, recent, w, pos, max_ctx=None):
 @pytest.mark.parametrize("kind", ["random", "ties", "equal", "special"])
 @pytest.mark.parametrize("H,D,B,ctx,budget,sink,recent", [
     (2, 64, 16, [100, 30, 0, 31, 1], 30, 4, 8), (1, 128, 16, [2500], 1024, 4, 64), (3, 96, 48, [500, 400], 499, 0, 0),
-    (2, 32, 16, [1100, 1025], 1, 0, 1), (1, 256, 16, [90], 80, 10, 70), (2, 64, 16, [3000, 2000], 1500, 0, 1500)])
+    (2, 32, 16, [1100, 1025], 1, 0, 1), (1, 256, 16, [90], 80, 10, 70), (2, 64, 16, [3000, 2000], 1500, 0, 1500),
+    (2, 32, 32, [7000, 4097], 4000, 4, 64), (1, 32, 64, [30001, 8193, 26000], 8192, 4, 64)])
 def test_evict(H, D, B, ctx, budget, sink, recent, kind):
     c = Step(H, H, D, B, ctx, seed=budget)
     g = ac.gen(budget + len(kind))
