@@ -63,7 +63,7 @@ template <int DP>
 struct TileTail {
     uint64_t q_full;
     uint64_t full[TileSmem<DP>::kStages], empty[TileSmem<DP>::kStages];
-    uint64_t s_full[2], p_full[2], o_full[2];
+    uint64_t s_full[2], p_full[2][2], o_full[2];  // p: P's first and second 64 keys
     uint64_t v_fixed;
     uint64_t drained;
     uint32_t tmem;
@@ -76,20 +76,15 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 
 // Shared-memory descriptors, 128-byte swizzle: rows of 128 bytes in groups of
 // 8 (1024 bytes).  K-major (Q, K): the stride offset is the group's; MN-major
-// (V): 64 channels of 8 keys are a group, the next 64 channels lie `half` on.
-__device__ __forceinline__ uint64_t desc_k(uint32_t a)
-{
-    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
-           ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_mn(uint32_t a)
-{
-    return (uint64_t)((a & 0x3FFFFu) >> 4) | ((uint64_t)(kHalf >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// (V): 64 channels of 8 keys are a group, the next 64 channels lie a half on
+// (the leading offset, which K-major operands do not use).  The address is the
+// low word's, in units of 16 bytes, so that a step is an addition to it.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t a) { return (a >> 4) | ((uint32_t)(kHalf >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
 
 // Instruction descriptor: D float32, A and B bf16, M = 128, N, B K- or MN-major
-__device__ __forceinline__ uint32_t bf16_idesc(int n, bool b_mn)
+__host__ __device__ constexpr uint32_t bf16_idesc(int n, bool b_mn)
 {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
            ((uint32_t)(kM >> 4) << 24);
@@ -154,8 +149,42 @@ __device__ __forceinline__ void tmem_store16(uint32_t a, const uint32_t *v)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Wait for this thread's loads; the registers are named so that nothing that
+// uses them moves ahead of the wait.
+__device__ __forceinline__ void tmem_wait_ld(float *v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]),
+                   "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]),
+                   "+f"(v[22]), "+f"(v[23]), "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]),
+                   "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Two float32 operations in one instruction
+__device__ __forceinline__ uint64_t pair2(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ void split2(uint64_t v, float &a, float &b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
 
 __device__ __forceinline__ float max3(float a, float b, float c)
 {
@@ -214,6 +243,37 @@ __device__ __forceinline__ void fix_values(uint8_t *v, int kr, int key, int ctx,
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
+// The largest of 64 scores
+__device__ __forceinline__ float largest64(const float *s)
+{
+    float t[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) t[c] = max3(s[3 * c], s[3 * c + 1], s[3 * c + 2]);
+#pragma unroll
+    for (int c = 12; c + 8 <= 64; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] = max3(t[e], s[c + 2 * e], s[c + 2 * e + 1]);
+    t[0] = max3(t[0], s[60], s[61]);
+    t[1] = max3(t[1], s[62], s[63]);
+    return fmaxf(max3(t[0], t[1], t[2]), t[3]);
+}
+
+// Scores from column `vis` on are not seen
+__device__ __forceinline__ void mask_scores(float *s, int vis)
+{
+#pragma unroll
+    for (int c = 0; c < kM; ++c) s[c] = c < vis ? s[c] : neg_inf();
+}
+
+// This warp's part of P has reached tensor memory
+__device__ __forceinline__ void announce(uint64_t &bar)
+{
+    tmem_wait_st();
+    fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+}
+
 template <int DP>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
@@ -267,7 +327,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&tl.s_full[i]), 1);
-            mbar_init(smem_u32(&tl.p_full[i]), kM);
+            mbar_init(smem_u32(&tl.p_full[i][0]), 4);
+            mbar_init(smem_u32(&tl.p_full[i][1]), 4);
             mbar_init(smem_u32(&tl.o_full[i]), 1);
         }
         mbar_init(smem_u32(&tl.v_fixed), kM);
@@ -325,7 +386,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!there) block = 0;
             for (int plane = 0; plane < 2; ++plane) {
                 bool got = true;
-                if (lane == 0) got = mbar_wait(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
+                if (lane == 0) got = mbar_wait_brisk(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
                 if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
                     if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                     ok = false;
@@ -348,34 +409,38 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (!ok) {
             if (lane < Sm::kStages && lane < slots) {
                 const int last = (slots - 1 - lane) / Sm::kStages;
-                (void)mbar_wait(smem_u32(&tl.full[lane]), (uint32_t)(last & 1), kTileWaitNs);
+                (void)mbar_wait_brisk(smem_u32(&tl.full[lane]), (uint32_t)(last & 1), kTileWaitNs);
             }
-            if (lane == 0 && n > 0) (void)mbar_wait(smem_u32(&tl.q_full), 0, kTileWaitNs);
+            if (lane == 0 && n > 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
         }
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------- matrix products
         if (lane == 0 && n > 0) {
-            const uint32_t id_s = bf16_idesc(kM, false), id_o = bf16_idesc(DP, true);
-            bool ok = mbar_wait(smem_u32(&tl.q_full), 0, kTileWaitNs);
+            constexpr uint32_t id_s = bf16_idesc(kM, false), id_o = bf16_idesc(DP, true);
+            bool ok = mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
             auto wait_slot = [&](int slot) {
-                return mbar_wait(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+                return mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
             };
-            auto stage_at = [&](int slot) { return smem_u32(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile); };
+            const uint32_t q_lo = desc_lo(smem_u32(base + Sm::kQ)), ring_lo = desc_lo(smem_u32(base + Sm::kRing));
+            auto stage_lo = [&](int slot) { return ring_lo + (slot % Sm::kStages) * (Sm::kTile >> 4); };
             auto free_slot = [&](int slot) { mma_commit(smem_u32(&tl.empty[slot % Sm::kStages])); };
             auto scores = [&](int i, int j) {
-                const uint32_t a = smem_u32(base + Sm::kQ + i * Sm::kTile), b = stage_at(2 * j);
+                const uint32_t a = q_lo + i * (Sm::kTile >> 4), b = stage_lo(2 * j);
 #pragma unroll
                 for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t at = (k >> 2) * kHalf + (k & 3) * 32;
-                    mma_ss(tmem + i * kM, desc_k(a + at), desc_k(b + at), id_s, k > 0);
+                    const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                    mma_ss(tmem + i * kM, desc(a + at), desc(b + at), id_s, k > 0);
                 }
                 mma_commit(smem_u32(&tl.s_full[i]));
             };
-            auto values = [&](int i, int j) {
-                const uint32_t b = stage_at(2 * j + 1);
+            // the keys of one half of a tile, as soon as their P is there
+            auto values = [&](int i, int j, int half) {
+                const uint32_t b = stage_lo(2 * j + 1);
 #pragma unroll
-                for (int k = 0; k < kM / 16; ++k)
-                    mma_ts(tmem + kColO + i * DP, tmem + i * kM + 8 * k, desc_mn(b + k * 2048), id_o, j > 0 || k > 0);
+                for (int k = 0; k < kM / 32; ++k) {
+                    const int kk = half * (kM / 32) + k;
+                    mma_ts(tmem + kColO + i * DP, tmem + i * kM + 8 * kk, desc(b + kk * (2048 >> 4)), id_o, j > 0 || kk > 0);
+                }
             };
             uint32_t fixes = 0;
             ok = ok && wait_slot(0);
@@ -387,13 +452,16 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             for (int j = 0; j < n && ok; ++j) {
                 ok = wait_slot(2 * j + 1);
-                if (ok && from + (j + 1) * kM > sure) ok = mbar_wait(smem_u32(&tl.v_fixed), fixes++ & 1u, kTileWaitNs);
+                if (ok && from + (j + 1) * kM > sure) ok = mbar_wait_brisk(smem_u32(&tl.v_fixed), fixes++ & 1u, kTileWaitNs);
                 for (int i = 0; i < 2 && ok; ++i) {
                     if (j < n_tiles[i]) {
-                        ok = mbar_wait(smem_u32(&tl.p_full[i]), (uint32_t)(j & 1), kTileWaitNs);
+                        for (int half = 0; half < 2 && ok; ++half) {
+                            ok = mbar_wait_brisk(smem_u32(&tl.p_full[i][half]), (uint32_t)(j & 1), kTileWaitNs);
+                            if (!ok) break;
+                            fence_after();
+                            values(i, j, half);
+                        }
                         if (!ok) break;
-                        fence_after();
-                        values(i, j);
                         if (j + 1 == n_tiles[i]) mma_commit(smem_u32(&tl.o_full[i]));
                     }
                     if (i == 1) free_slot(2 * j + 1);
@@ -410,7 +478,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             // whatever ended the loop, no product may still run when tensor
             // memory is given back
             mma_commit(smem_u32(&tl.drained));
-            if (!mbar_wait(smem_u32(&tl.drained), 0, kTileWaitNs)) record_status(p.status, KVI_ERR_TIMEOUT);
+            if (!mbar_wait_brisk(smem_u32(&tl.drained), 0, kTileWaitNs)) record_status(p.status, KVI_ERR_TIMEOUT);
         }
         __syncwarp();
     }
@@ -432,41 +500,46 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const bool partly = key0 + kM > sure;
             if (partly && i == (j < n_tiles[1] ? 1 : 0)) {
                 const int slot = 2 * j + 1;
-                ok = ok && mbar_wait(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+                ok = ok && mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
                 if (ok) fix_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, row, key0 + row, rq.ctx, tl);
                 mbar_arrive(smem_u32(&tl.v_fixed));
             }
-            ok = ok && mbar_wait(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
+            ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 ok = false;
                 break;
             }
             fence_after();
+            // two loads of 64 scores; the first half's largest is found while the
+            // second is on its way
             float s[kM];
+            tmem_load32(t_s, s);
+            tmem_load32(t_s + 32, s + 32);
+            tmem_wait_ld(s);
+            tmem_wait_ld(s + 32);
+            tmem_load32(t_s + 64, s + 64);
+            tmem_load32(t_s + 96, s + 96);
+            float top;
+            if (partly || lost) {
+                tmem_wait_ld(s + 64);
+                tmem_wait_ld(s + 96);
+                mask_scores(s, last + 1 - key0);
+                if (lost) {
+                    uint32_t gone[4] = {0, 0, 0, 0};
+                    for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
+                        if ((uint32_t)table[(key0 + c) / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_load32(t_s + 32 * c, s + 32 * c);
-            tmem_wait_ld();
-            if (partly) {
-                const int vis = last + 1 - key0;
-#pragma unroll
-                for (int c = 0; c < kM; ++c) s[c] = c < vis ? s[c] : neg_inf();
+                    for (int c = 0; c < kM; ++c)
+                        if ((gone[c >> 5] >> (c & 31)) & 1u) s[c] = neg_inf();
+                }
+                top = fmaxf(largest64(s), largest64(s + 64));
+            } else {
+                top = largest64(s);
+                tmem_wait_ld(s + 64);
+                tmem_wait_ld(s + 96);
+                top = fmaxf(top, largest64(s + 64));
             }
-            if (lost) {
-                uint32_t gone[4] = {0, 0, 0, 0};
-                for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
-                    if ((uint32_t)table[(key0 + c) / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
-#pragma unroll
-                for (int c = 0; c < kM; ++c)
-                    if ((gone[c >> 5] >> (c & 31)) & 1u) s[c] = neg_inf();
-            }
-            float top = max3(s[0], s[1], s[2]), top2 = max3(s[3], s[4], s[5]);
-#pragma unroll
-            for (int c = 6; c < kM - 2; c += 4) {
-                top = max3(top, s[c], s[c + 1]);
-                top2 = max3(top2, s[c + 2], s[c + 3]);
-            }
-            top = fmaxf(max3(top, s[kM - 2], s[kM - 1]), top2);
             const bool move = top > limit;
             if (__any_sync(0xffffffffu, move)) {
                 const float f = move ? exp2_fast((m - top) * p.scale) : 1.f;
@@ -481,36 +554,41 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     for (int c = 0; c < DP; c += 32) {
                         float v[32];
                         tmem_load32(t_o + c, v);
-                        tmem_wait_ld();
+                        tmem_wait_ld(v);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) v[e] *= f;
                         tmem_store32(t_o + c, v);
                     }
                 }
             }
-            float part[4] = {0.f, 0.f, 0.f, 0.f};
+            const uint64_t scale2 = pair2(p.scale, p.scale), ref2 = pair2(-ref, -ref);
+            uint64_t part[2] = {0, 0};  // sums of even and odd keys, twice
 #pragma unroll
             for (int c = 0; c < kM; c += 32) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    const float p0 = exp2_fast(fmaf(s[c + e], p.scale, -ref));
-                    const float p1 = exp2_fast(fmaf(s[c + e + 1], p.scale, -ref));
-                    part[e & 2] += p0;
-                    part[(e & 2) + 1] += p1;
+                    float p0, p1;
+                    split2(fma2(pair2(s[c + e], s[c + e + 1]), scale2, ref2), p0, p1);
+                    p0 = exp2_fast(p0);
+                    p1 = exp2_fast(p1);
+                    part[(e >> 1) & 1] = add2(part[(e >> 1) & 1], pair2(p0, p1));
                     w[e / 2] = pack_bf16(p0, p1);
                 }
+                // the first half of P is announced when the third quarter is
+                // computed, so that its way to tensor memory is not waited for
+                if (c == 64) announce(tl.p_full[i][0]);
                 tmem_store16(t_s + c / 2, w);
             }
-            sum += (part[0] + part[1]) + (part[2] + part[3]);
-            tmem_wait_st();
-            fence_before();
-            mbar_arrive(smem_u32(&tl.p_full[i]));
+            float a, b;
+            split2(add2(part[0], part[1]), a, b);
+            sum += a + b;
+            announce(tl.p_full[i][1]);
         }
         // ---- the rows' results; both tiles' warps have looked over their values
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (my > 0 && ok) {
-            ok = mbar_wait(smem_u32(&tl.o_full[i]), 0, kTileWaitNs);
+            ok = mbar_wait_brisk(smem_u32(&tl.o_full[i]), 0, kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 ok = false;
@@ -528,7 +606,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 float v[32];
                 if (my > 0) {
                     tmem_load32(t_o + c, v);
-                    tmem_wait_ld();
+                    tmem_wait_ld(v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;

@@ -66,5 +66,20 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, uint64_
     }
 }
 
+// mbar_wait for waits that a kernel's pace depends on: the clock, whose
+// reading takes longer than a try, is read once in 32 tries.
+__device__ __forceinline__ bool mbar_wait_brisk(uint32_t bar, uint32_t parity, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (uint32_t n = 0;; ++n) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((n & 31u) == 31u) {
+            const uint64_t t = global_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 > limit_ns) return false;
+        }
+    }
+}
+
 }  // namespace
 }  // namespace kvi
