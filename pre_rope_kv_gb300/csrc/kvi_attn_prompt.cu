@@ -392,9 +392,9 @@ PromptPlan plan_tiles(const kvi_attention &a, int32_t R, int32_t total_q, int32_
     return pl;
 }
 
-// The tensor-core tiles want 16-byte channels in boxes of 8 tokens and up to
-// 128 channels, and pay once a request has more rows than the other form
-// keeps in one or a few blocks.
+// The tensor-core tiles want boxes of 8 tokens or more of a page, up to 128
+// channels, and pay once a request has more rows than the other form keeps in
+// a few blocks.
 constexpr int kRowsMost = 64;
 bool tiles_fit(const kvi_attention &a, int32_t max_q, int32_t num_blocks, int32_t block_size)
 {

@@ -42,7 +42,7 @@ namespace kvi {
 namespace {
 
 constexpr int kM = 128;           // rows of a tile, keys of a tile
-constexpr int kCopyWarp = 8, kMmaWarp = 9;  // after four softmax warps per tile; two warps idle
+constexpr int kCopyK = 8, kMmaWarp = 9, kCopyV = 10;  // after four softmax warps per tile; one warp idles
 constexpr int kTileThreads = 12 * 32;
 // Registers: the launch gives 168 a thread (65536 / 384); the third warpgroup
 // keeps 72 of them, so that the softmax's hold a row of scores: 2 * 216 + 72 =
@@ -90,27 +90,40 @@ __host__ __device__ constexpr uint32_t bf16_idesc(int n, bool b_mn)
            ((uint32_t)(kM >> 4) << 24);
 }
 
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
+// The matrix instructions are issued by one lane but reached by the whole warp:
+// their operands then are uniform values, which is where the instruction takes
+// them from.
+__device__ __forceinline__ uint32_t one_lane()
+{
+    uint32_t p;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p;
+}
+
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-        "r"(add ? 1u : 0u)
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1u : 0u), "r"(lead)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
 {
     asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-        "r"(add ? 1u : 0u)
+        "{\n.reg .pred p, q;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+        "r"(add ? 1u : 0u), "r"(lead)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_commit(uint32_t bar)
+__device__ __forceinline__ void mma_commit(uint32_t lead, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar), "r"(lead)
+        : "memory");
 }
 
 // 32 columns of this warp's 32 lanes (no wait)
@@ -308,7 +321,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int seen0 = rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
-    int n_tiles[2];
+    int n_tiles[2];  // (indexed by constants alone: they stay in registers)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t0 = tok0 + i * per, t1 = min(rq.n_q, t0 + per);
@@ -353,132 +366,167 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // tensor memory: S (and P) of the two tiles, then their O
     constexpr int kColO = 2 * kM;
 
-    if (warp >= kCopyWarp) {
+    if (warp >= kCopyK) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == kCopyWarp) {
+    if (warp == kCopyK || warp == kCopyV) {
         // ------------------------------------------------------------ copies
-        if (lane < 2 && n > 0) {
+        if (warp == kCopyK && lane < 2 && n > 0) {
             const int t0 = tok0 + lane * per;
             const uint32_t bar = smem_u32(&tl.q_full);
             // rows past the tile's tokens keep what the memory held: their scores
             // are computed and not used
-            if (lane == 0)
-                mbar_expect_tx(bar, (n_tiles[1] > 0 ? 2 : 1) * Sm::kHalves * per * p.G * 128);
+            if (lane == 0) mbar_expect_tx(bar, (n_tiles[1] > 0 ? 2 : 1) * Sm::kHalves * per * p.G * 128);
             __syncwarp(3u);
             if (lane == 0 || n_tiles[1] > 0)
                 for (int x = 0; x < Sm::kHalves; ++x)
                     box3(smem_u32(base + Sm::kQ + lane * Sm::kTile + x * kHalf), &tm_q, 64 * x, h * p.G, rq.q0 + t0, bar);
         }
         __syncwarp();
-        const int boxes = kM / box_keys;
-        const int half = lane / boxes, box = lane % boxes;  // 32 lanes cover two halves of 16 boxes
-        int stage = 0;
-        uint32_t phase = 1;  // an unused stage is empty
+        // one warp copies K, one V; a box a lane: 32 lanes cover two halves of 16
+        const int plane = warp == kCopyV ? 1 : 0;
+        const int boxes = kM / box_keys, half = lane / boxes, box = lane % boxes;
+        const uint32_t dst = smem_u32(base + Sm::kRing) + half * kHalf + box * box_keys * 128;
+        uint32_t stage = plane, phase = 1;  // an unused stage is empty
         bool ok = true;
         int slots = 0;
-        for (int j = 0; j < n && ok; ++j) {
+        for (int j = 0; j < n; ++j) {
             const int key = from + j * kM + box * box_keys;
             int block = key < rq.ctx ? table[key / p.B] : -1;
             // a piece past the end, or of a block that is not there, reads as
             // zeros from past a page's last token
             const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
             const int y = there ? key % p.B : p.B;
-            if (!there) block = 0;
-            for (int plane = 0; plane < 2; ++plane) {
-                bool got = true;
-                if (lane == 0) got = mbar_wait_brisk(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
-                if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
-                    if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
-                    ok = false;
-                    break;
-                }
-                const uint32_t bar = smem_u32(&tl.full[stage]);
-                if (lane == 0) mbar_expect_tx(bar, Sm::kTile);
-                __syncwarp();
-                if (half < Sm::kHalves)
-                    box4(smem_u32(base + Sm::kRing + stage * Sm::kTile + half * kHalf + box * box_keys * 128), &tm_kv,
-                         64 * half, h, y, plane * p.num_blocks + block, bar);
-                ++slots;
-                if (++stage == Sm::kStages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
+            block = plane * p.num_blocks + (there ? block : 0);
+            bool got = true;
+            if (lane == 0) got = mbar_wait_brisk(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
+            if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                ok = false;
+                break;
+            }
+            const uint32_t bar = smem_u32(&tl.full[stage]);
+            if (lane == 0) mbar_expect_tx(bar, Sm::kTile);
+            __syncwarp();
+            if (half < Sm::kHalves) box4(dst + stage * Sm::kTile, &tm_kv, 64 * half, h, y, block, bar);
+            ++slots;
+            stage += 2;
+            if (stage >= Sm::kStages) {
+                stage = plane;
+                phase ^= 1u;
             }
         }
         // no copy may still be writing when the block ends
         if (!ok) {
-            if (lane < Sm::kStages && lane < slots) {
-                const int last = (slots - 1 - lane) / Sm::kStages;
-                (void)mbar_wait_brisk(smem_u32(&tl.full[lane]), (uint32_t)(last & 1), kTileWaitNs);
+            constexpr int kOwn = Sm::kStages / 2;
+            if (lane < kOwn && lane < slots) {
+                const int last = (slots - 1 - lane) / kOwn;
+                (void)mbar_wait_brisk(smem_u32(&tl.full[2 * lane + plane]), (uint32_t)(last & 1), kTileWaitNs);
             }
-            if (lane == 0 && n > 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
+            if (lane == 0 && plane == 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
         }
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------- matrix products
-        if (lane == 0 && n > 0) {
+        if (n > 0) {
+            const uint32_t lead = one_lane();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            // This warp's latencies set the pace of everything here, so between two
+            // products there is little more than a wait, and what the next tile of
+            // keys needs is looked after while products are queued.
             constexpr uint32_t id_s = bf16_idesc(kM, false), id_o = bf16_idesc(DP, true);
-            bool ok = mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
-            auto wait_slot = [&](int slot) {
-                return mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
-            };
+            constexpr uint32_t kTileLo = Sm::kTile >> 4;
             const uint32_t q_lo = desc_lo(smem_u32(base + Sm::kQ)), ring_lo = desc_lo(smem_u32(base + Sm::kRing));
-            auto stage_lo = [&](int slot) { return ring_lo + (slot % Sm::kStages) * (Sm::kTile >> 4); };
-            auto free_slot = [&](int slot) { mma_commit(smem_u32(&tl.empty[slot % Sm::kStages])); };
-            auto scores = [&](int i, int j) {
-                const uint32_t a = q_lo + i * (Sm::kTile >> 4), b = stage_lo(2 * j);
-#pragma unroll
-                for (int k = 0; k < DP / 16; ++k) {
-                    const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                    mma_ss(tmem + i * kM, desc(a + at), desc(b + at), id_s, k > 0);
-                }
-                mma_commit(smem_u32(&tl.s_full[i]));
-            };
-            // the keys of one half of a tile, as soon as their P is there
-            auto values = [&](int i, int j, int half) {
-                const uint32_t b = stage_lo(2 * j + 1);
-#pragma unroll
-                for (int k = 0; k < kM / 32; ++k) {
-                    const int kk = half * (kM / 32) + k;
-                    mma_ts(tmem + kColO + i * DP, tmem + i * kM + 8 * kk, desc(b + kk * (2048 >> 4)), id_o, j > 0 || kk > 0);
-                }
-            };
-            uint32_t fixes = 0;
-            ok = ok && wait_slot(0);
-            if (ok) {
+            const uint32_t full0 = smem_u32(&tl.full[0]), empty0 = smem_u32(&tl.empty[0]);
+            const uint32_t s_bar = smem_u32(&tl.s_full[0]), p_bar = smem_u32(&tl.p_full[0][0]);
+            const uint32_t o_bar = smem_u32(&tl.o_full[0]), fixed_bar = smem_u32(&tl.v_fixed);
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                const bool got = __all_sync(0xffffffffu, mbar_wait_brisk(bar, parity, kTileWaitNs));
                 fence_after();
-                for (int i = 0; i < 2; ++i)
-                    if (n_tiles[i] > 0) scores(i, 0);
-                free_slot(0);
-            }
-            for (int j = 0; j < n && ok; ++j) {
-                ok = wait_slot(2 * j + 1);
-                if (ok && from + (j + 1) * kM > sure) ok = mbar_wait_brisk(smem_u32(&tl.v_fixed), fixes++ & 1u, kTileWaitNs);
-                for (int i = 0; i < 2 && ok; ++i) {
-                    if (j < n_tiles[i]) {
-                        for (int half = 0; half < 2 && ok; ++half) {
-                            ok = mbar_wait_brisk(smem_u32(&tl.p_full[i][half]), (uint32_t)(j & 1), kTileWaitNs);
-                            if (!ok) break;
-                            fence_after();
-                            values(i, j, half);
-                        }
-                        if (!ok) break;
-                        if (j + 1 == n_tiles[i]) mma_commit(smem_u32(&tl.o_full[i]));
-                    }
-                    if (i == 1) free_slot(2 * j + 1);
-                    if (j + 1 < n_tiles[i]) {
-                        ok = wait_slot(2 * j + 2);
-                        if (!ok) break;
-                        fence_after();
-                        scores(i, j + 1);
-                    }
-                    if (i == 1 && j + 1 < n) free_slot(2 * j + 2);
+                return got;
+            };
+            auto score_part = [&](int i, uint32_t stage, int k0, int k1) {
+#pragma unroll
+                for (int k = k0; k < k1; ++k) {
+                    const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                    mma_ss(lead, tm + i * kM, desc(q_lo + i * kTileLo + at), desc(ring_lo + stage * kTileLo + at), id_s, k > 0);
                 }
+            };
+            constexpr int kSteps = DP / 16;
+            // the keys of one half of a tile, as soon as their P is there
+            auto values = [&](int i, uint32_t stage, int half, bool add) {
+                const uint32_t b = ring_lo + stage * kTileLo + half * (kHalf / 2 >> 4);
+#pragma unroll
+                for (int k = 0; k < kM / 32; ++k)
+                    mma_ts(lead, tm + kColO + i * DP, tm + i * kM + half * (kM / 4) + 8 * k, desc(b + k * (2048 >> 4)), id_o,
+                           add || half > 0 || k > 0);
+            };
+            const int n0 = n_tiles[0], n1 = n_tiles[1];
+            const int first_partly = sure > from ? (sure - from) / kM : 0;  // first tile that some row sees in part
+            uint32_t fixes = 0;
+            // Tile j of the keys, V in stage `vs` and K of j + 1 in stage `ks`; V's
+            // copy has been waited for.
+            auto step = [&](int j, uint32_t vs, uint32_t vnext, uint32_t ks, uint32_t kph, uint32_t vnph) {
+                const uint32_t par = (uint32_t)(j & 1);
+                const bool more0 = j + 1 < n0, more1 = j + 1 < n1, more = more0 || more1;
+                if (j >= first_partly && !wait(fixed_bar, fixes++ & 1u)) return false;
+                if (j < n0) {
+                    if (!wait(p_bar, par)) return false;
+                    values(0, vs, 0, j > 0);
+                    if (more && !wait(full0 + 8 * ks, kph)) return false;
+                    if (!wait(p_bar + 8, par)) return false;
+                    values(0, vs, 1, j > 0);
+                    if (!more0) mma_commit(lead, o_bar);
+                } else if (more && !wait(full0 + 8 * ks, kph)) {
+                    return false;
+                }
+                if (more0) {
+                    score_part(0, ks, 0, kSteps);
+                    mma_commit(lead, s_bar);
+                }
+                if (j < n1) {
+                    if (!wait(p_bar + 16, par)) return false;
+                    values(1, vs, 0, j > 0);
+                    if (!wait(p_bar + 24, par)) return false;
+                    values(1, vs, 1, j > 0);
+                    if (!more1) mma_commit(lead, o_bar + 8);
+                }
+                if (more1) score_part(1, ks, 0, kSteps / 2);
+                mma_commit(lead, empty0 + 8 * vs);
+                if (more && !wait(full0 + 8 * vnext, vnph)) return false;
+                if (more1) {
+                    score_part(1, ks, kSteps / 2, kSteps);
+                    mma_commit(lead, s_bar + 8);
+                }
+                if (more) mma_commit(lead, empty0 + 8 * ks);
+                return true;
+            };
+            bool ok = wait(smem_u32(&tl.q_full), 0) && wait(full0, 0);
+            if (ok) {
+                if (n0 > 0) {
+                    score_part(0, 0, 0, kSteps);
+                    mma_commit(lead, s_bar);
+                }
+                if (n1 > 0) {
+                    score_part(1, 0, 0, kSteps);
+                    mma_commit(lead, s_bar + 8);
+                }
+                mma_commit(lead, empty0);
+                ok = wait(full0 + 8, 0);
             }
-            if (!ok) record_status(p.status, KVI_ERR_TIMEOUT);
+            // slots alternate K and V: V of tile j is slot 2 j + 1, K of j + 1 the next
+            uint32_t vs = 1, ph = 0;
+#pragma unroll 1
+            for (int j = 0; j < n && ok; ++j) {
+                const bool wraps = vs + 1 == Sm::kStages;
+                const uint32_t ks = wraps ? 0 : vs + 1, vn = ks + 1, nph = wraps ? ph ^ 1u : ph;
+                ok = step(j, vs, vn, ks, nph, nph);
+                vs = vn;
+                ph = nph;
+            }
+            if (!ok && lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
             // whatever ended the loop, no product may still run when tensor
             // memory is given back
-            mma_commit(smem_u32(&tl.drained));
-            if (!mbar_wait_brisk(smem_u32(&tl.drained), 0, kTileWaitNs)) record_status(p.status, KVI_ERR_TIMEOUT);
+            mma_commit(lead, smem_u32(&tl.drained));
+            if (!wait(smem_u32(&tl.drained), 0) && lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
         }
         __syncwarp();
     }
@@ -486,7 +534,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoft));
         // ----------------------------------------------------------- softmax
         const int i = warp >> 2, row = tid & (kM - 1);
-        const int my = n_tiles[i];
+        const int my = i ? n_tiles[1] : n_tiles[0];
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;  // this warp's part of tensor memory
         const uint32_t t_s = tmem + lanes + i * kM, t_o = tmem + lanes + kColO + i * DP;
         const int token = tok0 + i * per + row / p.G;
