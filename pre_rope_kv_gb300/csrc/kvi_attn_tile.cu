@@ -224,36 +224,44 @@ __device__ __forceinline__ void box4(uint32_t dst, const CUtensorMap *map, int x
         : "memory");
 }
 
-// V of one tile before the products: thread `kr` of 128 looks over key kr's
-// row.  Values of keys that are not there become zero; an infinity or NaN too,
-// noted with its key for the rows that see it.
+// The warp that copies V looks over a tile of it before the products.  An infinity or NaN
+// becomes zero, noted with its key for the rows that see it (a key past the end
+// is seen by none).  The rule is that there is none: one maximum a word.
 template <int DP>
-__device__ __forceinline__ void fix_values(uint8_t *v, int kr, int key, int ctx, TileTail<DP> &tl)
+__device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> &tl)
 {
+    constexpr int kChunks = TileSmem<DP>::kTile / 16;
+    const int lane = threadIdx.x & 31;
+    const uint4 *at = reinterpret_cast<const uint4 *>(v);
+    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < DP / 8; ++i) {  // 16-byte chunks of 8 channels
-        uint4 *at = reinterpret_cast<uint4 *>(v + (i >> 3) * kHalf + kr * 128 + (((i & 7) ^ (kr & 7)) << 4));
-        if (key >= ctx) {
-            *at = make_uint4(0, 0, 0, 0);
-            continue;
-        }
-        const uint4 x = *at;
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        uint32_t any = 0;
+    for (int i = lane; i < kChunks; i += 32) {
+        const uint4 x = at[i];
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) any |= ((w[j] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-        if (any) {
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t b = (w[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                if ((b & 0x7f80u) != 0x7f80u) continue;
-                atomicMin(&tl.first[b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2][8 * i + e], key);
-                w[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-            }
-            tl.odd = 1;
-            *at = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 4; ++j) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j])));
+    }
+    const uint32_t bits = *reinterpret_cast<const uint32_t *>(&top);
+    const bool odd = (bits & 0x7f80u) == 0x7f80u || (bits & 0x7f800000u) == 0x7f800000u;
+    if (!__any_sync(0xffffffffu, odd)) return;
+    if (!tl.odd)
+        for (int i = lane; i < 3 * DP; i += 32) (&tl.first[0][0])[i] = INT32_MAX;
+    __syncwarp();
+    if (lane == 0) tl.odd = 1;
+    uint16_t *e = reinterpret_cast<uint16_t *>(v);
+#pragma unroll 1
+    for (int i = lane; odd && i < kChunks; i += 32) {
+        const int half = i / (kHalf / 16), row = (i % (kHalf / 16)) / 8, chunk = (i & 7) ^ (row & 7);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            const uint32_t b = e[8 * i + k];
+            if ((b & 0x7f80u) != 0x7f80u) continue;
+            atomicMin(&tl.first[b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2][64 * half + 8 * chunk + k], key0 + row);
+            e[8 * i + k] = 0;
         }
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
 }
 
 // The largest of 64 scores
@@ -332,29 +340,67 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int sure = seen0 + tok0 + 1;  // keys below it are seen by every row
     const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
 
-    if (tid == 0) {
-        mbar_init(smem_u32(&tl.q_full), 1);
-        for (int s = 0; s < Sm::kStages; ++s) {
-            mbar_init(smem_u32(&tl.full[s]), 1);
-            mbar_init(smem_u32(&tl.empty[s]), 1);
+    // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
+    // two halves of 16 boxes.  A piece past the end, or of a block that is not
+    // there, reads as zeros from past a page's last token.
+    const int boxes = kM / box_keys, half = lane / boxes, box = lane % boxes;
+    // (Its place is looked up before its stage is waited for.)
+    int at_token = 0, at_block = 0;
+    auto look_up = [&](int j) {
+        const int key = from + j * kM + box * box_keys;
+        const int block = key < rq.ctx ? __ldg(table + key / p.B) : -1;
+        const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
+        at_token = there ? key % p.B : p.B;
+        at_block = there ? block : 0;
+    };
+    auto copy_tile = [&](int plane, uint32_t stage) {
+        const uint32_t bar = smem_u32(&tl.full[stage]);
+        if (lane == 0) mbar_expect_tx(bar, Sm::kTile);
+        __syncwarp();
+        if (half < Sm::kHalves)
+            box4(smem_u32(base + Sm::kRing) + stage * Sm::kTile + half * kHalf + box * box_keys * 128, &tm_kv, 64 * half, h,
+                 at_token, plane * p.num_blocks + at_block, bar);
+    };
+    if (warp == kCopyK) {
+        // the first copies go out while tensor memory is allocated
+        if (lane == 0) {
+            mbar_init(smem_u32(&tl.q_full), 1);
+            for (int s = 0; s < Sm::kStages; ++s) {
+                mbar_init(smem_u32(&tl.full[s]), 1);
+                mbar_init(smem_u32(&tl.empty[s]), 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_u32(&tl.s_full[i]), 1);
+                mbar_init(smem_u32(&tl.p_full[i][0]), 4);
+                mbar_init(smem_u32(&tl.p_full[i][1]), 4);
+                mbar_init(smem_u32(&tl.o_full[i]), 1);
+            }
+            mbar_init(smem_u32(&tl.v_fixed), 1);
+            mbar_init(smem_u32(&tl.drained), 1);
+            tl.odd = 0;
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&tl.s_full[i]), 1);
-            mbar_init(smem_u32(&tl.p_full[i][0]), 4);
-            mbar_init(smem_u32(&tl.p_full[i][1]), 4);
-            mbar_init(smem_u32(&tl.o_full[i]), 1);
+        __syncwarp();
+        if (n > 0) {
+            // rows past a tile's tokens keep what the memory held: their scores are
+            // computed and not used
+            const uint32_t bar = smem_u32(&tl.q_full);
+            const int tiles = n_tiles[1] > 0 ? 2 : 1;
+            if (lane == 0) mbar_expect_tx(bar, tiles * Sm::kHalves * per * p.G * 128);
+            __syncwarp();
+            if (lane < tiles * Sm::kHalves)
+                box3(smem_u32(base + Sm::kQ) + (lane / Sm::kHalves) * Sm::kTile + (lane % Sm::kHalves) * kHalf, &tm_q,
+                     64 * (lane % Sm::kHalves), h * p.G, rq.q0 + tok0 + (lane / Sm::kHalves) * per, bar);
+            look_up(0);
+            copy_tile(0, 0);
+            copy_tile(1, 1);
         }
-        mbar_init(smem_u32(&tl.v_fixed), kM);
-        mbar_init(smem_u32(&tl.drained), 1);
-        tl.odd = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     if (warp == kMmaWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tl.tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    for (int i = tid; i < 3 * DP; i += kTileThreads) (&tl.first[0][0])[i] = INT32_MAX;
     bool lost = false;  // a block of this range lies outside the pool
     for (int b = from / p.B + tid; (int64_t)b * p.B < min(rq.ctx, from + n * kM); b += kTileThreads)
         lost |= (uint32_t)table[b] >= (uint32_t)p.num_blocks;
@@ -370,33 +416,34 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kCopyK || warp == kCopyV) {
         // ------------------------------------------------------------ copies
-        if (warp == kCopyK && lane < 2 && n > 0) {
-            const int t0 = tok0 + lane * per;
-            const uint32_t bar = smem_u32(&tl.q_full);
-            // rows past the tile's tokens keep what the memory held: their scores
-            // are computed and not used
-            if (lane == 0) mbar_expect_tx(bar, (n_tiles[1] > 0 ? 2 : 1) * Sm::kHalves * per * p.G * 128);
-            __syncwarp(3u);
-            if (lane == 0 || n_tiles[1] > 0)
-                for (int x = 0; x < Sm::kHalves; ++x)
-                    box3(smem_u32(base + Sm::kQ + lane * Sm::kTile + x * kHalf), &tm_q, 64 * x, h * p.G, rq.q0 + t0, bar);
-        }
-        __syncwarp();
-        // one warp copies K, one V; a box a lane: 32 lanes cover two halves of 16
+        // one warp copies K, one V, from the second tile on
         const int plane = warp == kCopyV ? 1 : 0;
-        const int boxes = kM / box_keys, half = lane / boxes, box = lane % boxes;
-        const uint32_t dst = smem_u32(base + Sm::kRing) + half * kHalf + box * box_keys * 128;
-        uint32_t stage = plane, phase = 1;  // an unused stage is empty
+        uint32_t stage = plane + 2, phase = 1;  // an unused stage is empty
         bool ok = true;
-        int slots = 0;
-        for (int j = 0; j < n; ++j) {
-            const int key = from + j * kM + box * box_keys;
-            int block = key < rq.ctx ? table[key / p.B] : -1;
-            // a piece past the end, or of a block that is not there, reads as
-            // zeros from past a page's last token
-            const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
-            const int y = there ? key % p.B : p.B;
-            block = plane * p.num_blocks + (there ? block : 0);
+        int slots = n > 0 ? 1 : 0;
+        // V of the tiles that some row sees in part is looked over before the next
+        // V is asked for (it has been there for a while by then)
+        const int first_partly = sure > from ? (sure - from) / kM : 0;
+        auto look_over = [&](int j) {
+            if (plane == 0 || j < first_partly) return true;
+            const int slot = 2 * j + 1;
+            const bool got = mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                return false;
+            }
+            check_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl);
+            if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed));
+            return true;
+        };
+        for (int j = 1; j < n; ++j) {
+            look_up(j);
+            ok = look_over(j - 1);
+            if (!ok) break;
+            if (stage >= Sm::kStages) {
+                stage = plane;
+                phase ^= 1u;
+            }
             bool got = true;
             if (lane == 0) got = mbar_wait_brisk(smem_u32(&tl.empty[stage]), phase, kTileWaitNs);
             if (!__shfl_sync(0xffffffffu, got ? 1 : 0, 0)) {
@@ -404,17 +451,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 ok = false;
                 break;
             }
-            const uint32_t bar = smem_u32(&tl.full[stage]);
-            if (lane == 0) mbar_expect_tx(bar, Sm::kTile);
-            __syncwarp();
-            if (half < Sm::kHalves) box4(dst + stage * Sm::kTile, &tm_kv, 64 * half, h, y, block, bar);
+            copy_tile(plane, stage);
             ++slots;
             stage += 2;
-            if (stage >= Sm::kStages) {
-                stage = plane;
-                phase ^= 1u;
-            }
         }
+        if (ok && n > 0) ok = look_over(n - 1);
         // no copy may still be writing when the block ends
         if (!ok) {
             constexpr int kOwn = Sm::kStages / 2;
@@ -424,6 +465,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             if (lane == 0 && plane == 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
         }
+        __syncwarp();
+        if (plane == 1) asm volatile("bar.arrive 1, 288;" ::: "memory");
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------- matrix products
         if (n > 0) {
@@ -546,12 +589,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int j = 0; j < my; ++j) {
             const int key0 = from + j * kM;
             const bool partly = key0 + kM > sure;
-            if (partly && i == (j < n_tiles[1] ? 1 : 0)) {
-                const int slot = 2 * j + 1;
-                ok = ok && mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
-                if (ok) fix_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, row, key0 + row, rq.ctx, tl);
-                mbar_arrive(smem_u32(&tl.v_fixed));
-            }
             ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
@@ -633,8 +670,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             sum += a + b;
             announce(tl.p_full[i][1]);
         }
-        // ---- the rows' results; both tiles' warps have looked over their values
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        // ---- the rows' results; the values have been looked over
+        asm volatile("bar.sync 1, 288;" ::: "memory");
         if (my > 0 && ok) {
             ok = mbar_wait_brisk(smem_u32(&tl.o_full[i]), 0, kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
@@ -648,41 +685,63 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
+            // A thread holds a row, and rows lie far apart, so the warp's 32 rows go
+            // through its quarter of the tile's Q (which nothing reads any more): row
+            // by row out of it, a store covers whole lines.  16-byte pieces: 8
+            // channels in bf16, or in two passes 4 in float32.
+            constexpr int kPieces = DP / 8, kRowsAt = 32 / kPieces;
+            uint4 *stage = reinterpret_cast<uint4 *>(base + Sm::kQ + i * Sm::kTile) + (warp & 3) * 32 * kPieces;
+            const uint64_t mine = reinterpret_cast<uint64_t>(
+                whole ? static_cast<void *>(p.out + tok * p.out_stride + (int64_t)head * p.D)
+                      : static_cast<void *>(p.po + (at * p.S + split) * p.D));
+            const uint32_t rows_there = __ballot_sync(0xffffffffu, real);
 #pragma unroll 1
-            for (int c = 0; c < DP; c += 32) {
-                __syncwarp();
-                float v[32];
-                if (my > 0) {
-                    tmem_load32(t_o + c, v);
-                    tmem_wait_ld(v);
-                } else {
+            for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
+                const int c0 = whole ? 0 : pass * (DP / 2), c1 = whole ? DP : c0 + DP / 2;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    float v[32];
+                    if (my > 0) {
+                        tmem_load32(t_o + c, v);
+                        tmem_wait_ld(v);
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                }
-                if (!real || c >= p.D) continue;
-                if (odd) {
-                    const float inf = __int_as_float(0x7f800000);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (tl.first[0][c + e] <= last) v[e] += inf;
-                        if (tl.first[1][c + e] <= last) v[e] -= inf;
-                        if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
                     }
-                }
-                if (whole) {
-                    __nv_bfloat16 *out = p.out + tok * p.out_stride + (int64_t)head * p.D + c;
+                    if (odd) {
+                        const float inf = __int_as_float(0x7f800000);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        if (c + e < p.D)
-                            *reinterpret_cast<uint4 *>(out + e) =
+                        for (int e = 0; e < 32; ++e) {
+                            if (tl.first[0][c + e] <= last) v[e] += inf;
+                            if (tl.first[1][c + e] <= last) v[e] -= inf;
+                            if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                        }
+                    }
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            stage[lane * kPieces + (((c + e) / 8) ^ (lane & 7))] =
                                 make_uint4(pack_bf16(v[e] * inv, v[e + 1] * inv), pack_bf16(v[e + 2] * inv, v[e + 3] * inv),
                                            pack_bf16(v[e + 4] * inv, v[e + 5] * inv), pack_bf16(v[e + 6] * inv, v[e + 7] * inv));
-                } else {
-                    float *out = p.po + (at * p.S + split) * p.D + c;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        if (c + e < p.D) *reinterpret_cast<float4 *>(out + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                        for (int e = 0; e < 32; e += 4)
+                            stage[lane * kPieces + (((c - c0 + e) / 4) ^ (lane & 7))] =
+                                make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                           __float_as_uint(v[e + 3]));
+                    }
+                    __syncwarp();
                 }
+                const int piece = lane % kPieces;
+                const bool in_row = whole ? 8 * piece < p.D : c0 + 4 * piece < p.D;
+#pragma unroll 4
+                for (int k = 0; k < 32; k += kRowsAt) {
+                    const int rr = k + lane / kPieces;
+                    const uint64_t to = __shfl_sync(0xffffffffu, mine, rr);
+                    if (((rows_there >> rr) & 1u) && in_row)
+                        reinterpret_cast<uint4 *>(to)[piece + pass * kPieces] = stage[rr * kPieces + (piece ^ (rr & 7))];
+                }
+                __syncwarp();
             }
             if (real) {
                 const float M = m * p.scale;
