@@ -65,7 +65,7 @@ struct PromptParams {
     const __nv_bfloat16 *q;
     int64_t q_stride;
     const int32_t *q_start;
-    int32_t total_q, max_q;
+    int32_t R, total_q, max_q;
     const int32_t *ctx_lens;
     int32_t max_ctx, max_blocks;
     const int32_t *block_tables;
@@ -76,7 +76,7 @@ struct PromptParams {
     __nv_bfloat16 *out;
     int64_t out_stride;
     float *lse;
-    int32_t chunks;             // row chunks per request and KV head
+    int32_t chunks;             // row chunks per KV head: of each request, or (tiles) of all
     int32_t S, span;
     float *po;
     float2 *ml;
@@ -84,9 +84,10 @@ struct PromptParams {
 };
 
 // The tensor-core form (kvi_attn_tile.cu): two tiles of 128 rows a block.
-// Tokens that a tile holds, and the launch (p.chunks = tile pairs).
+// Tokens that a tile holds, and the launch (p.chunks: no fewer than the tile
+// pairs of all requests together).
 inline int tile_tokens(int G) { return 128 / G; }
-cudaError_t launch_tiles(const PromptParams &p, int32_t R, cudaStream_t s);
+cudaError_t launch_tiles(const PromptParams &p, cudaStream_t s);
 
 // A tensor map of bf16 boxes with the 128-byte swizzle (rank <= 5; pitches in
 // bytes of the dimensions past the first); out-of-range elements read as 0.

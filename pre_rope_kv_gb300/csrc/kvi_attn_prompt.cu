@@ -352,9 +352,12 @@ struct PromptPlan {
     size_t ml, total;
 };
 
-// `splits` pieces of the keys are wanted, none below `least` keys
-void plan_split(PromptPlan &pl, const kvi_attention &a, int32_t total_q, int32_t max_ctx, int64_t splits, int least)
+// `splits` pieces of the keys are wanted, none below `least` keys, and none at
+// all up to `alone` keys, which cost no more than the join does (2 us).
+void plan_split(PromptPlan &pl, const kvi_attention &a, int32_t total_q, int32_t max_ctx, int64_t splits, int alone,
+                int least)
 {
+    if (max_ctx <= alone) splits = 1;
     int64_t span = (max_ctx + splits - 1) / splits;
     span = std::max<int64_t>(least, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
@@ -374,9 +377,10 @@ PromptPlan plan_rows(const kvi_attention &a, int32_t R, int32_t total_q, int32_t
     const int64_t rows = (int64_t)max_q * G;
     pl.nt = rows > 8 && pl.dp <= 128 ? 2 : 1;
     pl.chunks = std::max<int64_t>(1, (rows + 8 * pl.nt - 1) / (8 * pl.nt));
-    // blocks for four on every SM, none below 256 keys (four tiles a warp)
+    // blocks for four on every SM; short ones only where there are few (16 requests
+    // of one token, 512 keys: 14 us in pieces of 128, 12 us in pieces of 256)
     const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
-    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n), 256);
+    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n), 256, 2 * n > kPlanSms ? 256 : 128);
     return pl;
 }
 
@@ -385,28 +389,35 @@ PromptPlan plan_tiles(const kvi_attention &a, int32_t R, int32_t total_q, int32_
     PromptPlan pl{};
     pl.tiles = true;
     const int per = 2 * tile_tokens(a.q_heads / a.kv_heads);
-    pl.chunks = std::max<int64_t>(1, ((int64_t)max_q + per - 1) / per);
-    // a block for every SM, none below a tile of keys
-    const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
-    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 128);
+    // a request's last pair may be partly filled
+    pl.chunks = std::max<int64_t>(1, std::min((int64_t)R * ((max_q + (int64_t)per - 1) / per), total_q / per + (int64_t)R));
+    // a block for every SM
+    const int64_t n = (int64_t)a.kv_heads * pl.chunks;
+    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 384, 128);
     return pl;
 }
 
-// The tensor-core tiles want boxes of 8 tokens or more of a page, up to 128
-// channels, and pay once a request has more rows than the other form keeps in
-// a few blocks.
-constexpr int kRowsMost = 64;
-bool tiles_fit(const kvi_attention &a, int32_t max_q, int32_t num_blocks, int32_t block_size)
+// The tensor-core tiles want boxes of 8 tokens or more of a page and up to 128
+// channels.  They take a fixed time for a call, and then hardly more for 128
+// rows than for one; the other form pays by the row.  Measured, us, rows form
+// and tiles (R requests, rows per KV head, keys): 8 KV heads of 128 channels,
+// R = 1: 8 rows x 128 keys 6.4, 7.8, x 4096 11, 13; 16 rows x 128 keys 8.3, 7.8,
+// x 4096 14, 13; R = 16: 8 rows x 4096 keys 61, 54.  2 KV heads of 64 channels,
+// R = 16: 16 rows x 1024 keys 9.8, 11; 64 rows x 1024 keys 14, 12; few and short
+// enough for one wave of the rows form, R = 1: 256 rows x 256 keys 7.7, 9.6.
+bool tiles_fit(const kvi_attention &a, int32_t R, int32_t max_q, int32_t max_ctx, int32_t num_blocks, int32_t block_size)
 {
-    return a.head_dim <= 128 && block_size % 8 == 0 && num_blocks <= (1 << 29) &&
-           (int64_t)max_q * (a.q_heads / a.kv_heads) > kRowsMost;
+    if (a.head_dim > 128 || block_size % 8 || num_blocks > (1 << 29)) return false;
+    const int64_t rows = (int64_t)max_q * (a.q_heads / a.kv_heads);
+    if (a.head_dim > 64) return rows > 8;
+    return rows > 32 && (max_ctx > 256 || (int64_t)R * a.kv_heads * rows > 8192);
 }
 
 // Workspace for whichever form the cache's pages decide on.
 size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
 {
     size_t n = std::max<size_t>(256, plan_rows(a, R, total_q, max_q, max_ctx).total);
-    if (tiles_fit(a, max_q, 1, 8)) n = std::max(n, plan_tiles(a, R, total_q, max_q, max_ctx).total);
+    if (tiles_fit(a, R, max_q, max_ctx, 1, 8)) n = std::max(n, plan_tiles(a, R, total_q, max_q, max_ctx).total);
     return n;
 }
 
@@ -468,7 +479,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     if (reinterpret_cast<uintptr_t>(d_q) % 16 || reinterpret_cast<uintptr_t>(d_out) % 16 || q_row_stride % 8 ||
         out_row_stride % 8 || q_row_stride < wide || out_row_stride < wide)
         return arg_error("q and out rows must be 16-byte aligned, with strides of at least q_heads * head_dim elements");
-    const PromptPlan pl = tiles_fit(*a, max_q, cache->num_blocks, cache->block_size)
+    const PromptPlan pl = tiles_fit(*a, R, max_q, max_ctx, cache->num_blocks, cache->block_size)
                               ? plan_tiles(*a, R, total_q, max_q, max_ctx)
                               : plan_rows(*a, R, total_q, max_q, max_ctx);
     const size_t need = prompt_bytes(*a, R, total_q, max_q, max_ctx);
@@ -481,6 +492,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.q = static_cast<const __nv_bfloat16 *>(d_q);
     p.q_stride = q_row_stride;
     p.q_start = d_q_start;
+    p.R = R;
     p.total_q = total_q;
     p.max_q = max_q;
     p.ctx_lens = d_ctx_lens;
@@ -505,7 +517,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
     p.status = d_status;
     if (max_q == 0) return KVI_OK;  // no rows
-    st = cuda_status(pl.tiles ? launch_tiles(p, R, stream) : launch_rows(p, pl, R, stream), "kvi_attn_prompt");
+    st = cuda_status(pl.tiles ? launch_tiles(p, stream) : launch_rows(p, pl, R, stream), "kvi_attn_prompt");
     if (st != KVI_OK || pl.S == 1) return st;
     JoinParams j{};
     j.po = p.po;

@@ -306,23 +306,47 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     TileTail<DP> &tl = *reinterpret_cast<TileTail<DP> *>(base + Sm::kTail);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- the block's rows and keys (heaviest prompts' ends first)
-    const int split = blockIdx.x % p.S, h = (blockIdx.x / p.S) % p.H, pair = p.chunks - 1 - blockIdx.x / p.S / p.H;
-    const int r = blockIdx.y;
+    // ---- the block's rows and keys
+    const int split = blockIdx.x % p.S, h = (blockIdx.x / p.S) % p.H;
+    const int per = kM / p.G;  // tokens of a tile
     if (tid == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
     }
     pdl_wait();
     pdl_launch_dependents();
-    RequestSpan rq;
-    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
-        if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-        return;
+    // Blocks are for the tile pairs that there are, numbered request after request
+    // and from a request's end (its heaviest) to its start; a warp looks over 32
+    // requests at once.
+    int item = blockIdx.x / p.S / p.H, r = -1, pair = 0;
+    RequestSpan rq{0, 0, 0};
+    for (int r0 = 0; r0 < p.R; r0 += 32) {
+        RequestSpan c{0, 0, 0};
+        const bool asked = r0 + lane < p.R;
+        const bool good = asked && request_span(r0 + lane, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
+                                                p.max_blocks, p.B, c);
+        if (asked && !good && h == 0 && split == 0 && warp == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        const int pairs = good ? (c.n_q + 2 * per - 1) / (2 * per) : 0;
+        int sum = pairs;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += u;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, sum > item);
+        if (past) {
+            const int from_lane = __ffs((int)past) - 1;
+            pair = __shfl_sync(0xffffffffu, sum, from_lane) - 1 - item;
+            r = r0 + from_lane;
+            rq.q0 = __shfl_sync(0xffffffffu, c.q0, from_lane);
+            rq.n_q = __shfl_sync(0xffffffffu, c.n_q, from_lane);
+            rq.ctx = __shfl_sync(0xffffffffu, c.ctx, from_lane);
+            break;
+        }
+        item -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    const int per = kM / p.G;         // tokens of a tile
+    if (r < 0) return;
     const int tok0 = pair * 2 * per;  // the block's first token
-    if (tok0 >= rq.n_q) return;
     const int pieces = max(1, (rq.ctx + p.span - 1) / p.span);
     if (split >= pieces) return;
     const bool whole = pieces == 1;
@@ -763,7 +787,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 }  // namespace
 
 template <int DP>
-static cudaError_t run_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
+static cudaError_t run_tiles(const PromptParams &p, cudaStream_t s)
 {
     CUtensorMap tq, tkv;
     const uint32_t per = (uint32_t)tile_tokens(p.G);
@@ -785,13 +809,13 @@ static cudaError_t run_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
     static_assert(bytes <= 227 * 1024, "shared memory");
     e = smem_opt_in(tile_kernel<DP>, bytes);
     if (e != cudaSuccess) return e;
-    return launch_chained(tile_kernel<DP>, dim3((unsigned)(p.S * p.H * p.chunks), (unsigned)R), kTileThreads, bytes, s, tq,
+    return launch_chained(tile_kernel<DP>, dim3((unsigned)(p.S * p.H * p.chunks)), kTileThreads, bytes, s, tq,
                           tkv, p, box);
 }
 
-cudaError_t launch_tiles(const PromptParams &p, int32_t R, cudaStream_t s)
+cudaError_t launch_tiles(const PromptParams &p, cudaStream_t s)
 {
-    return p.D <= 64 ? run_tiles<64>(p, R, s) : run_tiles<128>(p, R, s);
+    return p.D <= 64 ? run_tiles<64>(p, s) : run_tiles<128>(p, s);
 }
 
 }  // namespace kvi
