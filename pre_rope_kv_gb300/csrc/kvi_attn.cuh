@@ -112,12 +112,12 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 // the next one begin (pdl_launch_dependents): what a launch costs is hidden
 // behind the work before it.
 template <typename P, typename... Args>
-inline cudaError_t launch_chained(void (*kernel)(P, Args...), dim3 grid, int threads, size_t smem, cudaStream_t s,
+inline cudaError_t launch_chained(void (*kernel)(P, Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                   const std::decay_t<P> &p, const std::decay_t<Args> &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
+    cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];

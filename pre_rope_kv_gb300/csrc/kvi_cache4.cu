@@ -32,10 +32,13 @@ namespace {
 // 1/2 is either a half-integer exactly or at least 2^-10 from one: with x =
 // X 2^a, step = S 2^b (128 <= S < 256) and 2 X 2^a - h S 2^b != 0 for an odd h,
 // that difference is at least 2^(b - 1), and divided by 2 S 2^b at least 2^-10.
-// x * (1 / step) in float32 is off by less than 2^-20 here; rounded to
-// multiples of 2^-12 it is the half-integer again where the quotient is
-// one, and on the same side as the quotient everywhere else.  Steps too small
-// for their reciprocal take the division.
+// x * (1 / step) in float32 is off by less than 2^-19 here; rounded to
+// multiples of 2^-12 (by adding 3072) it is the half-integer again where the
+// quotient is one, and on the same side as the quotient everywhere else.  The
+// integer then falls out of a second addition, of a number with a last place
+// of 1.  Likewise max / 7 is max * (1 / 7) rounded to bf16: 7 times the middle of
+// two neighbouring bf16 numbers is at least 2^-12 of itself from any bf16 number.
+// Steps too small for their reciprocal take a division.
 
 struct RowParams {
     const __nv_bfloat16 *k_in, *v_in;
@@ -45,7 +48,6 @@ struct RowParams {
     int64_t T, n_slots;
     int32_t H, D;
     int32_t lanes;               // H * D / 8: threads of a pair of rows
-    int32_t pairs;               // pairs of rows per block (0: a pair takes several blocks)
     Page4 page;
     uint8_t *pool;
     int32_t *status;
@@ -76,30 +78,34 @@ __device__ __forceinline__ int64_t v_step_at(const Page4 &pg, int off, int g)
 __device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t &step)
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-    // |x| as bf16 bits: their order is that of the values, infinities and
-    // NaN at the top
-    uint32_t top = 0;
+    // the largest |x| of both halves of the words; infinities and NaN win
+    __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[0]));
 #pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(top, max(w[j] & 0x7fffu, (w[j] >> 16) & 0x7fffu));
+    for (int j = 1; j < 4; ++j) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j])));
+    const uint32_t both = *reinterpret_cast<const uint32_t *>(&m);
+    uint32_t top = max(both & 0x7fffu, (both >> 16) & 0x7fffu);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     if (top >= 0x7f80u) {  // not finite: the whole group reads back as NaN
         step = 0x7fff;
         return 0x88888888u;
     }
-    const __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top << 16), 7.0f));
+    const __nv_bfloat16 sb = __float2bfloat16_rn(__fmul_rn(__uint_as_float(top << 16), 1.0f / 7.0f));
     step = __bfloat16_as_ushort(sb);
     const float sf = __bfloat162float(sb);
     uint32_t c = 0;
     if (sf >= 1.1754944e-38f) {  // 1 / step is finite; |x / step| < 7.03
-        const float inv = __frcp_rn(sf);
+        float inv;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(sf));
+        // the bits of 12582920 + q, 0x4b400000 + 8 + q: summed up with weights
+        // 16^n, and what is not codes taken off at the end
 #pragma unroll
         for (int n = 7; n >= 0; --n) {
             const float x = n & 1 ? bf16_hi(w[n >> 1]) : bf16_lo(w[n >> 1]);
-            const float q = __fadd_rn(__fadd_rn(__fmul_rn(x, inv), 3072.f), -3072.f);  // multiples of 2^-12
-            // the integer in the low bits, plus 8
-            c = (c << 4) | (__float_as_uint(__fadd_rn(q, 12582920.f)) & 15u);
+            const float q = __fadd_rn(__fmaf_rn(x, inv, 3072.f), 12582920.f - 3072.f);
+            c = c * 16u + __float_as_uint(q);
         }
+        c -= 0x4b400000u * 0x11111111u;
     } else {
 #pragma unroll 1
         for (int n = 7; n >= 0; --n) {
@@ -135,28 +141,20 @@ struct RowWork {
     bool pair;         // slots 2 n and 2 n + 1 of one page
 };
 
+// (threadIdx.x: the lane of the pair, threadIdx.y: the pair of the block)
 __device__ __forceinline__ bool row_work(const RowParams &p, RowWork &o)
 {
-    const int tid = threadIdx.x;
-    int64_t i;
-    int lane;
-    if (p.pairs) {
-        const int at = tid / p.lanes;
-        lane = tid - at * p.lanes;
-        i = (int64_t)blockIdx.x * p.pairs + at;
-        if (at >= p.pairs) i = -1;
-    } else {
-        lane = blockIdx.y * kRowThreads + tid;
-        i = lane < p.lanes ? (int64_t)blockIdx.x : -1;
-    }
-    const int parts = p.D / 8;
-    o.h = lane / parts;
-    const int part = lane - o.h * parts;
-    o.g = part >> 2;
-    o.t = part & 3;
+    const uint32_t lane = blockIdx.y * blockDim.x + threadIdx.x;
+    const int64_t i = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    const bool in = lane < (uint32_t)p.lanes;
+    const uint32_t parts = (uint32_t)p.D / 8;
+    o.h = (int32_t)(lane / parts);
+    const uint32_t part = lane - (uint32_t)o.h * parts;
+    o.g = (int32_t)(part >> 2);
+    o.t = (int32_t)(part & 3);
     o.row = 2 * i - (p.slots[0] & 1);
     o.slot[0] = o.slot[1] = -1;
-    if (i >= 0) {
+    if (in) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t r = o.row + e;
@@ -169,18 +167,24 @@ __device__ __forceinline__ bool row_work(const RowParams &p, RowWork &o)
             }
         }
     }
+    o.pair = o.slot[0] >= 0 && !(o.slot[0] & 1) && o.slot[1] == o.slot[0] + 1;  // (B is even: one page)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
+        if (e == 1 && o.pair) {
+            o.page[1] = o.page[0];
+            o.off[1] = o.off[0] + 1;
+            continue;
+        }
         const int64_t s = max((int64_t)0, o.slot[e]);
         if (p.n_slots <= 0x7fffffff) {
-            o.page[e] = (int32_t)s / p.page.B;
-            o.off[e] = (int32_t)s % p.page.B;
+            const uint32_t page = (uint32_t)s / (uint32_t)p.page.B;
+            o.page[e] = page;
+            o.off[e] = (int32_t)((uint32_t)s - page * (uint32_t)p.page.B);
         } else {
             o.page[e] = s / p.page.B;
             o.off[e] = (int32_t)(s % p.page.B);
         }
     }
-    o.pair = o.slot[0] >= 0 && !(o.slot[0] & 1) && o.slot[1] == o.slot[0] + 1;  // (B is even: one page)
     return o.slot[0] >= 0 || o.slot[1] >= 0;
 }
 
@@ -605,15 +609,17 @@ kvi_status rows_params(RowParams &p, int32_t H, int32_t D, const kvi_paged_cache
     return KVI_OK;
 }
 
-// Pairs of rows on x (one more than half the rows: pairs may start at row -1),
-// the parts of a wide pair on y.
-dim3 row_blocks(RowParams &p)
+// A block's shape, and the grid: pairs of rows on x (one more than half the
+// rows, as pairs may start at row -1), the parts of a wide pair on y.
+void row_shape(RowParams &p, dim3 &grid, dim3 &block)
 {
-    p.lanes = p.H * (p.D / 8);
-    p.pairs = kRowThreads / p.lanes;
+    p.lanes = p.H * (p.D / 8);  // a multiple of 4: a group never leaves its warp
+    // whole warps: eight pairs together are one, or a pair is rounded up
+    const int x = p.lanes <= 32 ? p.lanes : std::min((p.lanes + 31) & ~31, kRowThreads);
+    const int y = p.lanes <= 32 ? (kRowThreads / x) & ~7 : kRowThreads / x;
     const int64_t pairs = p.T / 2 + 1;
-    if (p.pairs) return dim3((unsigned)((pairs + p.pairs - 1) / p.pairs));
-    return dim3((unsigned)pairs, (unsigned)((p.lanes + kRowThreads - 1) / kRowThreads));
+    block = dim3((unsigned)x, (unsigned)y);
+    grid = dim3((unsigned)((pairs + y - 1) / y), (unsigned)((p.lanes + x - 1) / x));
 }
 
 size_t evict_bytes(int32_t H, int32_t R, int32_t max_ctx, int32_t *most)
@@ -651,8 +657,9 @@ extern "C" kvi_status kvi_cache4_write(int32_t kv_heads, int32_t head_dim, const
     if (st != KVI_OK || T == 0) return st;
     p.k_in = static_cast<const __nv_bfloat16 *>(d_k);
     p.v_in = static_cast<const __nv_bfloat16 *>(d_v);
-    const dim3 grid = row_blocks(p);
-    return cuda_status(launch_chained(cache4_write_kernel, grid, kRowThreads, 0, stream, p), "kvi_cache4_write");
+    dim3 grid, block;
+    row_shape(p, grid, block);
+    return cuda_status(launch_chained(cache4_write_kernel, grid, block, 0, stream, p), "kvi_cache4_write");
 }
 
 extern "C" kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const kvi_paged_cache *cache, int32_t layer,
@@ -665,8 +672,9 @@ extern "C" kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const 
     if (st != KVI_OK || T == 0) return st;
     p.k_out = static_cast<__nv_bfloat16 *>(d_k);
     p.v_out = static_cast<__nv_bfloat16 *>(d_v);
-    const dim3 grid = row_blocks(p);
-    return cuda_status(launch_chained(cache4_read_kernel, grid, kRowThreads, 0, stream, p), "kvi_cache4_read");
+    dim3 grid, block;
+    row_shape(p, grid, block);
+    return cuda_status(launch_chained(cache4_read_kernel, grid, block, 0, stream, p), "kvi_cache4_read");
 }
 
 extern "C" size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int32_t max_ctx)
