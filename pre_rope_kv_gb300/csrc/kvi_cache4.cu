@@ -47,13 +47,15 @@ struct RowParams {
     const int64_t *slots;
     int64_t T, n_slots;
     int32_t H, D;
-    int32_t lanes;               // H * D / 8: threads of a pair of rows
+    int32_t heads_apart;         // a thread takes the heads h, h + heads_apart, ..
+    int32_t lanes;               // heads_apart * D / 8: threads of a pair of rows
     Page4 page;
     uint8_t *pool;
     int32_t *status;
 };
 
 constexpr int kRowThreads = 256;
+constexpr int kPlanSms4 = 152;
 
 // The 16-bit pieces of channels 32 g + 4 s .. + 3 of the token at `off`.
 __device__ __forceinline__ int64_t k_piece(const Page4 &pg, int off, int g, int s)
@@ -134,7 +136,7 @@ __device__ __forceinline__ uint4 values8(uint32_t codes, uint32_t step)
 // the first slot's parity, so that runs of consecutive slots pair up.
 struct RowWork {
     int64_t row;       // the first row (it or the second may lie outside [0, T))
-    int32_t h, g, t;   // head, group, 8-channel part of the group
+    int32_t h, g, t;   // first head, group, 8-channel part of the group
     int64_t slot[2];   // -1: nothing to do
     int64_t page[2];
     int32_t off[2];
@@ -188,45 +190,66 @@ __device__ __forceinline__ bool row_work(const RowParams &p, RowWork &o)
     return o.slot[0] >= 0 || o.slot[1] >= 0;
 }
 
+// A row's pieces inside a page: byte offsets of this thread's codes and steps.
+struct Pieces {
+    int32_t k, ks, v, vs;
+};
+__device__ __forceinline__ Pieces pieces_of(const Page4 &pg, int off, int g, int t)
+{
+    return Pieces{(int32_t)k_piece(pg, off, g, 2 * t), (int32_t)k_step_at(pg, off, g), (int32_t)v_piece(pg, off, g, 2 * t),
+                  (int32_t)v_step_at(pg, off, g)};
+}
+
 __global__ void __launch_bounds__(kRowThreads) cache4_write_kernel(const __grid_constant__ RowParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
     RowWork o;
     row_work(p, o);
-    const int64_t col = (int64_t)o.h * p.D + 32 * o.g + 8 * o.t;
-    uint4 k[2], v[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        k[e] = v[e] = make_uint4(0, 0, 0, 0);
-        if (o.slot[e] >= 0) {
-            k[e] = *reinterpret_cast<const uint4 *>(p.k_in + (o.row + e) * p.k_stride + col);
-            v[e] = *reinterpret_cast<const uint4 *>(p.v_in + (o.row + e) * p.v_stride + col);
-        }
-    }
-    uint32_t ks[2], kc[2], vs[2], vc[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        kc[e] = quantise8(k[e], ks[e]);
-        vc[e] = quantise8(v[e], vs[e]);
-    }
     const int64_t bytes = p.page.bytes();
+    const int64_t col = 32 * o.g + 8 * o.t;
+    const __nv_bfloat16 *k_src = p.k_in + o.row * p.k_stride + col, *v_src = p.v_in + o.row * p.v_stride + col;
+    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
+    uint8_t *pages[2] = {p.pool + o.page[0] * p.H * bytes, p.pool + o.page[1] * p.H * bytes};
+    const int v_next = 4 * p.page.groups();  // from a piece of V to the next four channels'
+    // (every lane stays in the loop: groups of four agree on their steps)
+    const int rounds = (p.H + p.heads_apart - 1) / p.heads_apart;
+#pragma unroll 1
+    for (int n = 0, h = o.h; n < rounds; ++n, h += p.heads_apart) {
+        const bool in = h < p.H;
+        uint4 k[2], v[2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (o.slot[e] < 0) continue;
-        uint8_t *page = p.pool + (o.page[e] * p.H + o.h) * bytes;
-        *reinterpret_cast<uint32_t *>(page + k_piece(p.page, o.off[e], o.g, 2 * o.t)) = kc[e];
-        if (o.t == 0) *reinterpret_cast<uint16_t *>(page + k_step_at(p.page, o.off[e], o.g)) = (uint16_t)ks[e];
-        if (o.pair) continue;
-        *reinterpret_cast<uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t)) = (uint16_t)vc[e];
-        *reinterpret_cast<uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t + 1)) = (uint16_t)(vc[e] >> 16);
-        if (o.t == 0) *reinterpret_cast<uint16_t *>(page + v_step_at(p.page, o.off[e], o.g)) = (uint16_t)vs[e];
-    }
-    if (o.pair) {
-        uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
-        *reinterpret_cast<uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t)) = __byte_perm(vc[0], vc[1], 0x5410);
-        *reinterpret_cast<uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t + 1)) = __byte_perm(vc[0], vc[1], 0x7632);
-        if (o.t == 0) *reinterpret_cast<uint32_t *>(page + v_step_at(p.page, o.off[0], o.g)) = vs[0] | (vs[1] << 16);
+        for (int e = 0; e < 2; ++e) {
+            k[e] = v[e] = make_uint4(0, 0, 0, 0);
+            if (in && o.slot[e] >= 0) {
+                k[e] = *reinterpret_cast<const uint4 *>(k_src + (int64_t)e * p.k_stride + h * p.D);
+                v[e] = *reinterpret_cast<const uint4 *>(v_src + (int64_t)e * p.v_stride + h * p.D);
+            }
+        }
+        uint32_t ks[2], kc[2], vs[2], vc[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            kc[e] = quantise8(k[e], ks[e]);
+            vc[e] = quantise8(v[e], vs[e]);
+        }
+        if (!in) continue;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (o.slot[e] < 0) continue;
+            uint8_t *page = pages[e] + h * bytes;
+            *reinterpret_cast<uint32_t *>(page + at[e].k) = kc[e];
+            if (o.t == 0) *reinterpret_cast<uint16_t *>(page + at[e].ks) = (uint16_t)ks[e];
+            if (o.pair) continue;
+            *reinterpret_cast<uint16_t *>(page + at[e].v) = (uint16_t)vc[e];
+            *reinterpret_cast<uint16_t *>(page + at[e].v + v_next) = (uint16_t)(vc[e] >> 16);
+            if (o.t == 0) *reinterpret_cast<uint16_t *>(page + at[e].vs) = (uint16_t)vs[e];
+        }
+        if (o.pair) {
+            uint8_t *page = pages[0] + h * bytes;
+            *reinterpret_cast<uint32_t *>(page + at[0].v) = __byte_perm(vc[0], vc[1], 0x5410);
+            *reinterpret_cast<uint32_t *>(page + at[0].v + v_next) = __byte_perm(vc[0], vc[1], 0x7632);
+            if (o.t == 0) *reinterpret_cast<uint32_t *>(page + at[0].vs) = vs[0] | (vs[1] << 16);
+        }
     }
 }
 
@@ -236,35 +259,43 @@ __global__ void __launch_bounds__(kRowThreads) cache4_read_kernel(const __grid_c
     pdl_launch_dependents();
     RowWork o;
     if (!row_work(p, o)) return;
-    const int64_t col = (int64_t)o.h * p.D + 32 * o.g + 8 * o.t, bytes = p.page.bytes();
-    uint32_t kc[2], ks[2], vc[2], vs[2];
-    if (o.pair) {
-        const uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
-        const uint32_t a = *reinterpret_cast<const uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t));
-        const uint32_t b = *reinterpret_cast<const uint32_t *>(page + v_piece(p.page, o.off[0], o.g, 2 * o.t + 1));
-        const uint32_t s = *reinterpret_cast<const uint32_t *>(page + v_step_at(p.page, o.off[0], o.g));
-        vc[0] = __byte_perm(a, b, 0x5410);
-        vc[1] = __byte_perm(a, b, 0x7632);
-        vs[0] = s & 0xffffu;
-        vs[1] = s >> 16;
-    }
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (o.slot[e] < 0) continue;
-        const uint8_t *page = p.pool + (o.page[e] * p.H + o.h) * bytes;
-        kc[e] = *reinterpret_cast<const uint32_t *>(page + k_piece(p.page, o.off[e], o.g, 2 * o.t));
-        ks[e] = *reinterpret_cast<const uint16_t *>(page + k_step_at(p.page, o.off[e], o.g));
-        if (!o.pair) {
-            vc[e] = *reinterpret_cast<const uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t)) |
-                    (uint32_t)*reinterpret_cast<const uint16_t *>(page + v_piece(p.page, o.off[e], o.g, 2 * o.t + 1)) << 16;
-            vs[e] = *reinterpret_cast<const uint16_t *>(page + v_step_at(p.page, o.off[e], o.g));
+    const int64_t bytes = p.page.bytes();
+    const int64_t col = 32 * o.g + 8 * o.t;
+    __nv_bfloat16 *k_dst = p.k_out + o.row * p.k_stride + col, *v_dst = p.v_out + o.row * p.v_stride + col;
+    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
+    const uint8_t *pages[2] = {p.pool + o.page[0] * p.H * bytes, p.pool + o.page[1] * p.H * bytes};
+    const int v_next = 4 * p.page.groups();
+#pragma unroll 2
+    for (int h = o.h; h < p.H; h += p.heads_apart) {
+        uint32_t kc[2], ks[2], vc[2], vs[2];
+        if (o.pair) {
+            const uint8_t *page = pages[0] + h * bytes;
+            const uint32_t a = *reinterpret_cast<const uint32_t *>(page + at[0].v);
+            const uint32_t b = *reinterpret_cast<const uint32_t *>(page + at[0].v + v_next);
+            const uint32_t s = *reinterpret_cast<const uint32_t *>(page + at[0].vs);
+            vc[0] = __byte_perm(a, b, 0x5410);
+            vc[1] = __byte_perm(a, b, 0x7632);
+            vs[0] = s & 0xffffu;
+            vs[1] = s >> 16;
         }
-    }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        if (o.slot[e] < 0) continue;
-        *reinterpret_cast<uint4 *>(p.k_out + (o.row + e) * p.k_stride + col) = values8(kc[e], ks[e]);
-        *reinterpret_cast<uint4 *>(p.v_out + (o.row + e) * p.v_stride + col) = values8(vc[e], vs[e]);
+        for (int e = 0; e < 2; ++e) {
+            if (o.slot[e] < 0) continue;
+            const uint8_t *page = pages[e] + h * bytes;
+            kc[e] = *reinterpret_cast<const uint32_t *>(page + at[e].k);
+            ks[e] = *reinterpret_cast<const uint16_t *>(page + at[e].ks);
+            if (!o.pair) {
+                vc[e] = *reinterpret_cast<const uint16_t *>(page + at[e].v) |
+                        (uint32_t)*reinterpret_cast<const uint16_t *>(page + at[e].v + v_next) << 16;
+                vs[e] = *reinterpret_cast<const uint16_t *>(page + at[e].vs);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            if (o.slot[e] < 0) continue;
+            *reinterpret_cast<uint4 *>(k_dst + (int64_t)e * p.k_stride + h * p.D) = values8(kc[e], ks[e]);
+            *reinterpret_cast<uint4 *>(v_dst + (int64_t)e * p.v_stride + h * p.D) = values8(vc[e], vs[e]);
+        }
     }
 }
 
@@ -613,7 +644,13 @@ kvi_status rows_params(RowParams &p, int32_t H, int32_t D, const kvi_paged_cache
 // rows, as pairs may start at row -1), the parts of a wide pair on y.
 void row_shape(RowParams &p, dim3 &grid, dim3 &block)
 {
-    p.lanes = p.H * (p.D / 8);  // a multiple of 4: a group never leaves its warp
+    // a head a thread while that keeps the threads below a wave of them, else
+    // four, which share a thread's looking up and addressing (stored and read back,
+    // 8 heads of 128 channels: 65 k rows 183 us with one head a thread, 145 us with
+    // four; 64 rows 5.7 us, 13 us)
+    const int64_t threads = (p.T / 2 + 1) * p.H * (p.D / 8);
+    p.heads_apart = threads <= (int64_t)kPlanSms4 * 2048 ? p.H : (p.H + 3) / 4;
+    p.lanes = p.heads_apart * (p.D / 8);  // a multiple of 4: a group never leaves its warp
     // whole warps: eight pairs together are one, or a pair is rounded up
     const int x = p.lanes <= 32 ? p.lanes : std::min((p.lanes + 31) & ~31, kRowThreads);
     const int y = p.lanes <= 32 ? (kRowThreads / x) & ~7 : kRowThreads / x;
