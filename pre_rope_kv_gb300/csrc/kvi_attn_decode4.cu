@@ -16,8 +16,11 @@
 //      not fit a bf16 operand).
 //   V: the step belongs to (key, group), and a key is summed over, so it is P
 //      that is scaled; P * step rounds to bf16, as any P on tensor cores does.
-//   A code c in the low nibble of a 16-bit half, or'ed with 0x4300, is the
-//      bf16 number 128 + c; 136 is subtracted exactly.
+//   A nibble c of a 16-bit half, or'ed with 0x4300, is the bf16 number 128 + c
+//      if it is the lowest; or'ed with 0x6400, the f16 number 1024 + c if it is
+//      the lowest and 1024 + 16 c if it is the next.  136, or 1032, or 64 + 8
+//      after a division by 16, is subtracted exactly.  K is taken in f16, which
+//      needs half the shifts; V in bf16, as P * step has no bound that fits f16.
 // A warp takes pairs of tiles of 16 keys in turn, from a ring of its own that
 // bulk copies fill ahead of it, with a softmax of its own; the warps of a block
 // join at the end, and blocks that share a request's keys in a second kernel.
@@ -41,6 +44,12 @@ namespace kvi {
 
 namespace {
 
+#ifndef KVI_WANT
+#define KVI_WANT 8
+#endif
+#ifndef KVI_OCC
+#define KVI_OCC 4
+#endif
 constexpr int kWarps4 = 4;
 constexpr int kStages4 = 2;  // pairs of tiles of 16 keys that a warp has in flight
 constexpr uint64_t kWait4Ns = 1000000000ull;
@@ -130,7 +139,7 @@ struct Smem4 {
 };
 
 template <int NG, int NT>
-__global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? 4 : NG * NT <= 6 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? KVI_OCC : NG * NT <= 6 ? 3 : 2)
 decode4_kernel(const __grid_constant__ Decode4Params p)
 {
     using Sm = Smem4<NG, NT>;
@@ -214,36 +223,54 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
         if (i < pairs) issue(i);
 
     // Q as B fragments: word (a, b) of group j is channels 32 j + 8 t + 2 a + b
-    // and + 4, the order of the codes' nibbles
+    // and + 4, the order of the codes' nibbles.  In f16, each head scaled by a power
+    // of two that brings its largest element to 2^13: f16 keeps three more bits
+    // than bf16 has, and what it loses of elements below 2^-27 of the largest is
+    // nothing beside float32 sums.  The scale of the scores takes it back.
     uint32_t qf[NT][2 * NG][2];
+    float scale[NT][2];  // of columns (heads) 2 t and 2 t + 1
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         const int head = c0 + 8 * nt + g;
         const __nv_bfloat16 *q = p.q + (int64_t)r * p.q_stride + ((int64_t)h * p.G + head) * D + 8 * t;
+        uint4 v[NG];
+        uint32_t top = 0;  // the largest |q| as bf16 bits
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (head < p.G) v = __ldg(reinterpret_cast<const uint4 *>(q + 32 * j));
-            // v = channels (0,1) (2,3) (4,5) (6,7)
-            qf[nt][2 * j][0] = __byte_perm(v.x, v.z, 0x5410);      // 0, 4
-            qf[nt][2 * j][1] = __byte_perm(v.x, v.z, 0x7632);      // 1, 5
-            qf[nt][2 * j + 1][0] = __byte_perm(v.y, v.w, 0x5410);  // 2, 6
-            qf[nt][2 * j + 1][1] = __byte_perm(v.y, v.w, 0x7632);  // 3, 7
+            v[j] = make_uint4(0, 0, 0, 0);
+            if (head < p.G) v[j] = __ldg(reinterpret_cast<const uint4 *>(q + 32 * j));
+            const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
         }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^(13 - e) and 2^(e - 13) of a largest element in [2^e, 2^(e + 1)); e is
+        // kept where both are normal numbers (an infinity or NaN stays one)
+        const int e = min(max((int)(top >> 7) - 127, -100), 100);
+        const float up = __int_as_float((127 + 13 - e) << 23), down = __int_as_float((127 - 13 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            // v = channels (0,1) (2,3) (4,5) (6,7)
+            qf[nt][2 * j][0] = pack_f16(bf16_lo(v[j].x) * up, bf16_lo(v[j].z) * up);      // 0, 4
+            qf[nt][2 * j][1] = pack_f16(bf16_hi(v[j].x) * up, bf16_hi(v[j].z) * up);      // 1, 5
+            qf[nt][2 * j + 1][0] = pack_f16(bf16_lo(v[j].y) * up, bf16_lo(v[j].w) * up);  // 2, 6
+            qf[nt][2 * j + 1][1] = pack_f16(bf16_hi(v[j].y) * up, bf16_hi(v[j].w) * up);  // 3, 7
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) scale[nt][c] = p.scale * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
     }
     float o[NT][2 * NG][4];
-    // per column (head): the reference m in the scores' own units, the score
-    // that moves it, m as the exponent's offset (0 while nothing is seen), and
-    // this lane's share of the sum
-    float m[NT][2], limit[NT][2], ref[NT][2], l[NT][2];
-    const float lazy = kLazy / p.scale;
+    // per column (head): the score that moves the reference (-inf while there is
+    // none), the reference as an exponent, and this lane's share of the sum
+    float limit[NT][2], ref[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int i = 0; i < 2 * NG; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[nt][i][j] = 0.f;
-        m[nt][0] = m[nt][1] = limit[nt][0] = limit[nt][1] = neg_inf();
+        limit[nt][0] = limit[nt][1] = neg_inf();
         ref[nt][0] = ref[nt][1] = l[nt][0] = l[nt][1] = 0.f;
     }
 
@@ -277,14 +304,14 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
                 float sum[NT][4];
 #pragma unroll
                 for (int a = 0; a < 2; ++a) {
-                    const uint32_t a0 = codes_bf16x2(kc[0][j] >> (8 * a)), a1 = codes_bf16x2(kc[1][j] >> (8 * a));
-                    const uint32_t a2 = codes_bf16x2(kc[0][j] >> (8 * a + 4)), a3 = codes_bf16x2(kc[1][j] >> (8 * a + 4));
+                    const uint32_t x = kc[0][j] >> (8 * a), y = kc[1][j] >> (8 * a);
+                    const uint32_t a0 = codes_f16x2(x), a1 = codes_f16x2(y), a2 = codes_f16x2_high(x), a3 = codes_f16x2_high(y);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         if (a == 0)
-                            mma16816_first(sum[nt], a0, a1, a2, a3, qf[nt][2 * j][0], qf[nt][2 * j][1]);
+                            mma16816_f16_first(sum[nt], a0, a1, a2, a3, qf[nt][2 * j][0], qf[nt][2 * j][1]);
                         else
-                            mma16816(sum[nt], a0, a1, a2, a3, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
+                            mma16816_f16(sum[nt], a0, a1, a2, a3, qf[nt][2 * j + 1][0], qf[nt][2 * j + 1][1]);
                     }
                 }
 #pragma unroll
@@ -318,10 +345,10 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
                     float *sc = p.scores + (((int64_t)r * p.H + h) * p.max_ctx + key) * p.score_stride + head;
                     if (head < p.score_stride) {
                         if (key < to)
-                            *reinterpret_cast<float2 *>(sc) = make_float2(s[f][nt][0] * p.scale, s[f][nt][1] * p.scale);
+                            *reinterpret_cast<float2 *>(sc) = make_float2(s[f][nt][0] * scale[nt][0], s[f][nt][1] * scale[nt][1]);
                         if (key + 8 < to)
                             *reinterpret_cast<float2 *>(sc + 8 * p.score_stride) =
-                                make_float2(s[f][nt][2] * p.scale, s[f][nt][3] * p.scale);
+                                make_float2(s[f][nt][2] * scale[nt][0], s[f][nt][3] * scale[nt][1]);
                     }
                 }
         }
@@ -335,10 +362,10 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
                     for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
                     // each column goes by its own scores alone
                     if (!(top > limit[nt][c])) continue;
-                    const float f = exp2_fast((m[nt][c] - top) * p.scale);
-                    m[nt][c] = top;
-                    limit[nt][c] = top + lazy;
-                    ref[nt][c] = top * p.scale;
+                    const float to = top * scale[nt][c];
+                    const float f = limit[nt][c] == neg_inf() ? 0.f : exp2_fast(ref[nt][c] - to);
+                    limit[nt][c] = top + kLazy / scale[nt][c];
+                    ref[nt][c] = to;
                     l[nt][c] *= f;
 #pragma unroll
                     for (int i = 0; i < 2 * NG; ++i) {
@@ -354,10 +381,10 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
         for (int f = 0; f < 2; ++f)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float p0 = exp2_fast(fmaf(s[f][nt][0], p.scale, -ref[nt][0]));
-                const float p1 = exp2_fast(fmaf(s[f][nt][1], p.scale, -ref[nt][1]));
-                const float p2 = exp2_fast(fmaf(s[f][nt][2], p.scale, -ref[nt][0]));
-                const float p3 = exp2_fast(fmaf(s[f][nt][3], p.scale, -ref[nt][1]));
+                const float p0 = exp2_fast(fmaf(s[f][nt][0], scale[nt][0], -ref[nt][0]));
+                const float p1 = exp2_fast(fmaf(s[f][nt][1], scale[nt][1], -ref[nt][1]));
+                const float p2 = exp2_fast(fmaf(s[f][nt][2], scale[nt][0], -ref[nt][0]));
+                const float p3 = exp2_fast(fmaf(s[f][nt][3], scale[nt][1], -ref[nt][1]));
                 l[nt][0] += p0 + p2;
                 l[nt][1] += p1 + p3;
                 const uint32_t h0 = pack_bf16(p0, p1), h1 = pack_bf16(p2, p3);
@@ -423,10 +450,6 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     float *s_o = reinterpret_cast<float *>(smem);
     constexpr int kO = D + 4;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) m[nt][0] *= p.scale, m[nt][1] *= p.scale;
-
-    // ---- the block's warps join
-#pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
@@ -434,7 +457,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
             for (int off = 4; off < 32; off <<= 1) l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], off);
             const int n = 8 * nt + 2 * t + c;
             if (g == 0) {
-                s_m[warp][n] = m[nt][c];
+                s_m[warp][n] = limit[nt][c] == neg_inf() ? neg_inf() : ref[nt][c];
                 s_l[warp][n] = l[nt][c];
             }
 #pragma unroll
@@ -580,7 +603,7 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     // enough blocks for four on every SM, twice, but none below 128 keys (a pair
     // of tiles a warp)
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
-    const int64_t want = std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
+    const int64_t want = std::max<int64_t>(1, (KVI_WANT * kPlanSms + rows - 1) / rows);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
