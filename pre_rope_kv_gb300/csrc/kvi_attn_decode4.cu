@@ -44,12 +44,6 @@ namespace kvi {
 
 namespace {
 
-#ifndef KVI_WANT
-#define KVI_WANT 8
-#endif
-#ifndef KVI_OCC
-#define KVI_OCC 4
-#endif
 constexpr int kWarps4 = 4;
 constexpr int kStages4 = 2;  // pairs of tiles of 16 keys that a warp has in flight
 constexpr uint64_t kWait4Ns = 1000000000ull;
@@ -139,7 +133,7 @@ struct Smem4 {
 };
 
 template <int NG, int NT>
-__global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? KVI_OCC : NG * NT <= 6 ? 3 : 2)
+__global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? 4 : NG * NT <= 6 ? 3 : 2)
 decode4_kernel(const __grid_constant__ Decode4Params p)
 {
     using Sm = Smem4<NG, NT>;
@@ -509,7 +503,7 @@ struct WeightParams {
     int64_t stride;
 };
 
-constexpr int kKeysThread = 2;
+constexpr int kKeysThread = 4;
 constexpr int kKeysBlock = kKeysThread * kJoinWarps * 32;
 
 // After the attention, per request: blocks that join its pieces' outputs, and
@@ -603,7 +597,7 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     // enough blocks for four on every SM, twice, but none below 128 keys (a pair
     // of tiles a warp)
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
-    const int64_t want = std::max<int64_t>(1, (KVI_WANT * kPlanSms + rows - 1) / rows);
+    const int64_t want = std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
