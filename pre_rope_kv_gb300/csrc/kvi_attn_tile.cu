@@ -64,7 +64,7 @@ struct TileTail {
     uint64_t q_full;
     uint64_t full[TileSmem<DP>::kStages], empty[TileSmem<DP>::kStages];
     uint64_t s_full[2], p_full[2][2], o_full[2];  // p: P's first and second 64 keys
-    uint64_t v_fixed;
+    uint64_t v_fixed[TileSmem<DP>::kStages / 2];  // of V's stages
     uint64_t drained;
     uint32_t tmem;
     int32_t odd;            // `first` holds something
@@ -399,7 +399,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 mbar_init(smem_u32(&tl.p_full[i][1]), 4);
                 mbar_init(smem_u32(&tl.o_full[i]), 1);
             }
-            mbar_init(smem_u32(&tl.v_fixed), 1);
+            for (int s = 0; s < Sm::kStages / 2; ++s) mbar_init(smem_u32(&tl.v_fixed[s]), 1);
             mbar_init(smem_u32(&tl.drained), 1);
             tl.odd = 0;
             asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -450,14 +450,14 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const int first_partly = sure > from ? (sure - from) / kM : 0;
         auto look_over = [&](int j) {
             if (plane == 0 || j < first_partly) return true;
-            const int slot = 2 * j + 1;
+            const int slot = 2 * j + 1;  // (V's stages are the odd ones)
             const bool got = mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 return false;
             }
             check_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl);
-            if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed));
+            if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
             return true;
         };
         for (int j = 1; j < n; ++j) {
@@ -504,7 +504,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const uint32_t q_lo = desc_lo(smem_u32(base + Sm::kQ)), ring_lo = desc_lo(smem_u32(base + Sm::kRing));
             const uint32_t full0 = smem_u32(&tl.full[0]), empty0 = smem_u32(&tl.empty[0]);
             const uint32_t s_bar = smem_u32(&tl.s_full[0]), p_bar = smem_u32(&tl.p_full[0][0]);
-            const uint32_t o_bar = smem_u32(&tl.o_full[0]), fixed_bar = smem_u32(&tl.v_fixed);
+            const uint32_t o_bar = smem_u32(&tl.o_full[0]), fixed_bar = smem_u32(&tl.v_fixed[0]);
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 const bool got = __all_sync(0xffffffffu, mbar_wait_brisk(bar, parity, kTileWaitNs));
                 fence_after();
@@ -528,13 +528,16 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             };
             const int n0 = n_tiles[0], n1 = n_tiles[1];
             const int first_partly = sure > from ? (sure - from) / kM : 0;  // first tile that some row sees in part
-            uint32_t fixes = 0;
+            uint32_t fixes = 0;  // the phase of each v_fixed, a bit a stage
             // Tile j of the keys, V in stage `vs` and K of j + 1 in stage `ks`; V's
             // copy has been waited for.
             auto step = [&](int j, uint32_t vs, uint32_t vnext, uint32_t ks, uint32_t kph, uint32_t vnph) {
                 const uint32_t par = (uint32_t)(j & 1);
                 const bool more0 = j + 1 < n0, more1 = j + 1 < n1, more = more0 || more1;
-                if (j >= first_partly && !wait(fixed_bar, fixes++ & 1u)) return false;
+                if (j >= first_partly) {
+                    if (!wait(fixed_bar + 4 * (vs - 1), (fixes >> vs) & 1u)) return false;
+                    fixes ^= 1u << vs;
+                }
                 if (j < n0) {
                     if (!wait(p_bar, par)) return false;
                     values(0, vs, 0, j > 0);
