@@ -25,14 +25,14 @@
 // bulk copies fill ahead of it, with a softmax of its own; the warps of a block
 // join at the end, and blocks that share a request's keys in a second kernel.
 //
-// What bounds it is the issue of the decoding instructions, not the bytes: 14
-// integer operations and 8 subtractions per 16 codes, with the softmax, make about 400 warp
-// instructions per tile of 2304 bytes (D = 128), where HBM delivers a tile in
-// the time of 390.  Two tiles an iteration share the bookkeeping and run
-// independently of one another (16 requests x 28 k keys, D = 128, 8 KV heads:
-// 152 us one tile at a time, 140 us two; 12 warps an SM instead of 16: 148 us;
-// shifts as multiplications: 166 us; the offset of V's codes taken off by a
-// second matrix product instead of a subtraction: 155 us).
+// What bounds it is the issue of the decoding instructions, not the bytes: with
+// the softmax a tile of 2304 bytes (D = 128) takes nearly 400 warp instructions,
+// and HBM delivers a tile in the time of 390.  Measured at 16 requests x 28 k
+// keys, D = 128, 8 KV heads (0.53 GB): 129 us, 4.1 TB/s.  On the way there: one
+// tile an iteration 152 us, two, which share the bookkeeping and run independently
+// of one another, 140; P * step rounded once 132; K in f16 129.  Against the 140:
+// 12 warps an SM instead of 16 took 148, shifts as multiplications 166, the
+// offset of V's codes taken off by a second matrix product 155.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -595,9 +595,14 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     pl.nt = G > 8 && a.head_dim <= 128 ? 2 : 1;
     pl.chunks = (G + 8 * pl.nt - 1) / (8 * pl.nt);
     // enough blocks for four on every SM, twice, but none below 128 keys (a pair
-    // of tiles a warp)
+    // of tiles a warp).  One piece where the join would cost more than the pieces
+    // save: up to 384 keys (1 request x 8 KV heads: 6.1 us whole, 6.2 split; 512
+    // keys 7.1 and 6.3), and up to 1024 where the rows alone are a block for most
+    // SMs (16 x 8: 11.2 whole, 12.9 split; 64 x 8: 21.0 and 28.2; 2048 keys, 16 x
+    // 8: 18.8 and 17.0).
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
-    const int64_t want = std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
+    const int alone = rows >= 128 ? 1024 : 384;
+    const int64_t want = max_ctx <= alone ? 1 : std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
