@@ -325,6 +325,7 @@ struct EvictParams {
     int32_t *moves;          // [R][H]
     int32_t most;            // moves a row can need
     int32_t cap;             // ranks kept in shared memory
+    int32_t move_here;       // the rows are moved by the block that found them
     int32_t *status;
 };
 
@@ -367,6 +368,44 @@ __device__ __forceinline__ int warp_sum_before(int v, int *warp_sums)
     if (lane == 0) warp_sums[warp] = v;
     __syncthreads();
     return __reduce_add_sync(0xffffffffu, lane < warp ? warp_sums[lane] : 0);
+}
+
+// One moved row, by eight lanes (`lane`); 16-bit pieces, as two tokens share each
+// word of the V codes and steps.
+__device__ __forceinline__ void move_row(const EvictParams &p, const int32_t *table, int h, int dst, int src, int lane)
+{
+    const int G = p.page.groups();
+    const int db = table[dst / p.page.B], sb = table[src / p.page.B];
+    if (db < 0 || db >= p.num_blocks || sb < 0 || sb >= p.num_blocks) {
+        if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        return;
+    }
+    uint8_t *to = p.pool + ((int64_t)db * p.H + h) * p.page.bytes();
+    const uint8_t *fr = p.pool + ((int64_t)sb * p.H + h) * p.page.bytes();
+    const int d = dst % p.page.B, s = src % p.page.B;
+    constexpr int kMost = KVI_MAX_ATTN_HEAD_DIM / 32;
+    uint32_t k[kMost / 2];
+    uint16_t v[kMost], ks = 0, vs = 0;
+#pragma unroll
+    for (int g = 0; g < kMost; ++g) {
+        const int word = lane + 8 * g;  // of the row's 4 G words of K codes
+        if (g < kMost / 2 && word < 4 * G) k[g] = *reinterpret_cast<const uint32_t *>(fr + (int64_t)s * (p.page.D / 2) + 4 * word);
+        if (g < G) v[g] = *reinterpret_cast<const uint16_t *>(fr + v_piece(p.page, s, g, lane));
+    }
+    if (lane < G) {
+        ks = *reinterpret_cast<const uint16_t *>(fr + k_step_at(p.page, s, lane));
+        vs = *reinterpret_cast<const uint16_t *>(fr + v_step_at(p.page, s, lane));
+    }
+#pragma unroll
+    for (int g = 0; g < kMost; ++g) {
+        const int word = lane + 8 * g;
+        if (g < kMost / 2 && word < 4 * G) *reinterpret_cast<uint32_t *>(to + (int64_t)d * (p.page.D / 2) + 4 * word) = k[g];
+        if (g < G) *reinterpret_cast<uint16_t *>(to + v_piece(p.page, d, g, lane)) = v[g];
+    }
+    if (lane < G) {
+        *reinterpret_cast<uint16_t *>(to + k_step_at(p.page, d, lane)) = ks;
+        *reinterpret_cast<uint16_t *>(to + v_step_at(p.page, d, lane)) = vs;
+    }
 }
 
 // ITEMS > 0: a row of at most THREADS * ITEMS slots, each read once and kept in
@@ -534,54 +573,26 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
         w_out[to] = w[at];
         pos_out[to] = pos[at];
     }
-    if (tid == 0) p.moves[row] = n_holes;
+    if (p.move_here) {
+        const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+        for (int i = tid >> 3; i < n_holes; i += THREADS / 8) move_row(p, table, h, holes[i], tails[i], tid & 7);
+    } else if (tid == 0) {
+        p.moves[row] = n_holes;
+    }
 }
 
 // Eight lanes per moved row, so that enough rows are in flight to hide a
-// chain of three latencies (list, table, page); 16-bit pieces, as two tokens
-// share each word of the V codes and steps.
+// chain of three latencies (list, table, page).
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int64_t row = blockIdx.y;
-    const int h = (int)(row % p.H), r = (int)(row / p.H), lane = threadIdx.x & 7;
+    const int h = (int)(row % p.H), r = (int)(row / p.H);
     const int i = blockIdx.x * (kMoveThreads / 8) + (threadIdx.x >> 3);
     if (i >= p.moves[row]) return;
-    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
-    const int G = p.page.groups();
-    const int dst = p.holes[row * p.most + i], src = p.tails[row * p.most + i];
-    const int db = table[dst / p.page.B], sb = table[src / p.page.B];
-    if (db < 0 || db >= p.num_blocks || sb < 0 || sb >= p.num_blocks) {
-        if (lane == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-        return;
-    }
-    uint8_t *to = p.pool + ((int64_t)db * p.H + h) * p.page.bytes();
-    const uint8_t *fr = p.pool + ((int64_t)sb * p.H + h) * p.page.bytes();
-    const int d = dst % p.page.B, s = src % p.page.B;
-    constexpr int kMost = KVI_MAX_ATTN_HEAD_DIM / 32;
-    uint32_t k[kMost / 2];
-    uint16_t v[kMost], ks = 0, vs = 0;
-#pragma unroll
-    for (int g = 0; g < kMost; ++g) {
-        const int word = lane + 8 * g;  // of the row's 4 G words of K codes
-        if (g < kMost / 2 && word < 4 * G) k[g] = *reinterpret_cast<const uint32_t *>(fr + (int64_t)s * (p.page.D / 2) + 4 * word);
-        if (g < G) v[g] = *reinterpret_cast<const uint16_t *>(fr + v_piece(p.page, s, g, lane));
-    }
-    if (lane < G) {
-        ks = *reinterpret_cast<const uint16_t *>(fr + k_step_at(p.page, s, lane));
-        vs = *reinterpret_cast<const uint16_t *>(fr + v_step_at(p.page, s, lane));
-    }
-#pragma unroll
-    for (int g = 0; g < kMost; ++g) {
-        const int word = lane + 8 * g;
-        if (g < kMost / 2 && word < 4 * G) *reinterpret_cast<uint32_t *>(to + (int64_t)d * (p.page.D / 2) + 4 * word) = k[g];
-        if (g < G) *reinterpret_cast<uint16_t *>(to + v_piece(p.page, d, g, lane)) = v[g];
-    }
-    if (lane < G) {
-        *reinterpret_cast<uint16_t *>(to + k_step_at(p.page, d, lane)) = ks;
-        *reinterpret_cast<uint16_t *>(to + v_step_at(p.page, d, lane)) = vs;
-    }
+    move_row(p, p.block_tables + (int64_t)r * p.max_blocks, h, p.holes[row * p.most + i], p.tails[row * p.most + i],
+             threadIdx.x & 7);
 }
 
 // A block's threads and the slots a thread keeps, by the longest row.
@@ -770,10 +781,14 @@ extern "C" kvi_status kvi_cache4_evict(int32_t kv_heads, int32_t head_dim, int32
     p.tails = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + list);
     p.moves = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(d_ws) + 2 * list);
     p.status = d_status;
+    const int rows = std::min(budget, max_ctx - budget);  // a head moves at most so many
+    // Moved by the block that found them where those are few, or the blocks many:
+    // 8 KV heads, 1 request: 101 rows a head 7.5 us so, 7.9 by a second kernel;
+    // 577 rows 11.4 and 7.9; 16 requests, 800 rows: 12.4 and 15.4 (4: 11.8, 10.9).
+    p.move_here = rows <= 128 || (int64_t)R * kv_heads >= 128;
     cudaError_t e = launch_select(p, (unsigned)(R * kv_heads), stream);
     st = cuda_status(e, "kvi_cache4_evict");
-    if (st != KVI_OK || max_ctx <= budget) return st;  // nothing can move
-    const int rows = std::min(budget, max_ctx - budget);  // a head moves at most so many
+    if (st != KVI_OK || rows <= 0 || p.move_here) return st;
     const unsigned gx = (unsigned)((rows + kMoveThreads / 8 - 1) / (kMoveThreads / 8));
     const dim3 grid(gx, (unsigned)(R * kv_heads));
     e = launch_chained(evict_move_kernel, grid, kMoveThreads, 0, stream, p);
