@@ -623,6 +623,7 @@ class _Cache4:
         self._arr = (ctypes.c_void_p * len(ptrs))(*ptrs)
         self.struct = PagedCache(ctypes.cast(self._arr, ctypes.POINTER(ctypes.c_void_p)),
                                  len(ptrs), blocks, int(block_size))
+        self.ref = ctypes.byref(self.struct)
         self.layer_tensors = list(layer_tensors)
         self.kv_heads, self.head_dim = int(kv_heads), int(head_dim)
 
@@ -634,25 +635,42 @@ def cache4(layer_tensors, block_size: int, kv_heads: int, head_dim: int) -> _Cac
     return _Cache4(layer_tensors, block_size, kv_heads, head_dim)
 
 
-_bf16 = None  # torch.bfloat16, once a call has needed it
+_types = None  # (torch.bfloat16, torch.int32, torch.int64), once a call has needed them
+
+
+def _dtypes():
+    global _types
+    if _types is None:
+        import torch
+        _types = (torch.bfloat16, torch.int32, torch.int64)
+    return _types
 
 
 def _rows(t, heads: int, head_dim: int, name: str, n: int = -1):
     """Address and row stride of bf16 rows [n][heads][head_dim] (a row may be
     part of a wider one, e.g. of a fused projection); n < 0: any number."""
-    global _bf16
-    if _bf16 is None:
-        import torch
-        _bf16 = torch.bfloat16
     shape = t.shape
-    if t.dtype is not _bf16 or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
+    if t.dtype is not (_types or _dtypes())[0] or len(shape) != 3 or shape[1] != heads or shape[2] != head_dim:
         raise ValueError(f"{name} must be bfloat16 [rows][{heads}][{head_dim}]")
     if n >= 0 and shape[0] != n:
         raise ValueError(f"{name} has {shape[0]} rows, {n} are needed")
+    if t.is_contiguous():
+        return t.data_ptr(), heads * head_dim
     row, head, one = t.stride()
-    if shape[0] and (one != 1 or (heads > 1 and head != head_dim)):
+    if one != 1 or (heads > 1 and head != head_dim):
         raise ValueError(f"the rows of {name} must be contiguous")
     return t.data_ptr(), (row if shape[0] > 1 else heads * head_dim)
+
+
+def _ints(t, n: int, name: str, wide: bool = False):
+    """Address of at least n rows of integers, int32 or int64, in one piece
+    (more requests than the library takes are its own to refuse)."""
+    if t is None:
+        return None
+    if t.dtype is not (_types or _dtypes())[2 if wide else 1] or not t.is_contiguous() \
+            or t.shape[0] < n <= MAX_REQUESTS + 1:
+        raise ValueError(f"{name} must be contiguous int{64 if wide else 32}, at least {n} long")
+    return t.data_ptr()
 
 
 def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
@@ -666,14 +684,14 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
     [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
     int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
     c = cache.struct if hasattr(cache, "struct") else cache
-    total = q.shape[0]
+    total, R = q.shape[0], ctx_lens.shape[0]
     qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
     op, os_ = _rows(out, a.q_heads, a.head_dim, "out", total)
     _check(load_library().kvi_attn_prompt(
-        ctypes.byref(a), ctx_lens.shape[0], qp, qs, _ptr(q_start), total, int(max_q),
-        _ptr(ctx_lens), int(max_ctx), _ptr(block_tables), block_tables.shape[1], ctypes.byref(c),
-        int(layer), op, os_, _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _ptr(status),
-        _stream(stream)), "kvi_attn_prompt")
+        ctypes.byref(a), R, qp, qs, _ints(q_start, R + 1, "q_start"), total, max_q,
+        _ints(ctx_lens, R, "ctx_lens"), max_ctx, _ints(block_tables, R, "block_tables"),
+        block_tables.shape[1], ctypes.byref(c), layer, op, os_, _ptr(lse), _ptr(ws), ws.nbytes,
+        _ptr(status), _stream(stream)), "kvi_attn_prompt")
 
 
 def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:
@@ -687,8 +705,8 @@ def kvi_cache4_write(cache: _Cache4, layer: int, k, v, slots, status, stream=Non
     kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k", T)
     vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_write(
-        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), T, kp, ks, vp, vs,
-        _ptr(slots), _ptr(status), _stream(stream)), "kvi_cache4_write")
+        cache.kv_heads, cache.head_dim, cache.ref, layer, T, kp, ks, vp, vs,
+        _ints(slots, T, "slots", True), _ptr(status), _stream(stream)), "kvi_cache4_write")
 
 
 def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None) -> None:
@@ -697,8 +715,8 @@ def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None
     kp, ks = _rows(k, cache.kv_heads, cache.head_dim, "k", T)
     vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_read(
-        cache.kv_heads, cache.head_dim, ctypes.byref(cache.struct), int(layer), T,
-        _ptr(slots), kp, ks, vp, vs, _ptr(status), _stream(stream)), "kvi_cache4_read")
+        cache.kv_heads, cache.head_dim, cache.ref, layer, T,
+        _ints(slots, T, "slots", True), kp, ks, vp, vs, _ptr(status), _stream(stream)), "kvi_cache4_read")
 
 
 def kvi_attn_decode4_workspace_bytes(a: Attention, R: int, max_ctx: int, weights: bool) -> int:
@@ -724,10 +742,10 @@ def kvi_attn_decode4(a: Attention, q, ctx_lens, max_ctx: int, block_tables, cach
     op, os_ = _rows(out, a.q_heads, a.head_dim, "out", R)
     wp = None if weights is None else _weights(weights, R, a.kv_heads, "weights")
     _check(load_library().kvi_attn_decode4(
-        ctypes.byref(a), R, qp, qs, _ptr(ctx_lens), int(max_ctx), _ptr(block_tables),
-        block_tables.shape[1], ctypes.byref(cache.struct), int(layer), op, os_, wp,
-        0 if weights is None else weights.shape[2], _ptr(ws), ws.numel() * ws.element_size(),
-        _ptr(status), _stream(stream)), "kvi_attn_decode4")
+        ctypes.byref(a), R, qp, qs, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
+        _ints(block_tables, R, "block_tables"), block_tables.shape[1], cache.ref, layer, op, os_, wp,
+        0 if weights is None else weights.shape[2], _ptr(ws), ws.nbytes, _ptr(status),
+        _stream(stream)), "kvi_attn_decode4")
 
 
 def kvi_cache4_evict_workspace_bytes(kv_heads: int, R: int, max_ctx: int) -> int:
@@ -740,14 +758,17 @@ def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_t
     """Cut a layer of the 4-bit cache back to `budget` slots per request and
     head by accumulated weight (weights float32, pos int32: [R][H][slots])."""
     R, H = ctx_lens.shape[0], cache.kv_heads
-    ptrs = [_weights(t, R, H, n) for t, n in ((weights, "weights"), (pos, "pos"),
-                                              (weights_out, "weights_out"), (pos_out, "pos_out"))]
-    if len({t.shape[2] for t in (weights, pos, weights_out, pos_out)}) > 1:
-        raise ValueError("weights and positions, in and out, must have the same number of slots")
+    ptrs = [_weights(weights, R, H, "weights")]
+    shape = weights.shape
+    for t in (pos, weights_out, pos_out):
+        if t.shape != shape or not t.is_contiguous() or t.element_size() != 4:
+            raise ValueError("weights and positions, in and out, must be contiguous, of one shape and of "
+                             "4-byte elements")
+        ptrs.append(t.data_ptr())
     _check(load_library().kvi_cache4_evict(
-        H, cache.head_dim, R, ctypes.byref(cache.struct), int(layer), _ptr(ctx_lens), int(max_ctx),
-        _ptr(block_tables), block_tables.shape[1], int(budget), int(sink), int(recent), ptrs[0], ptrs[1],
-        weights.shape[2], ptrs[2], ptrs[3], _ptr(ctx_out), _ptr(ws), ws.numel() * ws.element_size(),
+        H, cache.head_dim, R, cache.ref, layer, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
+        _ints(block_tables, R, "block_tables"), block_tables.shape[1], budget, sink, recent, ptrs[0],
+        ptrs[1], shape[2], ptrs[2], ptrs[3], _ints(ctx_out, R, "ctx_out"), _ptr(ws), ws.nbytes,
         _ptr(status), _stream(stream)), "kvi_cache4_evict")
 
 

@@ -154,3 +154,17 @@ def test_evict_arguments():
     with pytest.raises(ValueError):
         evict(p2=i32(1, 2, 41))
     assert kvi.kvi_cache4_evict_workspace_bytes(2, 1, -1) == 0
+
+
+def test_integers_of_another_type():
+    # read as they are not, these would be other blocks, lengths or slots
+    k, slots, st = bf16(3, 2, 64), torch.zeros(3, dtype=torch.int64), i32(1)
+    for bad in (slots.int(), torch.zeros(6, dtype=torch.int64)[::2]):
+        with pytest.raises(ValueError):
+            kvi.kvi_cache4_write(cache(), 0, k, k, bad, st, stream=0)
+        with pytest.raises(ValueError):
+            kvi.kvi_cache4_read(cache(), 0, bad, k, k, st, stream=0)
+    for bad in (dict(ctx=i32(1).long()), dict(start=i32(2).long()), dict(start=i32(1)), dict(table=i32(1, 4).long()),
+                dict(table=i32(1, 8)[:, ::2]), dict(ctx=i32(2), start=i32(3))):
+        with pytest.raises(ValueError):
+            prompt(**bad)
