@@ -587,6 +587,28 @@ struct Plan4 {
 
 size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// Pieces of a request's keys.  A wave is four blocks on every SM.  (us, 8 KV heads
+// of 128 channels, requests x keys, by the number of pieces:)
+//  - One wave where the rows divide it well and the pieces stay short, as a part
+//    of a second wave costs most of a whole one: 16 x 2048 4: 15.6, 8: 17.5; 24 x
+//    4096 3: 32.4, 6: 36.1; 64 x 2048 1: 39.7, 3: 46.6.
+//  - Else two waves, whose ends even out: 40 x 2048 1: 36.4, 4: 30.8; 16 x 28000
+//    4: 119.7, 10: 114.2; and with lengths from half of that up, 16 x 28000 4:
+//    118.9, 10: 94.5, 24 x 8192 3: 53.0, 8: 45.2 (24 x 2048 the same, 64 x 2048
+//    1: 36.2, 3: 37.0).
+//  - No more than 16 pieces, or one per 1024 keys, for the join reads them one
+//    after the other: 1 x 8192 16: 10.6, 64: 15.1; 1 x 28000 32: 17.5, 73: 21.8.
+//  - One piece, and no join, for few keys: 1 x 384 1: 6.1, 3: 6.2; 16 x 600 1:
+//    8.8, 2: 10.2; 1 x 600 1: 8.7, 5: 6.9.
+int64_t pieces(int64_t rows, int32_t max_ctx)
+{
+    constexpr int64_t kWave = 4 * kPlanSms;
+    if (max_ctx <= (rows >= 128 ? 768 : 384)) return 1;
+    int64_t n = std::max<int64_t>(1, kWave / rows);
+    if (n * rows < kWave * 3 / 4 || max_ctx > n * 2048) n = (2 * kWave + rows - 1) / rows;
+    return std::min<int64_t>(n, std::max(16, max_ctx / 1024));
+}
+
 Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
 {
     Plan4 pl{};
@@ -594,15 +616,8 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     // two blocks of 8 heads share each decoded tile where registers allow
     pl.nt = G > 8 && a.head_dim <= 128 ? 2 : 1;
     pl.chunks = (G + 8 * pl.nt - 1) / (8 * pl.nt);
-    // enough blocks for four on every SM, twice, but none below 128 keys (a pair
-    // of tiles a warp).  One piece where the join would cost more than the pieces
-    // save: up to 384 keys (1 request x 8 KV heads: 6.1 us whole, 6.2 split; 512
-    // keys 7.1 and 6.3), and up to 1024 where the rows alone are a block for most
-    // SMs (16 x 8: 11.2 whole, 12.9 split; 64 x 8: 21.0 and 28.2; 2048 keys, 16 x
-    // 8: 18.8 and 17.0).
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
-    const int alone = rows >= 128 ? 1024 : 384;
-    const int64_t want = max_ctx <= alone ? 1 : std::max<int64_t>(1, (8 * kPlanSms + rows - 1) / rows);
+    const int64_t want = pieces(rows, max_ctx);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
