@@ -76,8 +76,8 @@ __device__ __forceinline__ int64_t v_step_at(const Page4 &pg, int off, int g)
 }
 
 // Step and eight codes (channel n in nibble n) of this lane's channels; the
-// four lanes of a group agree on the step.
-__device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t &step)
+// four lanes of a group (`group`, of the warp's) agree on the step.
+__device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t group, uint32_t &step)
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
     // the largest |x| of both halves of the words; infinities and NaN win
@@ -86,8 +86,8 @@ __device__ __forceinline__ uint32_t quantise8(const uint4 &raw, uint32_t &step)
     for (int j = 1; j < 4; ++j) m = __hmax2_nan(m, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j])));
     const uint32_t both = *reinterpret_cast<const uint32_t *>(&m);
     uint32_t top = max(both & 0x7fffu, (both >> 16) & 0x7fffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    top = max(top, __shfl_xor_sync(group, top, 1));
+    top = max(top, __shfl_xor_sync(group, top, 2));
     if (top >= 0x7f80u) {  // not finite: the whole group reads back as NaN
         step = 0x7fff;
         return 0x88888888u;
@@ -200,101 +200,133 @@ __device__ __forceinline__ Pieces pieces_of(const Page4 &pg, int off, int g, int
                   (int32_t)v_step_at(pg, off, g)};
 }
 
+// Pairs of slots, the rule for a prefix, have a loop of their own, with one page
+// pointer and no pieces (65 k rows of 8 heads of 128 channels stored and read back:
+// 117 us, 5.2 TB/s, against 149 with one loop for both).  HBM bounds it, and how
+// much of it is asked for at a time: with reading held to 40 registers, six blocks
+// an SM, it takes those 117 us, 123 with four.
 __global__ void __launch_bounds__(kRowThreads) cache4_write_kernel(const __grid_constant__ RowParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
     RowWork o;
-    row_work(p, o);
+    if (!row_work(p, o)) return;
+    const uint32_t group = 0xfu << ((threadIdx.y * blockDim.x + threadIdx.x) & 28u);  // (lanes of one row work alike)
     const int64_t bytes = p.page.bytes();
-    const int64_t col = 32 * o.g + 8 * o.t;
-    const __nv_bfloat16 *k_src = p.k_in + o.row * p.k_stride + col, *v_src = p.v_in + o.row * p.v_stride + col;
-    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
-    uint8_t *pages[2] = {p.pool + o.page[0] * p.H * bytes, p.pool + o.page[1] * p.H * bytes};
+    const int32_t col = 32 * o.g + 8 * o.t;
     const int v_next = 4 * p.page.groups();  // from a piece of V to the next four channels'
-    // (every lane stays in the loop: groups of four agree on their steps)
-    const int rounds = (p.H + p.heads_apart - 1) / p.heads_apart;
+    if (o.pair) {
+        const Pieces at = pieces_of(p.page, o.off[0], o.g, o.t);
+        uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
+        const __nv_bfloat16 *k_src = p.k_in + o.row * p.k_stride + o.h * p.D + col;
+        const __nv_bfloat16 *v_src = p.v_in + o.row * p.v_stride + o.h * p.D + col;
 #pragma unroll 1
-    for (int n = 0, h = o.h; n < rounds; ++n, h += p.heads_apart) {
-        const bool in = h < p.H;
+        for (int h = o.h; h < p.H; h += p.heads_apart) {
+            const uint4 k0 = *reinterpret_cast<const uint4 *>(k_src);
+            const uint4 k1 = *reinterpret_cast<const uint4 *>(k_src + p.k_stride);
+            const uint4 v0 = *reinterpret_cast<const uint4 *>(v_src);
+            const uint4 v1 = *reinterpret_cast<const uint4 *>(v_src + p.v_stride);
+            uint32_t s0, s1;
+            uint32_t c0 = quantise8(k0, group, s0), c1 = quantise8(k1, group, s1);
+            *reinterpret_cast<uint32_t *>(page + at.k) = c0;
+            *reinterpret_cast<uint32_t *>(page + at.k + p.page.D / 2) = c1;
+            if (o.t == 0) {
+                *reinterpret_cast<uint16_t *>(page + at.ks) = (uint16_t)s0;
+                *reinterpret_cast<uint16_t *>(page + at.ks + 2 * p.page.groups()) = (uint16_t)s1;
+            }
+            c0 = quantise8(v0, group, s0);
+            c1 = quantise8(v1, group, s1);
+            *reinterpret_cast<uint32_t *>(page + at.v) = __byte_perm(c0, c1, 0x5410);
+            *reinterpret_cast<uint32_t *>(page + at.v + v_next) = __byte_perm(c0, c1, 0x7632);
+            if (o.t == 0) *reinterpret_cast<uint32_t *>(page + at.vs) = s0 | (s1 << 16);
+            k_src += p.heads_apart * p.D;
+            v_src += p.heads_apart * p.D;
+            page += p.heads_apart * bytes;
+        }
+        return;
+    }
+    // two rows of their own
+    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
+    const __nv_bfloat16 *k_src = p.k_in + o.row * p.k_stride + col, *v_src = p.v_in + o.row * p.v_stride + col;
+#pragma unroll 1
+    for (int h = o.h; h < p.H; h += p.heads_apart) {
         uint4 k[2], v[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            k[e] = v[e] = make_uint4(0, 0, 0, 0);
-            if (in && o.slot[e] >= 0) {
-                k[e] = *reinterpret_cast<const uint4 *>(k_src + (int64_t)e * p.k_stride + h * p.D);
-                v[e] = *reinterpret_cast<const uint4 *>(v_src + (int64_t)e * p.v_stride + h * p.D);
-            }
+            if (o.slot[e] < 0) continue;
+            k[e] = *reinterpret_cast<const uint4 *>(k_src + e * p.k_stride + h * p.D);
+            v[e] = *reinterpret_cast<const uint4 *>(v_src + e * p.v_stride + h * p.D);
         }
-        uint32_t ks[2], kc[2], vs[2], vc[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            kc[e] = quantise8(k[e], ks[e]);
-            vc[e] = quantise8(v[e], vs[e]);
-        }
-        if (!in) continue;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (o.slot[e] < 0) continue;
-            uint8_t *page = pages[e] + h * bytes;
-            *reinterpret_cast<uint32_t *>(page + at[e].k) = kc[e];
-            if (o.t == 0) *reinterpret_cast<uint16_t *>(page + at[e].ks) = (uint16_t)ks[e];
-            if (o.pair) continue;
-            *reinterpret_cast<uint16_t *>(page + at[e].v) = (uint16_t)vc[e];
-            *reinterpret_cast<uint16_t *>(page + at[e].v + v_next) = (uint16_t)(vc[e] >> 16);
-            if (o.t == 0) *reinterpret_cast<uint16_t *>(page + at[e].vs) = (uint16_t)vs[e];
-        }
-        if (o.pair) {
-            uint8_t *page = pages[0] + h * bytes;
-            *reinterpret_cast<uint32_t *>(page + at[0].v) = __byte_perm(vc[0], vc[1], 0x5410);
-            *reinterpret_cast<uint32_t *>(page + at[0].v + v_next) = __byte_perm(vc[0], vc[1], 0x7632);
-            if (o.t == 0) *reinterpret_cast<uint32_t *>(page + at[0].vs) = vs[0] | (vs[1] << 16);
+            uint32_t ks, vs;
+            const uint32_t kc = quantise8(k[e], group, ks), vc = quantise8(v[e], group, vs);
+            uint8_t *page = p.pool + (o.page[e] * p.H + h) * bytes;
+            *reinterpret_cast<uint32_t *>(page + at[e].k) = kc;
+            *reinterpret_cast<uint16_t *>(page + at[e].v) = (uint16_t)vc;
+            *reinterpret_cast<uint16_t *>(page + at[e].v + v_next) = (uint16_t)(vc >> 16);
+            if (o.t == 0) {
+                *reinterpret_cast<uint16_t *>(page + at[e].ks) = (uint16_t)ks;
+                *reinterpret_cast<uint16_t *>(page + at[e].vs) = (uint16_t)vs;
+            }
         }
     }
 }
 
-__global__ void __launch_bounds__(kRowThreads) cache4_read_kernel(const __grid_constant__ RowParams p)
+__global__ void __launch_bounds__(kRowThreads, 6) cache4_read_kernel(const __grid_constant__ RowParams p)
 {
     pdl_wait();
     pdl_launch_dependents();
     RowWork o;
     if (!row_work(p, o)) return;
     const int64_t bytes = p.page.bytes();
-    const int64_t col = 32 * o.g + 8 * o.t;
-    __nv_bfloat16 *k_dst = p.k_out + o.row * p.k_stride + col, *v_dst = p.v_out + o.row * p.v_stride + col;
-    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
-    const uint8_t *pages[2] = {p.pool + o.page[0] * p.H * bytes, p.pool + o.page[1] * p.H * bytes};
+    const int32_t col = 32 * o.g + 8 * o.t;
     const int v_next = 4 * p.page.groups();
-#pragma unroll 2
+    if (o.pair) {
+        const Pieces at = pieces_of(p.page, o.off[0], o.g, o.t);
+        const uint8_t *page = p.pool + (o.page[0] * p.H + o.h) * bytes;
+        __nv_bfloat16 *k_dst = p.k_out + o.row * p.k_stride + o.h * p.D + col;
+        __nv_bfloat16 *v_dst = p.v_out + o.row * p.v_stride + o.h * p.D + col;
+#pragma unroll 1
+        for (int h = o.h; h < p.H; h += p.heads_apart) {
+            const uint32_t k0 = *reinterpret_cast<const uint32_t *>(page + at.k);
+            const uint32_t k1 = *reinterpret_cast<const uint32_t *>(page + at.k + p.page.D / 2);
+            const uint32_t a = *reinterpret_cast<const uint32_t *>(page + at.v);
+            const uint32_t b = *reinterpret_cast<const uint32_t *>(page + at.v + v_next);
+            const uint32_t s0 = *reinterpret_cast<const uint16_t *>(page + at.ks);
+            const uint32_t s1 = *reinterpret_cast<const uint16_t *>(page + at.ks + 2 * p.page.groups());
+            const uint32_t s = *reinterpret_cast<const uint32_t *>(page + at.vs);
+            *reinterpret_cast<uint4 *>(k_dst) = values8(k0, s0);
+            *reinterpret_cast<uint4 *>(k_dst + p.k_stride) = values8(k1, s1);
+            *reinterpret_cast<uint4 *>(v_dst) = values8(__byte_perm(a, b, 0x5410), s & 0xffffu);
+            *reinterpret_cast<uint4 *>(v_dst + p.v_stride) = values8(__byte_perm(a, b, 0x7632), s >> 16);
+            k_dst += p.heads_apart * p.D;
+            v_dst += p.heads_apart * p.D;
+            page += p.heads_apart * bytes;
+        }
+        return;
+    }
+    const Pieces at[2] = {pieces_of(p.page, o.off[0], o.g, o.t), pieces_of(p.page, o.off[1], o.g, o.t)};
+    __nv_bfloat16 *k_dst = p.k_out + o.row * p.k_stride + col, *v_dst = p.v_out + o.row * p.v_stride + col;
+#pragma unroll 1
     for (int h = o.h; h < p.H; h += p.heads_apart) {
         uint32_t kc[2], ks[2], vc[2], vs[2];
-        if (o.pair) {
-            const uint8_t *page = pages[0] + h * bytes;
-            const uint32_t a = *reinterpret_cast<const uint32_t *>(page + at[0].v);
-            const uint32_t b = *reinterpret_cast<const uint32_t *>(page + at[0].v + v_next);
-            const uint32_t s = *reinterpret_cast<const uint32_t *>(page + at[0].vs);
-            vc[0] = __byte_perm(a, b, 0x5410);
-            vc[1] = __byte_perm(a, b, 0x7632);
-            vs[0] = s & 0xffffu;
-            vs[1] = s >> 16;
-        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (o.slot[e] < 0) continue;
-            const uint8_t *page = pages[e] + h * bytes;
+            const uint8_t *page = p.pool + (o.page[e] * p.H + h) * bytes;
             kc[e] = *reinterpret_cast<const uint32_t *>(page + at[e].k);
+            vc[e] = *reinterpret_cast<const uint16_t *>(page + at[e].v) |
+                    (uint32_t)*reinterpret_cast<const uint16_t *>(page + at[e].v + v_next) << 16;
             ks[e] = *reinterpret_cast<const uint16_t *>(page + at[e].ks);
-            if (!o.pair) {
-                vc[e] = *reinterpret_cast<const uint16_t *>(page + at[e].v) |
-                        (uint32_t)*reinterpret_cast<const uint16_t *>(page + at[e].v + v_next) << 16;
-                vs[e] = *reinterpret_cast<const uint16_t *>(page + at[e].vs);
-            }
+            vs[e] = *reinterpret_cast<const uint16_t *>(page + at[e].vs);
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             if (o.slot[e] < 0) continue;
-            *reinterpret_cast<uint4 *>(k_dst + (int64_t)e * p.k_stride + h * p.D) = values8(kc[e], ks[e]);
-            *reinterpret_cast<uint4 *>(v_dst + (int64_t)e * p.v_stride + h * p.D) = values8(vc[e], vs[e]);
+            *reinterpret_cast<uint4 *>(k_dst + e * p.k_stride + h * p.D) = values8(kc[e], ks[e]);
+            *reinterpret_cast<uint4 *>(v_dst + e * p.v_stride + h * p.D) = values8(vc[e], vs[e]);
         }
     }
 }
@@ -657,8 +689,8 @@ void row_shape(RowParams &p, dim3 &grid, dim3 &block)
 {
     // a head a thread while that keeps the threads below a wave of them, else
     // four, which share a thread's looking up and addressing (stored and read back,
-    // 8 heads of 128 channels: 65 k rows 183 us with one head a thread, 145 us with
-    // four; 64 rows 5.7 us, 13 us)
+    // 8 heads of 128 channels: 65 k rows 145 us with one head a thread, 123 with two,
+    // 117 with four, 153 with eight; 64 rows 5.5 us with one, 13 with four)
     const int64_t threads = (p.T / 2 + 1) * p.H * (p.D / 8);
     p.heads_apart = threads <= (int64_t)kPlanSms4 * 2048 ? p.H : (p.H + 3) / 4;
     p.lanes = p.heads_apart * (p.D / 8);  // a multiple of 4: a group never leaves its warp
