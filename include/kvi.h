@@ -606,7 +606,8 @@ KVI_API size_t kvi_attn_prompt_workspace_bytes(const kvi_attention *a, int32_t R
 
 /* Causal attention of R packed prompts over the paged bf16 cache (Section
  * 3.4: the forward pass over the injected prefix).  Request r owns the query
- * rows d_q_start[r] .. d_q_start[r+1]-1 (n of them, possibly none) and
+ * rows d_q_start[r] .. d_q_start[r+1]-1 (n of them, possibly none; d_q_start
+ * [R + 1] never decreases) and
  * ctx = d_ctx_lens[r] keys: positions 0 .. ctx-1 of block table row r, the
  * injected memory first and the prompt's own K/V last.  Its row i sees the
  * positions <= ctx - n + i (so ctx == n is a whole prompt without memory, and
@@ -702,9 +703,9 @@ KVI_API size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int
  * head by head.  Kept are, in this order until the budget is full: the slots
  * whose position d_pos is < sink or among the newest (> the head's largest
  * position - recent), then those with the largest accumulated weight; ties
- * go to the lower slot, NaN weights count above infinity.  Kept rows at slots >= budget move
- * into the freed slots below it (the i-th freed slot takes the i-th such
- * row); the others stay where they are, so attention over the slots
+ * go to the lower slot, NaN weights count above infinity.  Kept rows at slots
+ * >= budget move into the freed slots below it (the i-th freed slot takes the
+ * i-th such row); the others stay where they are, so attention over the slots
  * 0 .. min(ctx, budget)-1 sees exactly the kept keys (their rotary positions
  * are in the keys already).  Rows at slots >= budget are read, never written.
  *   d_weights, d_pos          float32 / int32 [R][H][stride], read
