@@ -25,12 +25,13 @@
 // bulk copies fill ahead of it, with a softmax of its own; the warps of a block
 // join at the end, and blocks that share a request's keys in a second kernel.
 //
-// What bounds it is the issue of the decoding instructions, not the bytes: with
-// the softmax a tile of 2304 bytes (D = 128) takes nearly 400 warp instructions,
-// and HBM delivers a tile in the time of 390.  Measured at 16 requests x 28 k
-// keys, D = 128, 8 KV heads (0.53 GB): 129 us, 4.1 TB/s.  On the way there: one
-// tile an iteration 152 us, two, which share the bookkeeping and run independently
-// of one another, 140; P * step rounded once 132; K in f16 129.  Against the 140:
+// What bounds it is the decoding, not the bytes: with the softmax a tile of 2304
+// bytes (D = 128) takes nearly 400 warp instructions, and HBM delivers a tile in
+// the time of 390; 128 registers leave 16 warps an SM, which fill two thirds of
+// the issue slots.  Measured at 16 requests x 28 k keys, D = 128, 8 KV heads (0.53
+// GB): 125 us, 4.2 TB/s.  On the way there: one tile an iteration 152 us; two,
+// which share the bookkeeping and run independently of one another, 140; P * step
+// rounded once 132; K in f16 129; more and shorter pieces 125.  Against the 140:
 // 12 warps an SM instead of 16 took 148, shifts as multiplications 166, the
 // offset of V's codes taken off by a second matrix product 155.
 #include <cuda_runtime.h>
@@ -592,10 +593,10 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 //  - One wave where the rows divide it well and the pieces stay short, as a part
 //    of a second wave costs most of a whole one: 16 x 2048 4: 15.6, 8: 17.5; 24 x
 //    4096 3: 32.4, 6: 36.1; 64 x 2048 1: 39.7, 3: 46.6.
-//  - Else two waves, whose ends even out: 40 x 2048 1: 36.4, 4: 30.8; 16 x 28000
-//    4: 119.7, 10: 114.2; and with lengths from half of that up, 16 x 28000 4:
-//    118.9, 10: 94.5, 24 x 8192 3: 53.0, 8: 45.2 (24 x 2048 the same, 64 x 2048
-//    1: 36.2, 3: 37.0).
+//  - Else two waves, whose ends even out: 40 x 2048 1: 36.4, 4: 30.8; and up to
+//    four where the pieces are long: 16 x 28000 4: 119.7, 10: 114.2, 14: 110.3.
+//    Lengths from half of max_ctx up, 24 x 8192 3: 53.0, 8: 45.2; 16 x 28000 4:
+//    118.9, 10: 94.5, 14: 91.3 (24 x 2048 the same, 64 x 2048 1: 36.2, 3: 37.0).
 //  - No more than 16 pieces, or one per 1024 keys, for the join reads them one
 //    after the other: 1 x 8192 16: 10.6, 64: 15.1; 1 x 28000 32: 17.5, 73: 21.8.
 //  - One piece, and no join, for few keys: 1 x 384 1: 6.1, 3: 6.2; 16 x 600 1:
@@ -606,6 +607,7 @@ int64_t pieces(int64_t rows, int32_t max_ctx)
     if (max_ctx <= (rows >= 128 ? 768 : 384)) return 1;
     int64_t n = std::max<int64_t>(1, kWave / rows);
     if (n * rows < kWave * 3 / 4 || max_ctx > n * 2048) n = (2 * kWave + rows - 1) / rows;
+    n = std::max(n, std::min<int64_t>((max_ctx + 2047) / 2048, 4 * kWave / rows));
     return std::min<int64_t>(n, std::max(16, max_ctx / 1024));
 }
 
