@@ -4,7 +4,9 @@ Serving-time path of "InferScale: GPU-Native KV Injection for Personalized
 LLM Serving": exact top-k retrieval of memory facts by embedding similarity
 (Figure 2 caption), Chunked RoPE rotation of their pre-RoPE keys to the
 prompt positions they take (Section 5.1 / Theorem 6), and scatter-copy of K/V
-into a vLLM-style paged KV cache through a block table (Section 3.4).
+into a vLLM-style paged KV cache through a block table (Section 3.4); then the
+attention that reads the memory there: causal prompts, a 4-bit cache with its
+decoding step, and eviction from it by accumulated weight.
 
 The compute is in ``libkvi.so`` (hand-written CUDA for sm_103a, C ABI in
 ``include/kvi.h``); this package is a ctypes binding with the same function

@@ -30,8 +30,8 @@
 // the time of 390; 128 registers leave 16 warps an SM, which fill two thirds of
 // the issue slots.  Measured at 16 requests x 28 k keys, D = 128, 8 KV heads (0.53
 // GB): 125 us, 4.2 TB/s.  On the way there: one tile an iteration 152 us; two,
-// which share the bookkeeping and run independently of one another, 140; P * step
-// rounded once 132; K in f16 129; more and shorter pieces 125.  Against the 140:
+// which share the bookkeeping and run independently of one another, 140, later
+// 132; K in f16 129; more and shorter pieces 125.  Against the 140:
 // 12 warps an SM instead of 16 took 148, shifts as multiplications 166, the
 // offset of V's codes taken off by a second matrix product 155.
 #include <cuda_runtime.h>
