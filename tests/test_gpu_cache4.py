@@ -106,6 +106,31 @@ def test_converts_a_bf16_pool():
     assert torch.equal(out.view(2, -1, H, D)[1], c.vd.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("first", [0, 1])
+@pytest.mark.parametrize("H,D", [(6, 64), (5, 96), (7, 128)])
+def test_long_prefixes(H, D, first):
+    """Enough rows that a thread takes several heads; runs of slots that pair up, broken by skipped and by lone rows."""
+    g = ac.gen(H + D + first)
+    B, T = 48, 24001
+    blocks = T // B + 2
+    slots = torch.arange(first, first + T, device=DEV)
+    order = torch.randperm(blocks, generator=g, device=DEV)
+    slots = order[slots // B] * B + slots % B
+    slots[1000:1400:7] = -1
+    slots[5000:5200] = slots[5000:5200].flip(0)
+    k, v = (ac.randn(g, T, H, D).to(torch.bfloat16) for _ in range(2))
+    pool = torch.zeros(blocks, H, ac.page_bytes(B, D), dtype=torch.uint8, device=DEV)
+    cache, status = kvi.cache4([pool], B, H, D), torch.zeros(1, dtype=torch.int32, device=DEV)
+    kvi.kvi_cache4_write(cache, 0, k, v, slots, status)
+    kb, vb = torch.full_like(k, 3.0), torch.full_like(v, 3.0)
+    kvi.kvi_cache4_read(cache, 0, slots, kb, vb, status)
+    live = slots >= 0
+    for x, y in ((k, kb), (v, vb)):
+        assert torch.equal(y[live], ac.dequantise(*ac.quantise(x)).to(torch.bfloat16)[live])
+        assert bool((y[~live] == 3).all())
+    assert int(status) == 0
+
+
 # ------------------------------------------------------------- decoding step
 
 class Step:
@@ -335,6 +360,27 @@ def test_evict(H, D, B, ctx, budget, sink, recent, kind):
             assert torch.equal(vb[rows[:left], h], c.c.vd[at, h].to(torch.bfloat16))
             # rows at or past the budget are never written
             assert torch.equal(kb[rows[left:], h], c.c.kd[rows[left:], h].to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("H,ctx,budget", [(64, [300, 290], 150), (43, [700, 200, 701], 333), (2, [300], 150)])
+def test_evict_many_rows(H, ctx, budget):
+    """Many heads, whose blocks move their own rows, and few, whose rows a second kernel moves."""
+    c = Step(H, H, 32, 16, ctx, seed=H)
+    w = torch.rand(len(ctx), H, max(ctx) + 1, generator=ac.gen(H), device=DEV)
+    pos = torch.arange(max(ctx) + 1, dtype=torch.int32, device=DEV).expand(len(ctx), H, -1).contiguous()
+    w_out, pos_out, out = run_evict(c, ctx, budget, 4, 16, w, pos)
+    assert int(c.c.status) == 0 and out.tolist() == [min(n, budget) for n in ctx]
+    wc, pc = w.cpu(), pos.cpu()
+    for r, n in enumerate(ctx):
+        left = min(n, budget)
+        rows = c.c.rows(c.table[r], n)
+        k, v = (torch.empty(left, H, 32, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        kvi.kvi_cache4_read(c.c.cache, 0, rows[:left], k, v, c.c.status)
+        for h in range(H):
+            src = torch.tensor(evict_reference(wc[r, h].tolist(), pc[r, h].tolist(), n, budget, 4, 16), dtype=torch.long)
+            assert torch.equal(pos_out[r, h, :left].cpu(), pc[r, h, src])
+            assert torch.equal(k[:, h], c.c.kd[rows[src.to(DEV)], h].to(torch.bfloat16))
+            assert torch.equal(v[:, h], c.c.vd[rows[src.to(DEV)], h].to(torch.bfloat16))
 
 
 def test_evict_then_attend():
