@@ -79,6 +79,7 @@ struct PromptParams {
     float *lse;
     int32_t chunks;             // row chunks per KV head: of each request, or (tiles) of all
     int32_t S, span;
+    int32_t per;                // (tiles) tokens of a row tile
     float *po;
     float2 *ml;
     int32_t *status;

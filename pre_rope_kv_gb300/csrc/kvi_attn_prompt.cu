@@ -496,6 +496,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.R = R;
     p.total_q = total_q;
     p.max_q = max_q;
+    p.per = tile_tokens(a->q_heads / a->kv_heads);
     p.ctx_lens = d_ctx_lens;
     p.max_ctx = max_ctx;
     p.max_blocks = max_blocks;

@@ -74,6 +74,7 @@ struct TileTail {
     uint64_t drained;
     uint32_t tmem;
     int32_t odd;            // `first` holds something
+    int32_t lost;           // a key's block lies outside the pool
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
 };
 
@@ -230,6 +231,15 @@ __device__ __forceinline__ void box4(uint32_t dst, const CUtensorMap *map, int x
         : "memory");
 }
 
+// from shared memory; what lies past the tensor's end is not written
+__device__ __forceinline__ void box3_out(const CUtensorMap *map, int x, int y, int z, uint32_t src)
+{
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(z), "r"(src)
+                 : "memory");
+}
+
 // The warp that copies V looks over a tile of it before the products.  An infinity or NaN
 // becomes zero, noted with its key for the rows that see it (a key past the end
 // is seen by none).  The rule is that there is none: one maximum a word.
@@ -304,7 +314,7 @@ __device__ __forceinline__ void announce(uint64_t &bar)
 template <int DP>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-            const __grid_constant__ PromptParams p, int box_keys)
+            const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ PromptParams p, int box_shift)
 {
     using Sm = TileSmem<DP>;
     extern __shared__ uint8_t smem_raw[];
@@ -312,19 +322,38 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     TileTail<DP> &tl = *reinterpret_cast<TileTail<DP> *>(base + Sm::kTail);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // ---- the block's rows and keys
-    const int split = blockIdx.x % p.S, h = (blockIdx.x / p.S) % p.H;
-    const int per = kM / p.G;  // tokens of a tile
-    if (tid == 0) {
+    if (warp == kCopyK && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_q)) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tm_kv)) : "memory");
+        mbar_init(smem_u32(&tl.q_full), 1);
+        for (int s = 0; s < Sm::kStages; ++s) {
+            mbar_init(smem_u32(&tl.full[s]), 1);
+            mbar_init(smem_u32(&tl.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&tl.s_full[i]), 1);
+            mbar_init(smem_u32(&tl.p_full[i][0]), 4);
+            mbar_init(smem_u32(&tl.p_full[i][1]), 4);
+            mbar_init(smem_u32(&tl.o_full[i]), 1);
+        }
+        for (int s = 0; s < Sm::kStages / 2; ++s) mbar_init(smem_u32(&tl.v_fixed[s]), 1);
+        mbar_init(smem_u32(&tl.drained), 1);
+        tl.odd = 0;
+        tl.lost = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    // ---- the block's rows and keys
+    const uint32_t rest = p.S == 1 ? blockIdx.x : blockIdx.x / (uint32_t)p.S;
+    const int split = (int)(blockIdx.x - rest * (uint32_t)p.S);
+    const int per = p.per;
     pdl_wait();
     pdl_launch_dependents();
     // Blocks are for the tile pairs that there are, numbered request after request
     // and from a request's end (its heaviest) to its start; a warp looks over 32
     // requests at once.
-    int item = blockIdx.x / p.S / p.H, r = -1, pair = 0;
+    int item = (int)(rest / (uint32_t)p.H), r = -1, pair = 0;
+    const int h = (int)(rest - (uint32_t)item * (uint32_t)p.H);
     RequestSpan rq{0, 0, 0};
     for (int r0 = 0; r0 < p.R; r0 += 32) {
         RequestSpan c{0, 0, 0};
@@ -353,9 +382,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     if (r < 0) return;
     const int tok0 = pair * 2 * per;  // the block's first token
-    const int pieces = max(1, (rq.ctx + p.span - 1) / p.span);
-    if (split >= pieces) return;
-    const bool whole = pieces == 1;
+    const bool whole = rq.ctx <= p.span;  // its keys are one piece
+    if (split > 0 && (int64_t)split * p.span >= rq.ctx) return;
     const int seen0 = rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
@@ -373,14 +401,20 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
     // there, reads as zeros from past a page's last token.
-    const int boxes = kM / box_keys, half = lane / boxes, box = lane % boxes;
+    const int half = lane >> box_shift, box = lane & ((1 << box_shift) - 1), box_keys = kM >> box_shift;
     // (Its place is looked up before its stage is waited for.)
     int at_token = 0, at_block = 0;
     auto look_up = [&](int j) {
         const int key = from + j * kM + box * box_keys;
-        const int block = key < rq.ctx ? __ldg(table + key / p.B) : -1;
+        const uint32_t page = (uint32_t)key / (uint32_t)p.B;
+        const int block = key < rq.ctx ? __ldg(table + page) : -1;
         const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
-        at_token = there ? key % p.B : p.B;
+        // (noted before the copy is asked for, so before its scores are looked at)
+        if (warp == kCopyK && __any_sync(0xffffffffu, key < rq.ctx && !there) && lane == 0) {
+            tl.lost = 1;
+            record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        }
+        at_token = there ? key - (int)page * p.B : p.B;
         at_block = there ? block : 0;
     };
     auto copy_tile = [&](int plane, uint32_t stage) {
@@ -391,28 +425,33 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             box4(smem_u32(base + Sm::kRing) + stage * Sm::kTile + half * kHalf + box * box_keys * 128, &tm_kv, 64 * half, h,
                  at_token, plane * p.num_blocks + at_block, bar);
     };
-    if (warp == kCopyK) {
-        // the first copies go out while tensor memory is allocated
-        if (lane == 0) {
-            mbar_init(smem_u32(&tl.q_full), 1);
-            for (int s = 0; s < Sm::kStages; ++s) {
-                mbar_init(smem_u32(&tl.full[s]), 1);
-                mbar_init(smem_u32(&tl.empty[s]), 1);
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(smem_u32(&tl.s_full[i]), 1);
-                mbar_init(smem_u32(&tl.p_full[i][0]), 4);
-                mbar_init(smem_u32(&tl.p_full[i][1]), 4);
-                mbar_init(smem_u32(&tl.o_full[i]), 1);
-            }
-            for (int s = 0; s < Sm::kStages / 2; ++s) mbar_init(smem_u32(&tl.v_fixed[s]), 1);
-            mbar_init(smem_u32(&tl.drained), 1);
-            tl.odd = 0;
-            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
-        if (n > 0) {
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tl.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    // The warp that copies K made the barriers and has nothing to wait for.  (A
+    // barrier of its own: that warp may be at the last one before others are here.)
+    fence_before();
+    if (warp == kCopyK)
+        asm volatile("bar.arrive 2, 384;" ::: "memory");
+    else
+        asm volatile("bar.sync 2, 384;" ::: "memory");
+    fence_after();
+    const uint32_t tmem = warp == kCopyK ? 0 : tl.tmem;
+    // tensor memory: S (and P) of the two tiles, then their O
+    constexpr int kColO = 2 * kM;
+
+    if (warp >= kCopyK) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kCopyK || warp == kCopyV) {
+        // ------------------------------------------------------------ copies
+        // one warp copies Q and K, one V
+        const int plane = warp == kCopyV ? 1 : 0;
+        uint32_t stage = plane, phase = 1;  // an unused stage is empty
+        bool ok = true;
+        int slots = 0;
+        if (plane == 0 && n > 0) {
             // rows past a tile's tokens keep what the memory held: their scores are
             // computed and not used
             const uint32_t bar = smem_u32(&tl.q_full);
@@ -422,35 +461,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane < tiles * Sm::kHalves)
                 box3(smem_u32(base + Sm::kQ) + (lane / Sm::kHalves) * Sm::kTile + (lane % Sm::kHalves) * kHalf, &tm_q,
                      64 * (lane % Sm::kHalves), h * p.G, rq.q0 + tok0 + (lane / Sm::kHalves) * per, bar);
-            look_up(0);
-            copy_tile(0, 0);
-            copy_tile(1, 1);
         }
-    }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tl.tmem)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    bool lost = false;  // a block of this range lies outside the pool
-    for (int b = from / p.B + tid; (int64_t)b * p.B < min(rq.ctx, from + n * kM); b += kTileThreads)
-        lost |= (uint32_t)table[b] >= (uint32_t)p.num_blocks;
-    fence_before();
-    lost = __syncthreads_or(lost);
-    fence_after();
-    if (lost && tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-    const uint32_t tmem = tl.tmem;
-    // tensor memory: S (and P) of the two tiles, then their O
-    constexpr int kColO = 2 * kM;
-
-    if (warp >= kCopyK) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == kCopyK || warp == kCopyV) {
-        // ------------------------------------------------------------ copies
-        // one warp copies K, one V, from the second tile on
-        const int plane = warp == kCopyV ? 1 : 0;
-        uint32_t stage = plane + 2, phase = 1;  // an unused stage is empty
-        bool ok = true;
-        int slots = n > 0 ? 1 : 0;
         // V of the tiles that some row sees in part is looked over before the next
         // V is asked for (it has been there for a while by then)
         const int first_partly = sure > from ? (sure - from) / kM : 0;
@@ -466,9 +477,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
             return true;
         };
-        for (int j = 1; j < n; ++j) {
+        for (int j = 0; j < n; ++j) {
             look_up(j);
-            ok = look_over(j - 1);
+            ok = j == 0 || look_over(j - 1);
             if (!ok) break;
             if (stage >= Sm::kStages) {
                 stage = plane;
@@ -493,7 +504,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 const int last = (slots - 1 - lane) / kOwn;
                 (void)mbar_wait_brisk(smem_u32(&tl.full[2 * lane + plane]), (uint32_t)(last & 1), kTileWaitNs);
             }
-            if (lane == 0 && plane == 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
+            if (lane == 0 && plane == 0 && n > 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
         }
         __syncwarp();
         if (plane == 1) asm volatile("bar.arrive 1, 288;" ::: "memory");
@@ -639,6 +650,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tmem_load32(t_s + 64, s + 64);
             tmem_load32(t_s + 96, s + 96);
             float top;
+            const bool lost = *reinterpret_cast<volatile int32_t *>(&tl.lost) != 0;
             if (partly || lost) {
                 tmem_wait_ld(s + 64);
                 tmem_wait_ld(s + 96);
@@ -705,76 +717,99 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         // ---- the rows' results; the values have been looked over
         asm volatile("bar.sync 1, 288;" ::: "memory");
-        if (my > 0 && ok) {
-            ok = mbar_wait_brisk(smem_u32(&tl.o_full[i]), 0, kTileWaitNs);
+        if (n > 0 && ok) {
+            // (without products of its own the tile's Q may still be on its way, and its
+            // place is written to below)
+            ok = mbar_wait_brisk(smem_u32(my > 0 ? &tl.o_full[i] : &tl.q_full), 0, kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 ok = false;
             }
             fence_after();
         }
+        // One piece and all of a tile's tokens: its rows go out as Q came in, through
+        // the tile's Q (which nothing reads any more), by a copy that a lane asks for.
+        const bool full = whole && tok0 + (i + 1) * per <= rq.n_q;
         if (ok) {
             const int head = h * p.G + row % p.G;
             const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
-            // A thread holds a row, and rows lie far apart, so the warp's 32 rows go
-            // through its quarter of the tile's Q (which nothing reads any more): row
-            // by row out of it, a store covers whole lines.  16-byte pieces: 8
-            // channels in bf16, or in two passes 4 in float32.
-            constexpr int kPieces = DP / 8, kRowsAt = 32 / kPieces;
-            uint4 *stage = reinterpret_cast<uint4 *>(base + Sm::kQ + i * Sm::kTile) + (warp & 3) * 32 * kPieces;
-            const uint64_t mine = reinterpret_cast<uint64_t>(
-                whole ? static_cast<void *>(p.out + tok * p.out_stride + (int64_t)head * p.D)
-                      : static_cast<void *>(p.po + (at * p.S + split) * p.D));
-            const uint32_t rows_there = __ballot_sync(0xffffffffu, real);
+            // 32 channels of the row
+            auto row_values = [&](int c, float *v) {
+                if (my > 0) {
+                    tmem_load32(t_o + c, v);
+                    tmem_wait_ld(v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (odd) {
+                    const float inf = __int_as_float(0x7f800000);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (tl.first[0][c + e] <= last) v[e] += inf;
+                        if (tl.first[1][c + e] <= last) v[e] -= inf;
+                        if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                    }
+                }
+            };
+            auto packed = [&](const float *v) {
+                return make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
+                                  pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
+            };
+            if (full) {
+                uint8_t *to = base + Sm::kQ + i * Sm::kTile + row * 128;
 #pragma unroll 1
-            for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
-                const int c0 = whole ? 0 : pass * (DP / 2), c1 = whole ? DP : c0 + DP / 2;
-#pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
+                for (int c = 0; c < DP; c += 32) {
                     float v[32];
-                    if (my > 0) {
-                        tmem_load32(t_o + c, v);
-                        tmem_wait_ld(v);
-                    } else {
+                    row_values(c, v);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = 0.f;
-                    }
-                    if (odd) {
-                        const float inf = __int_as_float(0x7f800000);
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4 *>(to + (c >> 6) * kHalf + ((((c & 63) + e) / 8) ^ (row & 7)) * 16) = packed(v + e);
+                }
+            } else {
+                // A thread holds a row, and rows lie far apart, so the warp's 32 rows go
+                // through its quarter of the tile's Q (which nothing reads any more): row
+                // by row out of it, a store covers whole lines.  16-byte pieces: 8
+                // channels in bf16, or in two passes 4 in float32.
+                constexpr int kPieces = DP / 8, kRowsAt = 32 / kPieces;
+                uint4 *stage = reinterpret_cast<uint4 *>(base + Sm::kQ + i * Sm::kTile) + (warp & 3) * 32 * kPieces;
+                const uint64_t mine = reinterpret_cast<uint64_t>(
+                    whole ? static_cast<void *>(p.out + tok * p.out_stride + (int64_t)head * p.D)
+                          : static_cast<void *>(p.po + (at * p.S + split) * p.D));
+                const uint32_t rows_there = __ballot_sync(0xffffffffu, real);
+#pragma unroll 1
+                for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
+                    const int c0 = whole ? 0 : pass * (DP / 2), c1 = whole ? DP : c0 + DP / 2;
+#pragma unroll 1
+                    for (int c = c0; c < c1; c += 32) {
+                        float v[32];
+                        row_values(c, v);
+                        if (whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            if (tl.first[0][c + e] <= last) v[e] += inf;
-                            if (tl.first[1][c + e] <= last) v[e] -= inf;
-                            if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                            for (int e = 0; e < 32; e += 8)
+                                stage[lane * kPieces + (((c + e) / 8) ^ (lane & 7))] = packed(v + e);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 4)
+                                stage[lane * kPieces + (((c - c0 + e) / 4) ^ (lane & 7))] =
+                                    make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
+                                               __float_as_uint(v[e + 3]));
                         }
+                        __syncwarp();
                     }
-                    if (whole) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8)
-                            stage[lane * kPieces + (((c + e) / 8) ^ (lane & 7))] =
-                                make_uint4(pack_bf16(v[e] * inv, v[e + 1] * inv), pack_bf16(v[e + 2] * inv, v[e + 3] * inv),
-                                           pack_bf16(v[e + 4] * inv, v[e + 5] * inv), pack_bf16(v[e + 6] * inv, v[e + 7] * inv));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            stage[lane * kPieces + (((c - c0 + e) / 4) ^ (lane & 7))] =
-                                make_uint4(__float_as_uint(v[e]), __float_as_uint(v[e + 1]), __float_as_uint(v[e + 2]),
-                                           __float_as_uint(v[e + 3]));
+                    const int piece = lane % kPieces;
+                    const bool in_row = whole ? 8 * piece < p.D : c0 + 4 * piece < p.D;
+#pragma unroll 4
+                    for (int k = 0; k < 32; k += kRowsAt) {
+                        const int rr = k + lane / kPieces;
+                        const uint64_t to = __shfl_sync(0xffffffffu, mine, rr);
+                        if (((rows_there >> rr) & 1u) && in_row)
+                            reinterpret_cast<uint4 *>(to)[piece + pass * kPieces] = stage[rr * kPieces + (piece ^ (rr & 7))];
                     }
                     __syncwarp();
                 }
-                const int piece = lane % kPieces;
-                const bool in_row = whole ? 8 * piece < p.D : c0 + 4 * piece < p.D;
-#pragma unroll 4
-                for (int k = 0; k < 32; k += kRowsAt) {
-                    const int rr = k + lane / kPieces;
-                    const uint64_t to = __shfl_sync(0xffffffffu, mine, rr);
-                    if (((rows_there >> rr) & 1u) && in_row)
-                        reinterpret_cast<uint4 *>(to)[piece + pass * kPieces] = stage[rr * kPieces + (piece ^ (rr & 7))];
-                }
-                __syncwarp();
             }
             if (real) {
                 const float M = m * p.scale;
@@ -782,6 +817,21 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     p.ml[at * p.S + split] = make_float2(M, sum);
                 else if (p.lse)
                     p.lse[at] = sum == 0.f ? neg_inf() : (M + log2f(sum)) * kLn2;
+            }
+        }
+        if (full) {
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            // (by every warp, whatever became of its waits)
+            if (i == 0)
+                asm volatile("bar.sync 3, 128;" ::: "memory");
+            else
+                asm volatile("bar.sync 4, 128;" ::: "memory");
+            if ((warp & 3) == 0 && lane == 0 && ok) {
+#pragma unroll
+                for (int f = 0; f < Sm::kHalves; ++f)
+                    box3_out(&tm_out, 64 * f, h * p.G, rq.q0 + tok0 + i * per, smem_u32(base + Sm::kQ + i * Sm::kTile + f * kHalf));
+                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
             }
         }
     }
@@ -798,7 +848,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 template <int DP>
 static cudaError_t run_tiles(const PromptParams &p, cudaStream_t s)
 {
-    CUtensorMap tq, tkv;
+    CUtensorMap tq, tkv, to;
     const uint32_t per = (uint32_t)tile_tokens(p.G);
     const uint64_t qd[3] = {(uint64_t)p.D, (uint64_t)p.Hq, (uint64_t)p.total_q};
     const uint64_t qp[2] = {(uint64_t)p.D * 2, (uint64_t)p.q_stride * 2};
@@ -806,20 +856,26 @@ static cudaError_t run_tiles(const PromptParams &p, cudaStream_t s)
     cudaError_t e = tensor_map_bf16(&tq, p.q, 3, qd, qp, qb);
     if (e != cudaSuccess) return e;
     // K and V pieces: channels, heads, tokens of a page, pages (K's, then V's)
-    int box = 8;
-    while (box < kM && p.B % (2 * box) == 0) box *= 2;
+    int box = 8, shift = 4;  // 128 >> shift keys a box
+    while (box < kM && p.B % (2 * box) == 0) {
+        box *= 2;
+        --shift;
+    }
     const uint64_t row = (uint64_t)p.H * p.D * 2;
     const uint64_t kd[4] = {(uint64_t)p.D, (uint64_t)p.H, (uint64_t)p.B, 2 * (uint64_t)p.num_blocks};
     const uint64_t kp[3] = {(uint64_t)p.D * 2, row, row * p.B};
     const uint32_t kb[4] = {64, 1, (uint32_t)box, 1};
     e = tensor_map_bf16(&tkv, p.pool, 4, kd, kp, kb);
     if (e != cudaSuccess) return e;
+    const uint64_t op[2] = {(uint64_t)p.D * 2, (uint64_t)p.out_stride * 2};
+    e = tensor_map_bf16(&to, p.out, 3, qd, op, qb);
+    if (e != cudaSuccess) return e;
     constexpr int bytes = TileSmem<DP>::kTail + (int)sizeof(TileTail<DP>) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
     e = smem_opt_in(tile_kernel<DP>, bytes);
     if (e != cudaSuccess) return e;
     return launch_chained(tile_kernel<DP>, dim3((unsigned)(p.S * p.H * p.chunks)), kTileThreads, bytes, s, tq,
-                          tkv, p, box);
+                          tkv, to, p, shift);
 }
 
 cudaError_t launch_tiles(const PromptParams &p, cudaStream_t s)
