@@ -402,19 +402,21 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
     // there, reads as zeros from past a page's last token.
     const int half = lane >> box_shift, box = lane & ((1 << box_shift) - 1), box_keys = kM >> box_shift;
-    // (Its place is looked up before its stage is waited for.)
+    // (Its block is asked for a tile ahead.)
     int at_token = 0, at_block = 0;
-    auto look_up = [&](int j) {
+    auto block_of = [&](int j) {
         const int key = from + j * kM + box * box_keys;
-        const uint32_t page = (uint32_t)key / (uint32_t)p.B;
-        const int block = key < rq.ctx ? __ldg(table + page) : -1;
+        return key < rq.ctx ? __ldg(table + (uint32_t)key / (uint32_t)p.B) : -1;
+    };
+    auto look_up = [&](int j, int block) {
+        const int key = from + j * kM + box * box_keys;
         const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
         // (noted before the copy is asked for, so before its scores are looked at)
         if (warp == kCopyK && __any_sync(0xffffffffu, key < rq.ctx && !there) && lane == 0) {
             tl.lost = 1;
             record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         }
-        at_token = there ? key - (int)page * p.B : p.B;
+        at_token = there ? key % (uint32_t)p.B : p.B;
         at_block = there ? block : 0;
     };
     auto copy_tile = [&](int plane, uint32_t stage) {
@@ -451,6 +453,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         uint32_t stage = plane, phase = 1;  // an unused stage is empty
         bool ok = true;
         int slots = 0;
+        int block = n > 0 ? block_of(0) : 0;
         if (plane == 0 && n > 0) {
             // rows past a tile's tokens keep what the memory held: their scores are
             // computed and not used
@@ -478,7 +481,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             return true;
         };
         for (int j = 0; j < n; ++j) {
-            look_up(j);
+            look_up(j, block);
+            if (j + 1 < n) block = block_of(j + 1);
             ok = j == 0 || look_over(j - 1);
             if (!ok) break;
             if (stage >= Sm::kStages) {
