@@ -10,9 +10,9 @@
 //   O += P V       tcgen05.mma, P from tensor memory, V in shared memory
 //                  as it lies in the cache (channels contiguous)
 // The two tiles alternate: while one tile's scores go through the softmax the
-// tensor cores work on the other's products.  One warp copies (one box of K or
-// V per lane: a piece of a cache page, 64 channels wide), one issues the
-// matrix instructions, four per tile do the softmax.
+// tensor cores work on the other's products.  Two warps copy, K and V (a box per
+// lane: a piece of a cache page, 64 channels wide), one issues the matrix
+// instructions, four per tile do the softmax.
 //
 // The running reference m moves only when a score passes it by 2^kLazy (O is
 // rescaled in tensor memory then, which a row needs a few times in all).
@@ -30,10 +30,11 @@
 // long prompts, and for ragged ones the 6 us or so that a block takes beside
 // them (Q and the first keys, the rows' results), which nothing overlaps as a
 // block fills its SM.  32 heads over 8 of 128 channels: one prompt of 8192 tokens
-// 0.33 ms, 1650 TFLOP/s; 16 prompts of 1 to 2048 tokens and up to 1600 keys of
-// memory 0.19 ms, 1110 TFLOP/s.  Blocks that stay and take several pairs of tiles
-// measured the same (0.35 and 0.19 ms); two warps issuing matrix instructions, or
-// copies by cp.async instead of the tensor map, were slower.
+// 0.33 ms, 1670 TFLOP/s; 16 prompts of 1 to 2048 tokens and up to 1600 keys of
+// memory 0.19 ms, 1130 TFLOP/s.  No faster: blocks that stay and take several
+// pairs of tiles (0.35 and 0.19 ms), the pairs with the most keys first (0.34 and
+// 0.195 ms); slower: two warps issuing matrix instructions, copies by cp.async
+// instead of the tensor map.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
