@@ -112,23 +112,38 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 // Every kernel of these calls may begin while the previous kernel of the
 // stream drains, waits for it before it touches memory (pdl_wait), and lets
 // the next one begin (pdl_launch_dependents): what a launch costs is hidden
-// behind the work before it.
+// behind the work before it.  `blocks` > 1: the blocks along x form clusters of so
+// many.
 template <typename P, typename... Args>
-inline cudaError_t launch_chained(void (*kernel)(P, Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                                  const std::decay_t<P> &p, const std::decay_t<Args> &...args)
+inline cudaError_t launch_chained_clusters(void (*kernel)(P, Args...), int blocks, dim3 grid, dim3 block, size_t smem,
+                                           cudaStream_t s, const std::decay_t<P> &p, const std::decay_t<Args> &...args)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    if (blocks > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = (unsigned)blocks;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, args...);
     return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename P, typename... Args>
+inline cudaError_t launch_chained(void (*kernel)(P, Args...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                  const std::decay_t<P> &p, const std::decay_t<Args> &...args)
+{
+    return launch_chained_clusters(kernel, 1, grid, block, smem, s, p, args...);
 }
 
 namespace {

@@ -23,7 +23,8 @@
 //      needs half the shifts; V in bf16, as P * step has no bound that fits f16.
 // A warp takes pairs of tiles of 16 keys in turn, from a ring of its own that
 // bulk copies fill ahead of it, with a softmax of its own; the warps of a block
-// join at the end, and blocks that share a request's keys in a second kernel.
+// join at the end, and blocks that share a request's keys through one another's
+// shared memory as a cluster, or in a second kernel.
 //
 // What bounds it is the decoding, not the bytes: with the softmax a tile of 2304
 // bytes (D = 128) takes nearly 400 warp instructions, and HBM delivers a tile in
@@ -65,6 +66,7 @@ struct Decode4Params {
     __nv_bfloat16 *out;
     int64_t out_stride;
     int32_t S, span;
+    int32_t joined;  // a request's pieces are a cluster, which joins them
     float *po;
     float2 *ml;
     float *scores;   // [R][H][max_ctx][score_stride] or null
@@ -113,6 +115,24 @@ __device__ __forceinline__ void load_halves(uint32_t (&w)[(N + 1) / 2], const ui
     }
 }
 
+constexpr int kMostJoined = 8;  // blocks of a cluster
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// What block `rank` of the cluster has at this address of its shared memory.
+__device__ __forceinline__ float2 load_of_block(uint32_t addr, int rank)
+{
+    float2 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
@@ -129,11 +149,14 @@ struct Smem4 {
     static constexpr int kTile = 2 * kCodes + 2 * kSteps;
     static constexpr int kStage = 2 * kTile;
     static constexpr int kRing = kStages4 * kStage;
-    static constexpr int kJoin = kWarps4 * 8 * NT * (32 * NG + 4) * 4;
+    static constexpr int kSum = kWarps4 * 8 * NT * (32 * NG + 4) * 4;  // then the block's own
+    static constexpr int kJoin = kSum + 8 * NT * 32 * NG * 4;
     static constexpr int kBytes = kWarps4 * kRing > kJoin ? kWarps4 * kRing : kJoin;
 };
 
-template <int NG, int NT>
+// JOINED: a request's pieces are a cluster, which joins them.  (A kernel of its
+// own, as the join's registers are the loop's: 16 x 28 k keys 128 us in one, 125.)
+template <int NG, int NT, bool JOINED>
 __global__ void __launch_bounds__(kWarps4 * 32, NG * NT <= 4 ? 4 : NG * NT <= 6 ? 3 : 2)
 decode4_kernel(const __grid_constant__ Decode4Params p)
 {
@@ -142,6 +165,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t s_bar[kWarps4][kStages4];
     __shared__ float s_m[kWarps4][8 * NT], s_l[kWarps4][8 * NT];
+    __shared__ float2 s_ml[8 * NT];  // of the block
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x;
     const int h = blockIdx.y / p.chunks, c0 = (blockIdx.y % p.chunks) * 8 * NT;  // first head of the group
@@ -154,8 +178,14 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
         return;
     }
     const int from = split * p.span, to = min(rq.ctx, from + p.span);
-    if (from >= to && split > 0) return;  // split 0 writes the zeros of an empty cache
     const bool whole = rq.ctx <= p.span;
+    if (from >= to && split > 0) {  // split 0 writes the zeros of an empty cache
+        if (JOINED && !whole) {  // (the others of the cluster count on it)
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
 
     // ---- this warp's pairs of tiles: from / 32 + warp, + kWarps4, ...; a stage each
     if (lane == 0) {
@@ -484,11 +514,46 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
             const float inv = L == 0.f ? 0.f : 1.f / L;
             *reinterpret_cast<uint32_t *>(p.out + (int64_t)r * p.out_stride + ((int64_t)h * p.G + c0 + n) * D + d) =
                 pack_bf16(acc.x * inv, acc.y * inv);
+        } else if (JOINED) {
+            *reinterpret_cast<float2 *>(smem + Sm::kSum + (n * D + d) * 4) = acc;
+            if (d == 0) s_ml[n] = make_float2(M, L);
         } else {
             *reinterpret_cast<float2 *>(p.po + (row * p.S + split) * D + d) = acc;
         }
-        if (d == 0 && (!whole || p.scores)) p.ml[row * p.S + split] = make_float2(M, L);
+        if (!JOINED && d == 0 && (!whole || p.scores)) p.ml[row * p.S + split] = make_float2(M, L);
     }
+    if (!JOINED || whole) return;
+    // ---- each block of the cluster that has keys joins a part of the channels
+    cluster_sync();
+    const int pieces = (rq.ctx + p.span - 1) / p.span;
+    for (int i = split * kWarps4 * 32 + tid; i < 8 * NT * (D / 2); i += pieces * kWarps4 * 32) {
+        const int n = i / (D / 2), d = (i % (D / 2)) * 2;
+        if (c0 + n >= p.G) continue;
+        float2 ml[kMostJoined], part[kMostJoined];
+        float M = neg_inf();
+#pragma unroll
+        for (int k = 0; k < kMostJoined; ++k) {
+            if (k >= pieces) continue;
+            ml[k] = load_of_block(smem_u32(&s_ml[n]), k);
+            part[k] = load_of_block(smem_u32(smem + Sm::kSum + (n * D + d) * 4), k);
+            M = fmaxf(M, ml[k].x);
+        }
+        const float ref = M == neg_inf() ? 0.f : M;
+        float L = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMostJoined; ++k) {
+            if (k >= pieces) continue;
+            const float f = exp2_fast(ml[k].x - ref);
+            L += ml[k].y * f;
+            acc.x += part[k].x * f;
+            acc.y += part[k].y * f;
+        }
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        *reinterpret_cast<uint32_t *>(p.out + (int64_t)r * p.out_stride + ((int64_t)h * p.G + c0 + n) * D + d) =
+            pack_bf16(acc.x * inv, acc.y * inv);
+    }
+    cluster_sync();  // no block leaves while its sums are read
 }
 
 // ------------------------------------------------------ accumulated weights
@@ -582,6 +647,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) finish_kernel(const __grid_co
 
 struct Plan4 {
     int nt, chunks, S, span;
+    bool joined;
     size_t ml, scores, total;  // byte offsets after the partial outputs
     int score_stride;
 };
@@ -599,16 +665,21 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 //    118.9, 10: 94.5, 14: 91.3 (24 x 2048 the same, 64 x 2048 1: 36.2, 3: 37.0).
 //  - No more than 16 pieces, or one per 1024 keys, for the join reads them one
 //    after the other: 1 x 8192 16: 10.6, 64: 15.1; 1 x 28000 32: 17.5, 73: 21.8.
+//  - 8 instead of 9 to 16 where a cluster then joins them (below) and they stay
+//    short: 4 x 4096 8: 11.4, 16: 12.2; 1 x 1601 7.5 and 7.6, 1 x 4096 9.5 and 8.6.
 //  - One piece, and no join, for few keys: 1 x 384 1: 6.1, 3: 6.2; 16 x 600 1:
 //    8.8, 2: 10.2; 1 x 600 1: 8.7, 5: 6.9.
-int64_t pieces(int64_t rows, int32_t max_ctx)
+int64_t pieces(int64_t rows, int32_t max_ctx, bool weights)
 {
     constexpr int64_t kWave = 4 * kPlanSms;
     if (max_ctx <= (rows >= 128 ? 768 : 384)) return 1;
     int64_t n = std::max<int64_t>(1, kWave / rows);
     if (n * rows < kWave * 3 / 4 || max_ctx > n * 2048) n = (2 * kWave + rows - 1) / rows;
     n = std::max(n, std::min<int64_t>((max_ctx + 2047) / 2048, 4 * kWave / rows));
-    return std::min<int64_t>(n, std::max(16, max_ctx / 1024));
+    n = std::min<int64_t>(n, std::max(16, max_ctx / 1024));
+    if (!weights && n > kMostJoined && n <= 16 && max_ctx <= (rows >= 12 ? 4096 : 2048) && rows * kMostJoined <= kWave)
+        n = kMostJoined;
+    return n;
 }
 
 Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
@@ -619,29 +690,42 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     pl.nt = G > 8 && a.head_dim <= 128 ? 2 : 1;
     pl.chunks = (G + 8 * pl.nt - 1) / (8 * pl.nt);
     const int64_t rows = (int64_t)R * a.kv_heads * pl.chunks;
-    const int64_t want = pieces(rows, max_ctx);
+    const int64_t want = pieces(rows, max_ctx, weights);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
     pl.span = (int)std::min<int64_t>(span, 1 << 30);
     pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
     const size_t rq = (size_t)R * a.q_heads;
-    pl.ml = pl.S > 1 ? up256(rq * pl.S * a.head_dim * 4) : 0;
+    // Up to 8 pieces of one wave are clusters, which join them: a launch less (us, 4
+    // requests x 8 KV heads, 1024 keys 7.6 by a second kernel, 7.1; 24 x 2500 keys
+    // 22.6, 21.0).  Not with weights, whose kernel joins on the side (24 x 1024 16.5,
+    // 21.4), nor many clusters of 7, of which an odd number fits (8 x 2500 12.0, 13.0;
+    // 4 x 1601 9.1, 8.3).
+    pl.joined = !weights && pl.S > 1 && pl.S <= kMostJoined && rows * pl.S <= 4 * kPlanSms &&
+                (pl.S != 7 || rows * 7 <= 2 * kPlanSms);
+    pl.ml = pl.S > 1 && !pl.joined ? up256(rq * pl.S * a.head_dim * 4) : 0;
     pl.scores = pl.ml + up256(rq * pl.S * 8);
     pl.score_stride = (G + 1) & ~1;
     pl.total = pl.scores + (weights ? up256((size_t)R * a.kv_heads * max_ctx * pl.score_stride * 4) : 0);
     return pl;
 }
 
-template <int NG, int NT>
-cudaError_t run4(const Decode4Params &p, int32_t R, cudaStream_t s)
+template <int NG, int NT, bool JOINED>
+cudaError_t run4_as(const Decode4Params &p, int32_t R, cudaStream_t s)
 {
     constexpr int bytes = Smem4<NG, NT>::kBytes;
     if (bytes > 48 * 1024) {
-        const cudaError_t e = smem_opt_in(decode4_kernel<NG, NT>, bytes);
+        const cudaError_t e = smem_opt_in(decode4_kernel<NG, NT, JOINED>, bytes);
         if (e != cudaSuccess) return e;
     }
-    return launch_chained(decode4_kernel<NG, NT>, dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R),
-                          kWarps4 * 32, bytes, s, p);
+    return launch_chained_clusters(decode4_kernel<NG, NT, JOINED>, JOINED ? p.S : 1,
+                                   dim3((unsigned)p.S, (unsigned)(p.H * p.chunks), (unsigned)R), kWarps4 * 32, bytes, s, p);
+}
+
+template <int NG, int NT>
+cudaError_t run4(const Decode4Params &p, int32_t R, cudaStream_t s)
+{
+    return p.joined ? run4_as<NG, NT, true>(p, R, s) : run4_as<NG, NT, false>(p, R, s);
 }
 
 cudaError_t launch_decode4(const Decode4Params &p, int nt, int32_t R, cudaStream_t s)
@@ -720,6 +804,7 @@ extern "C" kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const 
     p.out_stride = out_row_stride;
     p.S = pl.S;
     p.span = pl.span;
+    p.joined = pl.joined;
     p.po = reinterpret_cast<float *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
     p.scores = d_weights ? reinterpret_cast<float *>(ws + pl.scores) : nullptr;
@@ -727,7 +812,7 @@ extern "C" kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const 
     p.status = d_status;
     st = cuda_status(launch_decode4(p, pl.nt, R, stream), "kvi_attn_decode4");
     if (st != KVI_OK) return st;
-    if (pl.S == 1 && (!d_weights || max_ctx == 0)) return st;
+    if ((pl.S == 1 || pl.joined) && (!d_weights || max_ctx == 0)) return st;
     WeightParams w{};
     JoinParams &j = w.join;
     j.po = p.po;
@@ -746,7 +831,7 @@ extern "C" kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const 
     j.out = p.out;
     j.out_stride = out_row_stride;
     if (!d_weights) return cuda_status(launch_join(j, stream), "kvi_attn_decode4");
-    w.join_blocks = pl.S > 1 ? (a->q_heads + kJoinWarps - 1) / kJoinWarps : 0;
+    w.join_blocks = pl.S > 1 && !pl.joined ? (a->q_heads + kJoinWarps - 1) / kJoinWarps : 0;
     w.key_blocks = (max_ctx + kKeysBlock - 1) / kKeysBlock;
     w.scores = p.scores;
     w.score_stride = pl.score_stride;

@@ -195,6 +195,26 @@ def test_decode_lengths(ctx, weights):
     c.check()
 
 
+@pytest.mark.parametrize("Hq,H,D", [(8, 2, 64), (8, 2, 128), (40, 2, 128), (9, 1, 256), (6, 3, 96)])
+@pytest.mark.parametrize("most", [400, 600, 1000, 1024, 2000])
+def test_decode_joined_pieces(Hq, H, D, most):
+    """Two to eight pieces a request without weights: requests with all of them, some, one and none."""
+    ctx = [most, 1, 0, most // 2 + 3, 129, most - 1, 128]
+    c = Step(Hq, H, D, 16, ctx, seed=most, weights=False)
+    c.run()
+    c.check()
+    first = c.out.clone()
+    c.run()
+    assert torch.equal(c.out, first)
+    # a request that is refused leaves the others as they are
+    c.out.fill_(7)
+    c.ctx_lens[3] = most + 1
+    c.run()
+    assert int(c.c.status) == kvi.ERR_OUT_OF_RANGE
+    keep = [0, 1, 2, 4, 5, 6]
+    assert torch.equal(c.out[keep], first[keep]) and bool((c.out[3] == 7).all())
+
+
 def test_decode_strides_stream_and_graph():
     c = Step(8, 2, 64, 16, [700, 33], seed=4, wide=3)
     s = torch.cuda.Stream()
