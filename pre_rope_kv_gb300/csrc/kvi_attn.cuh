@@ -80,6 +80,7 @@ struct PromptParams {
     int32_t chunks;             // row chunks per KV head: of each request, or (tiles) of all
     int32_t S, span;
     int32_t per;                // (tiles) tokens of a row tile
+    int32_t joined;             // (rows) a chunk's pieces are a cluster, which joins them
     float *po;
     float2 *ml;
     int32_t *status;
@@ -155,6 +156,24 @@ constexpr float kLn2 = 0.6931471805599453f;
 // inside float32, and the accumulators are rescaled a few times per row
 // instead of once per tile.
 constexpr float kLazy = 8.0f;
+
+constexpr int kMostJoined = 8;  // pieces that a cluster joins
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// What block `rank` of the cluster has at this address of its shared memory.
+__device__ __forceinline__ float2 load_of_block(uint32_t addr, int rank)
+{
+    float2 v;
+    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr), "r"(rank)
+                 : "memory");
+    return v;
+}
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float((int)0xff800000u); }
 

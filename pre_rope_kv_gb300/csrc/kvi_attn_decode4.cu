@@ -115,24 +115,6 @@ __device__ __forceinline__ void load_halves(uint32_t (&w)[(N + 1) / 2], const ui
     }
 }
 
-constexpr int kMostJoined = 8;  // blocks of a cluster
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
-}
-
-// What block `rank` of the cluster has at this address of its shared memory.
-__device__ __forceinline__ float2 load_of_block(uint32_t addr, int rank)
-{
-    float2 v;
-    asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.f32 {%0, %1}, [a];\n\t}"
-                 : "=f"(v.x), "=f"(v.y)
-                 : "r"(addr), "r"(rank)
-                 : "memory");
-    return v;
-}
-
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t *src, uint32_t bytes, uint32_t bar)
 {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),

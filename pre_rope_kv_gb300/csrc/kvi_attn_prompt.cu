@@ -10,8 +10,8 @@
 // O^T = V^T P^T, as with few rows it is K and V that fill the matrix instruction's
 // M.  Each warp streams its own tiles of 16 keys (16-byte asynchronous copies into
 // a ring of its own, so no block-wide wait) and keeps a softmax of its own; the
-// block's warps join at the end, and blocks that share a request's keys join in a
-// second kernel.  Where a block's rows are all there are (decoding steps) the
+// block's warps join at the end, and blocks that share a request's keys through one
+// another's shared memory as a cluster, or in a second kernel.  Where a block's rows are all there are (decoding steps) the
 // cache's bytes bound it: 64 requests x 1.5 k keys, 8 KV heads of 128 channels,
 // 71 us, 5.3 TB/s.
 #include <cuda_runtime.h>
@@ -65,13 +65,14 @@ struct RowsSmem {
     static constexpr int kPitch = DP * 2 + 16;
     static constexpr int kStage = 2 * 16 * kPitch;  // K then V of 16 keys
     static constexpr int kRing = kRowStages * kStage;
-    static constexpr int kJoin = kRowWarps * 8 * NT * (DP + 4) * 4;
+    static constexpr int kSum = kRowWarps * 8 * NT * (DP + 4) * 4;  // then the block's own
+    static constexpr int kJoin = kSum + 8 * NT * DP * 4;
     static constexpr int kBytes = kRowWarps * kRing > kJoin ? kRowWarps * kRing : kJoin;
 };
 
 // DP: the head size rounded up to 32, 64, 128 or 256 (the rest reads as zero);
-// 8 * NT rows per block.
-template <int DP, int NT>
+// 8 * NT rows per block.  JOINED: a chunk's pieces are a cluster, which joins them.
+template <int DP, int NT, bool JOINED>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ PromptParams p)
 {
     using Sm = RowsSmem<DP, NT>;
@@ -79,6 +80,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ uint32_t s_here[kRowWarps][kRowStages];
     __shared__ float s_m[kRowWarps][8 * NT], s_l[kRowWarps][8 * NT];
+    __shared__ float2 s_ml[8 * NT];  // of the block
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
     const int r = blockIdx.y;
@@ -92,7 +94,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     const int rows = rq.n_q * p.G, row0 = chunk * 8 * NT;
     if (row0 >= rows) return;
     const int pieces = max(1, (rq.ctx + p.span - 1) / p.span);
-    if (split >= pieces) return;
+    if (split >= pieces) {
+        if (JOINED && pieces > 1) {  // (the others of the cluster count on it)
+            cluster_sync();
+            cluster_sync();
+        }
+        return;
+    }
     const int seen_by_0 = rq.ctx - rq.n_q;  // last position that token 0 sees
     const int end = min(rq.ctx, seen_by_0 + (min(rows, row0 + 8 * NT) - 1) / p.G + 1);
     const int from = split * p.span, to = min(end, from + p.span);
@@ -334,11 +342,48 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
             *reinterpret_cast<uint32_t *>(p.out + token * p.out_stride + (int64_t)head * p.D + d) =
                 pack_bf16(acc.x * inv, acc.y * inv);
             if (p.lse && d == 0) p.lse[at] = L == 0.f ? neg_inf() : (M + log2f(L)) * kLn2;
+        } else if (JOINED) {
+            *reinterpret_cast<float2 *>(smem + Sm::kSum + (n * DP + d) * 4) = acc;
+            if (d == 0) s_ml[n] = make_float2(M, L);
         } else {
             *reinterpret_cast<float2 *>(p.po + (at * p.S + split) * p.D + d) = acc;
             if (d == 0) p.ml[at * p.S + split] = make_float2(M, L);
         }
     }
+    if (!JOINED || whole) return;
+    // ---- each block of the cluster that has keys joins a part of the channels
+    cluster_sync();
+    for (int i = split * kRowWarps * 32 + tid; i < 8 * NT * half; i += pieces * kRowWarps * 32) {
+        const int n = i / half, d = (i % half) * 2, row = row0 + n;
+        if (row >= rows) break;
+        float2 ml[kMostJoined], part[kMostJoined];
+        float M = neg_inf();
+#pragma unroll
+        for (int k = 0; k < kMostJoined; ++k) {
+            if (k >= pieces) continue;
+            ml[k] = load_of_block(smem_addr(&s_ml[n]), k);
+            part[k] = load_of_block(smem_addr(smem + Sm::kSum + (n * DP + d) * 4), k);
+            M = fmaxf(M, ml[k].x);
+        }
+        const float ref = M == neg_inf() ? 0.f : M;
+        float L = 0.f;
+        float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMostJoined; ++k) {
+            if (k >= pieces) continue;
+            const float f = exp2_fast(ml[k].x - ref);
+            L += ml[k].y * f;
+            acc.x += part[k].x * f;
+            acc.y += part[k].y * f;
+        }
+        const int64_t token = rq.q0 + row / p.G;
+        const int head = h * p.G + row % p.G;
+        const float inv = L == 0.f ? 0.f : 1.f / L;
+        *reinterpret_cast<uint32_t *>(p.out + token * p.out_stride + (int64_t)head * p.D + d) =
+            pack_bf16(acc.x * inv, acc.y * inv);
+        if (p.lse && d == 0) p.lse[token * p.Hq + head] = L == 0.f ? neg_inf() : (M + log2f(L)) * kLn2;
+    }
+    cluster_sync();  // no block leaves while its sums are read
 }
 
 // -------------------------------------------------------------------- host
@@ -350,6 +395,7 @@ struct PromptPlan {
     int dp, nt;
     int64_t chunks;
     int S, span;
+    bool joined;
     size_t ml, total;
 };
 
@@ -382,6 +428,12 @@ PromptPlan plan_rows(const kvi_attention &a, int32_t R, int32_t total_q, int32_t
     // of one token, 512 keys: 14 us in pieces of 128, 12 us in pieces of 256)
     const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
     plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n), 256, 2 * n > kPlanSms ? 256 : 128);
+    // Up to 8 pieces are clusters, which join them, while these find room at once
+    // (three blocks an SM; us, one token, 8 KV heads of 128 channels, by a second
+    // kernel and so: 1 request x 1024 keys 7.5, 6.7; 8 x 700, 384 blocks, 10.0, 8.9;
+    // 8 x 1601, 448 blocks, 12.8, 19.5; 16 x 1024, 512 blocks, 18.4, 20.8).
+    pl.joined = pl.S > 1 && pl.S <= kMostJoined && n * pl.S <= 400;
+    if (pl.joined) pl.ml = pl.total = 0;
     return pl;
 }
 
@@ -422,14 +474,20 @@ size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t 
     return n;
 }
 
+template <int DP, int NT, bool JOINED>
+cudaError_t run_rows_as(const PromptParams &p, int32_t R, cudaStream_t s)
+{
+    const int bytes = RowsSmem<DP, NT>::kBytes;
+    const cudaError_t e = smem_opt_in(rows_kernel<DP, NT, JOINED>, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_chained_clusters(rows_kernel<DP, NT, JOINED>, JOINED ? p.S : 1,
+                                   dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes, s, p);
+}
+
 template <int DP, int NT>
 cudaError_t run_rows(const PromptParams &p, int32_t R, cudaStream_t s)
 {
-    const int bytes = RowsSmem<DP, NT>::kBytes;
-    const cudaError_t e = smem_opt_in(rows_kernel<DP, NT>, bytes);
-    if (e != cudaSuccess) return e;
-    return launch_chained(rows_kernel<DP, NT>, dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes,
-                          s, p);
+    return p.joined ? run_rows_as<DP, NT, true>(p, R, s) : run_rows_as<DP, NT, false>(p, R, s);
 }
 
 cudaError_t launch_rows(const PromptParams &p, const PromptPlan &pl, int32_t R, cudaStream_t s)
@@ -515,12 +573,13 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.chunks = (int)pl.chunks;
     p.S = pl.S;
     p.span = pl.span;
+    p.joined = pl.joined;
     p.po = reinterpret_cast<float *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
     p.status = d_status;
     if (max_q == 0) return KVI_OK;  // no rows
     st = cuda_status(pl.tiles ? launch_tiles(p, stream) : launch_rows(p, pl, R, stream), "kvi_attn_prompt");
-    if (st != KVI_OK || pl.S == 1) return st;
+    if (st != KVI_OK || pl.S == 1 || pl.joined) return st;
     JoinParams j{};
     j.po = p.po;
     j.ml = p.ml;

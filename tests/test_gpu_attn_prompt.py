@@ -97,6 +97,18 @@ def test_single_tokens_many_requests():
     c.check()
 
 
+@pytest.mark.parametrize("Hq,H,D,B", [(8, 2, 64, 16), (8, 2, 128, 16), (6, 1, 256, 8), (7, 1, 96, 48), (4, 4, 32, 5)])
+@pytest.mark.parametrize("most", [300, 600, 1000, 1024])
+def test_joined_pieces(Hq, H, D, B, most):
+    """Few rows over two to eight pieces of the keys: requests with all of them, some, one and none."""
+    c = Case(Hq, H, D, B, [1, 0, 2, 1, 2, 1, 2], [most, 5, 1, most // 2 + 3, most - 1, 0, 128], seed=most)
+    c.run()
+    c.check()
+    first = c.out.clone()
+    c.run()
+    assert torch.equal(c.out, first)
+
+
 @pytest.mark.parametrize("n_q", [[9, 40], [200, 300]])
 def test_strided_rows_without_lse(n_q):
     c = Case(8, 2, 128, 16, n_q, [n + 30 for n in n_q], seed=5, wide=4, lse=False)
