@@ -635,14 +635,14 @@ def cache4(layer_tensors, block_size: int, kv_heads: int, head_dim: int) -> _Cac
     return _Cache4(layer_tensors, block_size, kv_heads, head_dim)
 
 
-_types = None  # (torch.bfloat16, torch.int32, torch.int64), once a call has needed them
+_types = None  # (torch.bfloat16, torch.int32, torch.int64, torch.float32), once a call has needed them
 
 
 def _dtypes():
     global _types
     if _types is None:
         import torch
-        _types = (torch.bfloat16, torch.int32, torch.int64)
+        _types = (torch.bfloat16, torch.int32, torch.int64, torch.float32)
     return _types
 
 
@@ -673,6 +673,17 @@ def _ints(t, n: int, name: str, wide: bool = False):
     return t.data_ptr()
 
 
+def _log_sums(t, rows: int, heads: int):
+    """Address of float32 [rows][heads] (a misaligned one is the library's own
+    to refuse)."""
+    if t is None:
+        return None
+    p = t.data_ptr()
+    if p % 4 == 0 and (t.dtype is not (_types or _dtypes())[3] or t.shape != (rows, heads) or not t.is_contiguous()):
+        raise ValueError(f"lse must be contiguous float32 [{rows}][{heads}]")
+    return p
+
+
 def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
     return load_library().kvi_attn_prompt_workspace_bytes(ctypes.byref(a), int(R), int(total_q),
                                                           int(max_q), int(max_ctx))
@@ -690,8 +701,8 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
     _check(load_library().kvi_attn_prompt(
         ctypes.byref(a), R, qp, qs, _ints(q_start, R + 1, "q_start"), total, max_q,
         _ints(ctx_lens, R, "ctx_lens"), max_ctx, _ints(block_tables, R, "block_tables"),
-        block_tables.shape[1], ctypes.byref(c), layer, op, os_, _ptr(lse), _ptr(ws), ws.nbytes,
-        _ptr(status), _stream(stream)), "kvi_attn_prompt")
+        block_tables.shape[1], ctypes.byref(c), layer, op, os_,
+        _log_sums(lse, total, a.q_heads), _ptr(ws), ws.nbytes, _ptr(status), _stream(stream)), "kvi_attn_prompt")
 
 
 def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:

@@ -1,0 +1,47 @@
+"""Tensors of another kind, type, shape or size than a call takes are refused
+by the binding (no GPU needed).  Every call here also lacks its status word, so
+that nothing is launched whatever the binding lets pass."""
+import pytest
+import torch
+
+import pre_rope_kv_gb300 as kvi
+from pre_rope_kv_gb300 import build as kbuild
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    kbuild.build()
+    return kvi.load_library()
+
+
+def bf16(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32)
+
+
+WS = torch.zeros((32 << 20) + 256, dtype=torch.uint8)
+WS = WS[(-WS.data_ptr()) % 256:]
+
+
+def prompt(a=None, cache=None, lse=None, ws=WS):
+    a = a or kvi.attention(4, 2, 64)
+    kvi.kvi_attn_prompt(a, bf16(3, a.q_heads, a.head_dim), i32(2), 3, i32(1), 8, i32(1, 4),
+                        cache or kvi.paged_cache([bf16(2, 4, 16, 2, 64)], 16), 0, bf16(3, a.q_heads, a.head_dim), ws, None,
+                        lse=lse, stream=0)
+
+
+def test_the_calls_reach_the_library():
+    for lse in (None, torch.zeros(3, 4)):
+        with pytest.raises(kvi.KviError, match="pointer"):
+            prompt(lse=lse)
+
+
+@pytest.mark.parametrize("lse", [torch.zeros(2, 4), torch.zeros(3, 3), torch.zeros(4, 3), torch.zeros(3, 8)[:, ::2],
+                                 torch.zeros(3, 4, dtype=torch.float16), torch.zeros(3, 4, dtype=torch.float64), torch.zeros(0)])
+def test_log_sums(lse):
+    # written as float32 [total_q][q_heads], these would be passed at their end
+    with pytest.raises(ValueError, match="lse"):
+        prompt(lse=lse)
