@@ -326,6 +326,7 @@ class _Cache:
         self.struct = PagedCache(ctypes.cast(self._arr, ctypes.POINTER(ctypes.c_void_p)),
                                  len(ptrs), nb, block_size)
         self.layer_tensors = list(layer_tensors)
+        self.fits = set()  # (layer, kv_heads, head_dim) that attention found its tensor laid out for
 
 
 def paged_cache(layer_tensors, block_size: int) -> _Cache:
@@ -684,6 +685,25 @@ def _log_sums(t, rows: int, heads: int):
     return p
 
 
+def _pool(a: Attention, cache, layer: int) -> PagedCache:
+    """The bf16 pool's struct, where the layer's tensor is one for these heads
+    (an invalid attention or layer is the library's own to refuse)."""
+    if isinstance(cache, _Cache4):
+        raise ValueError("kvi_attn_prompt reads a bf16 pool (paged_cache), not a 4-bit one")
+    if not isinstance(cache, _Cache):
+        return cache  # a struct filled in by the caller
+    c = cache.struct
+    key = (layer, a.kv_heads, a.head_dim)
+    if key not in cache.fits and 0 <= layer < c.layers:
+        t = cache.layer_tensors[layer]
+        want = (2, c.num_blocks, c.block_size, a.kv_heads, a.head_dim)
+        if (t.shape != want or t.element_size() != 2 or not t.is_contiguous()) and \
+                kvi_attn_prompt_workspace_bytes(a, 1, 1, 1, 1):
+            raise ValueError(f"layer {layer} of the cache must be a contiguous bfloat16 {list(want)}, not {list(t.shape)}")
+        cache.fits.add(key)
+    return c
+
+
 def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
     return load_library().kvi_attn_prompt_workspace_bytes(ctypes.byref(a), int(R), int(total_q),
                                                           int(max_q), int(max_ctx))
@@ -694,7 +714,7 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
     """Causal attention of packed prompts over the paged bf16 cache: q and out
     [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
     int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
-    c = cache.struct if hasattr(cache, "struct") else cache
+    c = _pool(a, cache, layer)
     total, R = q.shape[0], ctx_lens.shape[0]
     qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
     op, os_ = _rows(out, a.q_heads, a.head_dim, "out", total)

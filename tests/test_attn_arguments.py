@@ -45,3 +45,28 @@ def test_log_sums(lse):
     # written as float32 [total_q][q_heads], these would be passed at their end
     with pytest.raises(ValueError, match="lse"):
         prompt(lse=lse)
+
+
+@pytest.mark.parametrize("cache", [
+    kvi.paged_cache([bf16(2, 4, 16, 1, 64)], 16), kvi.paged_cache([bf16(2, 4, 16, 2, 32)], 16),
+    kvi.paged_cache([bf16(2, 4, 8, 2, 64)], 16), kvi.paged_cache([bf16(1, 4, 16, 2, 64)], 16),
+    kvi.paged_cache([torch.zeros(2, 4, 16, 2, 64, dtype=torch.uint8)], 16),
+    kvi.paged_cache([bf16(4, 2, 16, 2, 64).transpose(0, 1)], 16)])
+def test_pools_of_another_layout(cache):
+    with pytest.raises(ValueError, match="layer 0"):
+        prompt(cache=cache)
+
+
+def test_pools_of_another_layer():
+    cache = kvi.paged_cache([bf16(2, 4, 16, 2, 64), bf16(2, 3, 16, 2, 64)], 16)
+    with pytest.raises(kvi.KviError, match="pointer"):
+        prompt(cache=cache)
+    with pytest.raises(ValueError, match="layer 1"):
+        kvi.kvi_attn_prompt(kvi.attention(4, 2, 64), bf16(3, 4, 64), i32(2), 3, i32(1), 8, i32(1, 4), cache, 1, bf16(3, 4, 64),
+                            WS, None, stream=0)
+
+
+def test_a_4_bit_pool_is_no_bf16_pool():
+    one = kvi.kvi_cache4_layer_bytes(2, 64, 4, 16)
+    with pytest.raises(ValueError, match="4-bit"):
+        prompt(cache=kvi.cache4([torch.zeros(one, dtype=torch.uint8)], 16, 2, 64))
