@@ -757,8 +757,8 @@ def kvi_attn_decode4_workspace_bytes(a: Attention, R: int, max_ctx: int, weights
 
 def _weights(t, R: int, H: int, name: str):
     shape = t.shape
-    if len(shape) != 3 or shape[0] != R or shape[1] != H or not t.is_contiguous() or t.element_size() != 4:
-        raise ValueError(f"{name} must be contiguous [{R}][{H}][slots] of 4-byte elements")
+    if len(shape) != 3 or shape[0] != R or shape[1] != H or not t.is_contiguous() or t.dtype is not (_types or _dtypes())[3]:
+        raise ValueError(f"{name} must be contiguous float32 [{R}][{H}][slots]")
     return t.data_ptr()
 
 
@@ -791,10 +791,9 @@ def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_t
     R, H = ctx_lens.shape[0], cache.kv_heads
     ptrs = [_weights(weights, R, H, "weights")]
     shape = weights.shape
-    for t in (pos, weights_out, pos_out):
-        if t.shape != shape or not t.is_contiguous() or t.element_size() != 4:
-            raise ValueError("weights and positions, in and out, must be contiguous, of one shape and of "
-                             "4-byte elements")
+    for t, dtype in ((pos, _types[1]), (weights_out, _types[3]), (pos_out, _types[1])):
+        if t.shape != shape or not t.is_contiguous() or t.dtype is not dtype:
+            raise ValueError("weights (float32) and positions (int32), in and out, must be contiguous and of one shape")
         ptrs.append(t.data_ptr())
     _check(load_library().kvi_cache4_evict(
         H, cache.head_dim, R, cache.ref, layer, _ints(ctx_lens, R, "ctx_lens"), max_ctx,

@@ -70,3 +70,33 @@ def test_a_4_bit_pool_is_no_bf16_pool():
     one = kvi.kvi_cache4_layer_bytes(2, 64, 4, 16)
     with pytest.raises(ValueError, match="4-bit"):
         prompt(cache=kvi.cache4([torch.zeros(one, dtype=torch.uint8)], 16, 2, 64))
+
+
+def cache4():
+    return kvi.cache4([torch.zeros(kvi.kvi_cache4_layer_bytes(2, 64, 4, 16), dtype=torch.uint8)], 16, 2, 64)
+
+
+def decode(w=None, ws=WS):
+    kvi.kvi_attn_decode4(kvi.attention(4, 2, 64), bf16(1, 4, 64), i32(1), 8, i32(1, 4), cache4(), 0, bf16(1, 4, 64), ws, None,
+                         weights=w, stream=0)
+
+
+def evict(i=None, bad=None, ws=WS):
+    t = [torch.zeros(1, 2, 40), i32(1, 2, 40), torch.zeros(1, 2, 40), i32(1, 2, 40)]  # weights and positions, in and out
+    if i is not None:
+        t[i] = bad
+    kvi.kvi_cache4_evict(cache4(), 0, i32(1), 40, i32(1, 4), 10, 1, 2, t[0], t[1], t[2], t[3], i32(1), ws, None, stream=0)
+
+
+def test_accumulated_weights_of_another_type():
+    # read and written as float32, whole numbers would be other weights
+    for w in (None, torch.zeros(1, 2, 40)):
+        with pytest.raises(kvi.KviError, match="pointer"):
+            decode(w)
+    with pytest.raises(kvi.KviError, match="pointer"):
+        evict()
+    with pytest.raises(ValueError, match="float32"):
+        decode(i32(1, 2, 40))
+    for i, bad in ((0, i32(1, 2, 40)), (1, torch.zeros(1, 2, 40)), (2, i32(1, 2, 40)), (3, torch.zeros(1, 2, 40))):
+        with pytest.raises(ValueError, match="float32"):
+            evict(i, bad)
