@@ -618,8 +618,8 @@ class _Cache4:
         one = load_library().kvi_cache4_layer_bytes(int(kv_heads), int(head_dim), 1, int(block_size))
         blocks = (layer_tensors[0].numel() * layer_tensors[0].element_size()) // one if one else 0
         for t in layer_tensors:
-            if one and t.numel() * t.element_size() != blocks * one:
-                raise ValueError(f"every layer of a 4-bit cache holds the same number of blocks of {one} bytes")
+            if one and (t.numel() * t.element_size() != blocks * one or not t.is_contiguous()):
+                raise ValueError(f"every layer of a 4-bit cache holds the same number of blocks of {one} bytes, in one piece")
         ptrs = [t.data_ptr() for t in layer_tensors]
         self._arr = (ctypes.c_void_p * len(ptrs))(*ptrs)
         self.struct = PagedCache(ctypes.cast(self._arr, ctypes.POINTER(ctypes.c_void_p)),

@@ -100,3 +100,11 @@ def test_accumulated_weights_of_another_type():
     for i, bad in ((0, i32(1, 2, 40)), (1, torch.zeros(1, 2, 40)), (2, i32(1, 2, 40)), (3, torch.zeros(1, 2, 40))):
         with pytest.raises(ValueError, match="float32"):
             evict(i, bad)
+
+
+def test_4_bit_pools_in_pieces():
+    one = kvi.kvi_cache4_layer_bytes(2, 64, 1, 16)
+    kvi.cache4([torch.zeros(4, one, dtype=torch.uint8)], 16, 2, 64)
+    for pool in (torch.zeros(8, one, dtype=torch.uint8)[::2], torch.zeros(4, 2 * one, dtype=torch.uint8)[:, :one]):
+        with pytest.raises(ValueError, match="in one piece"):
+            kvi.cache4([pool], 16, 2, 64)
