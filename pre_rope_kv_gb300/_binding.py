@@ -674,6 +674,22 @@ def _ints(t, n: int, name: str, wide: bool = False):
     return t.data_ptr()
 
 
+def _scratch(t):
+    """Address and bytes of a workspace."""
+    if not t.is_contiguous():
+        raise ValueError("ws must be contiguous")
+    return t.data_ptr(), t.nbytes
+
+
+def _word(t):
+    """Address of a status word."""
+    if t is None:
+        return None
+    if t.dtype is not (_types or _dtypes())[1] or t.numel() < 1:
+        raise ValueError("status must be int32")
+    return t.data_ptr()
+
+
 def _log_sums(t, rows: int, heads: int):
     """Address of float32 [rows][heads] (a misaligned one is the library's own
     to refuse)."""
@@ -722,7 +738,7 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
         ctypes.byref(a), R, qp, qs, _ints(q_start, R + 1, "q_start"), total, max_q,
         _ints(ctx_lens, R, "ctx_lens"), max_ctx, _ints(block_tables, R, "block_tables"),
         block_tables.shape[1], ctypes.byref(c), layer, op, os_,
-        _log_sums(lse, total, a.q_heads), _ptr(ws), ws.nbytes, _ptr(status), _stream(stream)), "kvi_attn_prompt")
+        _log_sums(lse, total, a.q_heads), *_scratch(ws), _word(status), _stream(stream)), "kvi_attn_prompt")
 
 
 def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:
@@ -737,7 +753,7 @@ def kvi_cache4_write(cache: _Cache4, layer: int, k, v, slots, status, stream=Non
     vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_write(
         cache.kv_heads, cache.head_dim, cache.ref, layer, T, kp, ks, vp, vs,
-        _ints(slots, T, "slots", True), _ptr(status), _stream(stream)), "kvi_cache4_write")
+        _ints(slots, T, "slots", True), _word(status), _stream(stream)), "kvi_cache4_write")
 
 
 def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None) -> None:
@@ -747,7 +763,7 @@ def kvi_cache4_read(cache: _Cache4, layer: int, slots, k, v, status, stream=None
     vp, vs = _rows(v, cache.kv_heads, cache.head_dim, "v", T)
     _check(load_library().kvi_cache4_read(
         cache.kv_heads, cache.head_dim, cache.ref, layer, T,
-        _ints(slots, T, "slots", True), kp, ks, vp, vs, _ptr(status), _stream(stream)), "kvi_cache4_read")
+        _ints(slots, T, "slots", True), kp, ks, vp, vs, _word(status), _stream(stream)), "kvi_cache4_read")
 
 
 def kvi_attn_decode4_workspace_bytes(a: Attention, R: int, max_ctx: int, weights: bool) -> int:
@@ -775,7 +791,7 @@ def kvi_attn_decode4(a: Attention, q, ctx_lens, max_ctx: int, block_tables, cach
     _check(load_library().kvi_attn_decode4(
         ctypes.byref(a), R, qp, qs, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
         _ints(block_tables, R, "block_tables"), block_tables.shape[1], cache.ref, layer, op, os_, wp,
-        0 if weights is None else weights.shape[2], _ptr(ws), ws.nbytes, _ptr(status),
+        0 if weights is None else weights.shape[2], *_scratch(ws), _word(status),
         _stream(stream)), "kvi_attn_decode4")
 
 
@@ -798,8 +814,8 @@ def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_t
     _check(load_library().kvi_cache4_evict(
         H, cache.head_dim, R, cache.ref, layer, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
         _ints(block_tables, R, "block_tables"), block_tables.shape[1], budget, sink, recent, ptrs[0],
-        ptrs[1], shape[2], ptrs[2], ptrs[3], _ints(ctx_out, R, "ctx_out"), _ptr(ws), ws.nbytes,
-        _ptr(status), _stream(stream)), "kvi_cache4_evict")
+        ptrs[1], shape[2], ptrs[2], ptrs[3], _ints(ctx_out, R, "ctx_out"), *_scratch(ws),
+        _word(status), _stream(stream)), "kvi_cache4_evict")
 
 
 def kvi_selftest_bounded_wait(limit_ns: int, status, elapsed_ns=None, stream=None) -> None:

@@ -108,3 +108,27 @@ def test_4_bit_pools_in_pieces():
     for pool in (torch.zeros(8, one, dtype=torch.uint8)[::2], torch.zeros(4, 2 * one, dtype=torch.uint8)[:, :one]):
         with pytest.raises(ValueError, match="in one piece"):
             kvi.cache4([pool], 16, 2, 64)
+
+
+@pytest.mark.parametrize("call", [prompt, decode, evict])
+def test_workspaces_in_pieces(call):
+    with pytest.raises(ValueError, match="ws"):
+        call(ws=WS[:32 << 20].view(-1, 512)[:, :256])
+
+
+def test_status_words_of_another_type():
+    # the kernels write 32 bits
+    k, slots, w, p = bf16(1, 2, 64), torch.zeros(1, dtype=torch.int64), torch.zeros(1, 2, 40), i32(1, 2, 40)
+    a, q, n, table = kvi.attention(4, 2, 64), bf16(1, 4, 64), i32(1), i32(1, 4)
+    none = WS[:0]  # (refused by the library, so that nothing is launched)
+    for bad in (torch.zeros(4, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64), i32(0)):
+        with pytest.raises(ValueError, match="status"):
+            kvi.kvi_attn_prompt(a, q, i32(2), 1, n, 8, table, kvi.paged_cache([bf16(2, 4, 16, 2, 64)], 16), 0, q, none, bad, stream=0)
+        with pytest.raises(ValueError, match="status"):
+            kvi.kvi_attn_decode4(a, q, n, 8, table, cache4(), 0, q, none, bad, stream=0)
+        with pytest.raises(ValueError, match="status"):
+            kvi.kvi_cache4_evict(cache4(), 0, n, 40, table, 10, 1, 2, w, p, w.clone(), p.clone(), i32(1), none, bad, stream=0)
+        with pytest.raises(ValueError, match="status"):
+            kvi.kvi_cache4_write(cache4(), 5, k, k, slots, bad, stream=0)
+        with pytest.raises(ValueError, match="status"):
+            kvi.kvi_cache4_read(cache4(), 5, slots, k, k, bad, stream=0)
