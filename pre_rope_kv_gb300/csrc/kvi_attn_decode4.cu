@@ -284,7 +284,9 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
     int stage = 0;
     uint32_t phase = 0;
     for (int it = 0; it < pairs; ++it) {
-        if (!mbar_wait(smem_u32(&s_bar[warp][stage]), phase, kWait4Ns)) {
+        // (agreed on: what follows wants the whole warp, and a lane alone could give up
+        // where the others find the copy there)
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_bar[warp][stage]), phase, kWait4Ns))) {
             record_status(p.status, KVI_ERR_TIMEOUT);
             break;
         }
