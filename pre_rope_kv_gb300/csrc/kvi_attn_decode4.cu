@@ -382,6 +382,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
                         o[nt][i][c + 2] *= f;
                     }
                 }
+            __syncwarp();  // the next matrix instruction wants the warp as one
         }
         // ---- weights, as B fragments: keys 2 t, 2 t + 1 (and + 8) of head g,
         // in two parts, P = hi + lo, so that P * step rounds to bf16 once

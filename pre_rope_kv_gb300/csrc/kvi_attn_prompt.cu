@@ -241,6 +241,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
                         o[nt][i][c + 2] *= f;
                     }
                 }
+            __syncwarp();  // the next matrix instruction wants the warp as one
         }
         // ---- P rounds to bf16 for the second product; the sum takes it unrounded
         uint32_t b0[NT], b1[NT];
@@ -283,6 +284,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
                                 for (int c = 0; c < 2; ++c)
                                     if (tile * 16 + kk <= last[nt][c]) o[nt][i][2 * j + c] += x;
                         }
+                    __syncwarp();
                 }
             }
 #pragma unroll

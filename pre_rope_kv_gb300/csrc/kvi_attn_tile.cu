@@ -721,6 +721,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             announce(tl.p_full[i][1]);
         }
         // ---- the rows' results; the values have been looked over
+        __syncwarp();  // (a lane of its own announced P; the barrier wants the warp as one)
         asm volatile("bar.sync 1, 288;" ::: "memory");
         if (n > 0 && ok) {
             // (without products of its own the tile's Q may still be on its way, and its
@@ -826,6 +827,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         if (full) {
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
             // (by every warp, whatever became of its waits)
             if (i == 0)
                 asm volatile("bar.sync 3, 128;" ::: "memory");

@@ -16,3 +16,18 @@ def test_decoding_step_agrees_on_its_waits():
     loop = source("kvi_attn_decode4.cu").split("for (int it = 0; it < pairs; ++it)")[1].split("__any_sync")[0]
     waits = re.findall(r"[^\n]*\bmbar_wait\w*\([^\n]*", loop)
     assert len(waits) == 1 and "__all_sync(0xffffffffu, mbar_wait(" in waits[0]
+
+
+def test_warps_come_together_before_aligned_instructions():
+    """Lanes that went their own way (a lane's own store, a column's own rescaling) meet before a barrier or
+    matrix instruction that wants the warp as one."""
+    tile = source("kvi_attn_tile.cu")
+    for name in ("bar.sync 1, 288", "bar.sync 3, 128"):
+        before = tile.split(f'asm volatile("{name};"')[0].rstrip()
+        before = before.removesuffix("if (i == 0)").rstrip()
+        assert before.endswith("__syncwarp();"), name
+    for name in ("kvi_attn_prompt.cu", "kvi_attn_decode4.cu"):
+        rescale = source(name).split("if (__any_sync(0xffffffffu, move)) {")[1].split("pack_bf16(p0, p1)")[0]
+        assert re.search(r"\*= f;\s*}\s*}\s*__syncwarp\(\);\s*}", rescale), name
+    added = source("kvi_attn_prompt.cu").split("if (__any_sync(0xffffffffu, bad != 0)) {")[1].split("mma16816")[0]
+    assert re.search(r"\+= x;\s*}\s*__syncwarp\(\);\s*}", added)
