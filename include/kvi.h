@@ -599,8 +599,8 @@ typedef struct {
     float scale;      /* of the scores, finite and > 0 (usually D^-0.5) */
 } kvi_attention;
 
-/* Device scratch bytes of kvi_attn_prompt for these sizes (as there); 0 for
- * invalid ones. */
+/* Device scratch bytes of kvi_attn_prompt for these sizes (as there) and for
+ * any call that is no larger in any of them; 0 for invalid ones. */
 KVI_API size_t kvi_attn_prompt_workspace_bytes(const kvi_attention *a, int32_t R, int32_t total_q,
                                                int32_t max_q, int32_t max_ctx);
 
@@ -675,8 +675,9 @@ KVI_API kvi_status kvi_cache4_read(int32_t kv_heads, int32_t head_dim, const kvi
                                    int64_t k_row_stride, void *d_v, int64_t v_row_stride,
                                    int32_t *d_status, kvi_stream_t stream);
 
-/* Device scratch bytes of kvi_attn_decode4 for these sizes (weights != 0: with
- * accumulated weights); 0 for invalid ones. */
+/* Device scratch bytes of kvi_attn_decode4 for these sizes and any smaller
+ * ones (weights != 0: with or without accumulated weights); 0 for invalid
+ * ones. */
 KVI_API size_t kvi_attn_decode4_workspace_bytes(const kvi_attention *a, int32_t R, int32_t max_ctx,
                                                 int32_t weights);
 
@@ -696,7 +697,8 @@ KVI_API kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const voi
                                     void *d_ws, size_t ws_bytes, int32_t *d_status,
                                     kvi_stream_t stream);
 
-/* Device scratch bytes of kvi_cache4_evict; 0 for invalid sizes. */
+/* Device scratch bytes of kvi_cache4_evict for these sizes and any smaller
+ * ones; 0 for invalid sizes. */
 KVI_API size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int32_t max_ctx);
 
 /* Cut each request's 4-bit cache of one layer back to at most `budget` slots,

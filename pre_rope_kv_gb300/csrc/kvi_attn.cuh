@@ -46,8 +46,9 @@ struct Page4 {
 // ------------------------------------------------------------------ joining
 
 struct JoinParams {
-    const float *po;         // [rows][S][D]
+    const float *po;         // [rows][S][D], the rows' order as PromptParams has it
     const float2 *ml;        // [rows][S] (m in log2 units, l)
+    int32_t by_request;
     int32_t S, span;         // splits, keys per split
     int32_t R, q_heads, D;
     const int32_t *q_start;  // [R + 1] or null: one row per request
@@ -81,6 +82,10 @@ struct PromptParams {
     int32_t S, span;
     int32_t per;                // (tiles) tokens of a row tile
     int32_t joined;             // (rows) a chunk's pieces are a cluster, which joins them
+    // Partial results of row i of request r: at its place in q, or, where q has
+    // more rows than R * max_q, at r * max_q + i; so they take no more of the
+    // workspace than there can be rows that are split.
+    int32_t by_request;
     float *po;
     float2 *ml;
     int32_t *status;
@@ -321,8 +326,9 @@ __device__ __forceinline__ void join_rows(const JoinParams &p, int x, int r)
     const int64_t i = (int64_t)x * kJoinWarps + (threadIdx.x >> 5);
     if (i >= (int64_t)q.n_q * p.q_heads) return;
     const int64_t row = (int64_t)q.q0 * p.q_heads + i;
-    const float2 *ml = p.ml + row * p.S;
-    const float *po = p.po + row * p.S * p.D;
+    const int64_t part = p.by_request ? (int64_t)r * p.max_q * p.q_heads + i : row;
+    const float2 *ml = p.ml + part * p.S;
+    const float *po = p.po + part * p.S * p.D;
     const int d0 = 4 * lane;
     // eight pieces' outputs are asked for before the sums are known
     constexpr int kAhead = 8;

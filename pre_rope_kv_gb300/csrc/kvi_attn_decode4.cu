@@ -654,10 +654,12 @@ size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
 //    short: 4 x 4096 8: 11.4, 16: 12.2; 1 x 1601 7.5 and 7.6, 1 x 4096 9.5 and 8.6.
 //  - One piece, and no join, for few keys: 1 x 384 1: 6.1, 3: 6.2; 16 x 600 1:
 //    8.8, 2: 10.2; 1 x 600 1: 8.7, 5: 6.9.
+constexpr int64_t kWave = 4 * kPlanSms;
+constexpr int kAlone = 384, kLongest = 1 << 30;  // keys that are never split, and of a piece at most
+
 int64_t pieces(int64_t rows, int32_t max_ctx, bool weights)
 {
-    constexpr int64_t kWave = 4 * kPlanSms;
-    if (max_ctx <= (rows >= 128 ? 768 : 384)) return 1;
+    if (max_ctx <= (rows >= 128 ? 2 * kAlone : kAlone)) return 1;
     int64_t n = std::max<int64_t>(1, kWave / rows);
     if (n * rows < kWave * 3 / 4 || max_ctx > n * 2048) n = (2 * kWave + rows - 1) / rows;
     n = std::max(n, std::min<int64_t>((max_ctx + 2047) / 2048, 4 * kWave / rows));
@@ -678,7 +680,7 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     const int64_t want = pieces(rows, max_ctx, weights);
     int64_t span = (max_ctx + want - 1) / want;
     span = std::max<int64_t>(128, (span + 127) / 128 * 128);
-    pl.span = (int)std::min<int64_t>(span, 1 << 30);
+    pl.span = (int)std::min<int64_t>(span, kLongest);
     pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
     const size_t rq = (size_t)R * a.q_heads;
     // Up to 8 pieces of one wave are clusters, which join them: a launch less (us, 4
@@ -693,6 +695,22 @@ Plan4 plan4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
     pl.score_stride = (G + 1) & ~1;
     pl.total = pl.scores + (weights ? up256((size_t)R * a.kv_heads * max_ctx * pl.score_stride * 4) : 0);
     return pl;
+}
+
+// Workspace for these sizes and any smaller ones: fewer requests are cut into more
+// pieces, so what a call needs does not go by its sizes, but with more than one
+// piece a request there are 4 waves of blocks at most (`pieces`), and 16 pieces or
+// one per 1024 keys.
+size_t bytes4(const kvi_attention &a, int32_t R, int32_t max_ctx, bool weights)
+{
+    const Plan4 pl = plan4(a, R, max_ctx, weights);  // (its chunks and score rows go by the heads alone)
+    int64_t parts = max_ctx > kLongest ? 2 * (int64_t)R : 0;
+    if (max_ctx > kAlone)
+        parts = std::max(parts, std::min(R * std::min<int64_t>(std::max(16, max_ctx / 1024), ((int64_t)max_ctx + 127) / 128),
+                                         4 * kWave / ((int64_t)a.kv_heads * pl.chunks)));
+    const size_t rows = (size_t)std::max<int64_t>(R, parts) * a.q_heads;
+    return up256((size_t)parts * a.q_heads * a.head_dim * 4) + up256(rows * 8) +
+           (weights ? up256((size_t)R * a.kv_heads * max_ctx * pl.score_stride * 4) : 0);
 }
 
 template <int NG, int NT, bool JOINED>
@@ -741,7 +759,7 @@ using namespace kvi;
 extern "C" size_t kvi_attn_decode4_workspace_bytes(const kvi_attention *a, int32_t R, int32_t max_ctx, int32_t weights)
 {
     if (check_attention(a) != KVI_OK || !sizes_ok(a, R, max_ctx)) return 0;
-    return plan4(*a, R, max_ctx, weights != 0).total;
+    return bytes4(*a, R, max_ctx, weights != 0);
 }
 
 extern "C" kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,

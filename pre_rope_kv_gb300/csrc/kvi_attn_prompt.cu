@@ -348,8 +348,9 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
             *reinterpret_cast<float2 *>(smem + Sm::kSum + (n * DP + d) * 4) = acc;
             if (d == 0) s_ml[n] = make_float2(M, L);
         } else {
-            *reinterpret_cast<float2 *>(p.po + (at * p.S + split) * p.D + d) = acc;
-            if (d == 0) p.ml[at * p.S + split] = make_float2(M, L);
+            const int64_t part = ((p.by_request ? (int64_t)r * p.max_q : rq.q0) + row / p.G) * p.Hq + head;
+            *reinterpret_cast<float2 *>(p.po + (part * p.S + split) * p.D + d) = acc;
+            if (d == 0) p.ml[part * p.S + split] = make_float2(M, L);
         }
     }
     if (!JOINED || whole) return;
@@ -401,18 +402,24 @@ struct PromptPlan {
     size_t ml, total;
 };
 
+constexpr int kLongest = 1 << 30;              // keys of a piece at most
+constexpr int kRowsWanted = 4 * kPlanSms;      // blocks of the rows form
+constexpr int kRowsAlone = 256, kTilesAlone = 384;
+
+// Rows whose partial results are kept: of q, but no more than the requests have
+int64_t part_rows(int32_t R, int32_t total_q, int32_t max_q) { return std::min<int64_t>(total_q, (int64_t)R * max_q); }
+
 // `splits` pieces of the keys are wanted, none below `least` keys, and none at
 // all up to `alone` keys, which cost no more than the join does (2 us).
-void plan_split(PromptPlan &pl, const kvi_attention &a, int32_t total_q, int32_t max_ctx, int64_t splits, int alone,
-                int least)
+void plan_split(PromptPlan &pl, const kvi_attention &a, int64_t rows, int32_t max_ctx, int64_t splits, int alone, int least)
 {
     if (max_ctx <= alone) splits = 1;
     int64_t span = (max_ctx + splits - 1) / splits;
     span = std::max<int64_t>(least, (span + 127) / 128 * 128);
-    pl.span = (int)std::min<int64_t>(span, 1 << 30);
+    pl.span = (int)std::min<int64_t>(span, kLongest);
     pl.S = std::max(1, (int)(((int64_t)max_ctx + pl.span - 1) / pl.span));
     if (pl.S > 1) {
-        const size_t n_rows = (size_t)total_q * a.q_heads;
+        const size_t n_rows = (size_t)rows * a.q_heads;
         pl.ml = up256(n_rows * pl.S * a.head_dim * 4);
         pl.total = pl.ml + up256(n_rows * pl.S * 8);
     }
@@ -429,7 +436,8 @@ PromptPlan plan_rows(const kvi_attention &a, int32_t R, int32_t total_q, int32_t
     // blocks for four on every SM; short ones only where there are few (16 requests
     // of one token, 512 keys: 14 us in pieces of 128, 12 us in pieces of 256)
     const int64_t n = (int64_t)R * a.kv_heads * pl.chunks;
-    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, (4 * kPlanSms + n - 1) / n), 256, 2 * n > kPlanSms ? 256 : 128);
+    plan_split(pl, a, part_rows(R, total_q, max_q), max_ctx, std::max<int64_t>(1, (kRowsWanted + n - 1) / n), kRowsAlone,
+               2 * n > kPlanSms ? 256 : 128);
     // Up to 8 pieces are clusters, which join them, while these find room at once
     // (three blocks an SM; us, one token, 8 KV heads of 128 channels, by a second
     // kernel and so: 1 request x 1024 keys 7.5, 6.7; 8 x 700, 384 blocks, 10.0, 8.9;
@@ -448,7 +456,7 @@ PromptPlan plan_tiles(const kvi_attention &a, int32_t R, int32_t total_q, int32_
     pl.chunks = std::max<int64_t>(1, std::min((int64_t)R * ((max_q + (int64_t)per - 1) / per), total_q / per + (int64_t)R));
     // a block for every SM
     const int64_t n = (int64_t)a.kv_heads * pl.chunks;
-    plan_split(pl, a, total_q, max_ctx, std::max<int64_t>(1, kPlanSms / n), 384, 128);
+    plan_split(pl, a, part_rows(R, total_q, max_q), max_ctx, std::max<int64_t>(1, kPlanSms / n), kTilesAlone, 128);
     return pl;
 }
 
@@ -468,12 +476,22 @@ bool tiles_fit(const kvi_attention &a, int32_t R, int32_t max_q, int32_t max_ctx
     return rows > 32 && (max_ctx > 256 || (int64_t)R * a.kv_heads * rows > 8192);
 }
 
-// Workspace for whichever form the cache's pages decide on.
+// Workspace for whichever form the cache's pages decide on, and for any smaller
+// call: fewer rows are split into more pieces, so what a call needs does not go by
+// its sizes, but pieces times blocks are bounded.  With n blocks before the split:
+//   rows form: more than one piece only for n < kRowsWanted, and n S <= kRowsWanted
+//   + n - 1 then; the rows of a block are 8 nt, of all KV heads together;
+//   tiles: n S <= kPlanSms, and no more than `per` tokens of G heads a block.
+// Also no row has more pieces than there are 128 keys.
 size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
 {
-    size_t n = std::max<size_t>(256, plan_rows(a, R, total_q, max_q, max_ctx).total);
-    if (tiles_fit(a, R, max_q, max_ctx, 1, 8)) n = std::max(n, plan_tiles(a, R, total_q, max_q, max_ctx).total);
-    return n;
+    const int64_t G = a.q_heads / a.kv_heads, rows = part_rows(R, total_q, max_q) * a.q_heads;
+    const int64_t pieces = ((int64_t)max_ctx + 127) / 128;
+    int64_t parts = max_ctx > kLongest ? 2 * rows : 0;
+    auto at_most = [&](int64_t cap) { parts = std::max(parts, rows > cap ? cap : std::min(rows * pieces, cap)); };
+    if (max_ctx > kRowsAlone) at_most(8 * (a.head_dim <= 128 && max_q * G > 8 ? 2 : 1) * (2 * kRowsWanted - 2));
+    if (max_ctx > kTilesAlone && tiles_fit(a, R, max_q, max_ctx, 1, 8)) at_most(2 * tile_tokens((int)G) * G * kPlanSms);
+    return std::max<size_t>(256, up256((size_t)parts * a.head_dim * 4) + up256((size_t)parts * 8));
 }
 
 template <int DP, int NT, bool JOINED>
@@ -543,7 +561,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     const PromptPlan pl = tiles_fit(*a, R, max_q, max_ctx, cache->num_blocks, cache->block_size)
                               ? plan_tiles(*a, R, total_q, max_q, max_ctx)
                               : plan_rows(*a, R, total_q, max_q, max_ctx);
-    const size_t need = prompt_bytes(*a, R, total_q, max_q, max_ctx);
+    const size_t need = std::max<size_t>(256, pl.total);
     if (pl.chunks * pl.S * a->kv_heads > 0x7fffffff || (int64_t)max_q * (a->q_heads / a->kv_heads) > (1 << 30))
         return arg_error("max_q=%d is too large for this call", max_q);
     if (!d_ws || ws_bytes < need || reinterpret_cast<uintptr_t>(d_ws) % 256)
@@ -576,6 +594,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     p.S = pl.S;
     p.span = pl.span;
     p.joined = pl.joined;
+    p.by_request = total_q > (int64_t)R * max_q;
     p.po = reinterpret_cast<float *>(ws);
     p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
     p.status = d_status;
@@ -585,6 +604,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
     JoinParams j{};
     j.po = p.po;
     j.ml = p.ml;
+    j.by_request = p.by_request;
     j.S = pl.S;
     j.span = pl.span;
     j.R = R;

@@ -739,6 +739,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (ok) {
             const int head = h * p.G + row % p.G;
             const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
+            const int64_t part = ((p.by_request ? (int64_t)r * p.max_q : rq.q0) + token) * p.Hq + head;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
             // 32 channels of the row
@@ -783,7 +784,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 uint4 *stage = reinterpret_cast<uint4 *>(base + Sm::kQ + i * Sm::kTile) + (warp & 3) * 32 * kPieces;
                 const uint64_t mine = reinterpret_cast<uint64_t>(
                     whole ? static_cast<void *>(p.out + tok * p.out_stride + (int64_t)head * p.D)
-                          : static_cast<void *>(p.po + (at * p.S + split) * p.D));
+                          : static_cast<void *>(p.po + (part * p.S + split) * p.D));
                 const uint32_t rows_there = __ballot_sync(0xffffffffu, real);
 #pragma unroll 1
                 for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
@@ -820,7 +821,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (real) {
                 const float M = m * p.scale;
                 if (!whole)
-                    p.ml[at * p.S + split] = make_float2(M, sum);
+                    p.ml[part * p.S + split] = make_float2(M, sum);
                 else if (p.lse)
                     p.lse[at] = sum == 0.f ? neg_inf() : (M + log2f(sum)) * kLn2;
             }

@@ -1,6 +1,8 @@
 """Tensors of another kind, type, shape or size than a call takes are refused
 by the binding (no GPU needed).  Every call here also lacks its status word, so
 that nothing is launched whatever the binding lets pass."""
+import random
+
 import pytest
 import torch
 
@@ -132,3 +134,49 @@ def test_status_words_of_another_type():
             kvi.kvi_cache4_write(cache4(), 5, k, k, slots, bad, stream=0)
         with pytest.raises(ValueError, match="status"):
             kvi.kvi_cache4_read(cache4(), 5, slots, k, k, bad, stream=0)
+
+
+def grows(size, larger, smaller):
+    assert size(*larger) >= size(*smaller) > 0, (larger, smaller)
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(32, 8, 128), (8, 2, 64), (16, 1, 256), (128, 1, 96), (5, 5, 32)])
+def test_a_workspace_serves_smaller_calls(q_heads, kv_heads, head_dim):
+    """A program sizes its workspace once, for the largest call it makes."""
+    a, rng = kvi.attention(q_heads, kv_heads, head_dim), random.Random(head_dim)
+
+    def up_to(n):
+        return min(n, max(1, int(round(n ** rng.random()))))
+
+    def prompt_bytes(R, total, max_q, ctx):
+        return kvi.kvi_attn_prompt_workspace_bytes(a, R, total, max_q, ctx)
+
+    def decode_bytes(R, ctx, weights):
+        return kvi.kvi_attn_decode4_workspace_bytes(a, R, ctx, weights)
+
+    def evict_bytes(R, ctx):
+        return kvi.kvi_cache4_evict_workspace_bytes(kv_heads, R, ctx)
+
+    # a step longer, a request more; one prompt, and a question after it; an eviction and the step after it
+    grows(decode_bytes, (1, 2049, True), (1, 2048, True))
+    grows(decode_bytes, (64, 8192, False), (4, 8192, False))
+    grows(decode_bytes, (18, 6357, True), (18, 6086, True))
+    grows(prompt_bytes, (1, 8192, 8192, 8192), (1, 37, 37, 1601))
+    for _ in range(4000):
+        R, ctx, max_q = up_to(256), up_to(60000), up_to(5000)
+        total = rng.randint(max_q, R * max_q) if rng.random() < 0.7 else max_q + up_to(60000)
+        r, c = (R if rng.random() < 0.3 else up_to(R)), (ctx if rng.random() < 0.3 else up_to(ctx))
+        t = total if rng.random() < 0.3 else up_to(total)
+        m = min(max_q, t) if rng.random() < 0.3 else up_to(min(max_q, t))
+        grows(prompt_bytes, (R, total, max_q, ctx), (r, t, m, c))
+        w = rng.random() < 0.5
+        grows(decode_bytes, (R, ctx, w), (r, c, w and rng.random() < 0.5))
+        grows(evict_bytes, (R, ctx), (r, c))
+
+
+def test_workspaces_stay_small():
+    # pieces of a few rows, however large the call or the buffer q lies in
+    a = kvi.attention(32, 8, 128)
+    for sizes in ((1, 8192, 8192, 8192), (64, 100000, 8192, 32768), (1, 100000, 1, 100000), (1000, 100000, 37, 4000)):
+        assert kvi.kvi_attn_prompt_workspace_bytes(a, *sizes) < 24 << 20
+    assert kvi.kvi_attn_decode4_workspace_bytes(a, 1000, 100000, False) < 8 << 20
