@@ -77,6 +77,7 @@ struct TileTail {
     int32_t odd;            // `first` holds something
     int32_t lost;           // a key's block lies outside the pool
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
+    int32_t part0;          // row of token 0 among the partial results
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -398,6 +399,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int n = max(n_tiles[0], n_tiles[1]);
     const int sure = seen0 + tok0 + 1;  // keys below it are seen by every row
     const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+
+    if (tid == 0) tl.part0 = p.by_request ? r * p.max_q : rq.q0;  // (below total_q; here, as r is not kept to the end)
 
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
@@ -739,7 +742,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (ok) {
             const int head = h * p.G + row % p.G;
             const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
-            const int64_t part = ((p.by_request ? (int64_t)r * p.max_q : rq.q0) + token) * p.Hq + head;
+            const int64_t part = ((int64_t)tl.part0 + token) * p.Hq + head;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
             // 32 channels of the row
