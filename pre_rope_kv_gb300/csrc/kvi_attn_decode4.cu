@@ -252,9 +252,10 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // 2^(13 - e) and 2^(e - 13) of a largest element in [2^e, 2^(e + 1)); e is
-        // kept where both are normal numbers (an infinity or NaN stays one)
-        const int e = min(max((int)(top >> 7) - 127, -100), 100);
+        // 2^(13 - e) and 2^(e - 13) of a largest element in [2^e, 2^(e + 1)); both are
+        // normal numbers for any finite q (an infinity or NaN stays one), and heads
+        // below 2^-100 are taken as if they reached it, for kLazy / scale
+        const int e = min(max((int)(top >> 7) - 127, -100), 127);
         const float up = __int_as_float((127 + 13 - e) << 23), down = __int_as_float((127 - 13 + e) << 23);
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
