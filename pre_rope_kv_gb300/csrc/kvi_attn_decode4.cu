@@ -266,7 +266,8 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
             qf[nt][2 * j + 1][1] = pack_f16(bf16_hi(v[j].y) * up, bf16_hi(v[j].w) * up);  // 3, 7
         }
 #pragma unroll
-        for (int c = 0; c < 2; ++c) scale[nt][c] = p.scale * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c));
+        for (int c = 0; c < 2; ++c)  // (never 0, or a masked score would be NaN: 0 * inf)
+            scale[nt][c] = fmaxf(p.scale * __shfl_sync(0xffffffffu, down, 4 * (2 * t + c)), 1.1754944e-38f);
     }
     float o[NT][2 * NG][4];
     // per column (head): the score that moves the reference (-inf while there is

@@ -22,3 +22,14 @@ def test_large_queries(Hq, H, D, e):
     assert bool(torch.isfinite(c.q).all())
     c.run()
     c.check()
+
+
+@pytest.mark.parametrize("q", [0.0, 2.0 ** -120])
+@pytest.mark.parametrize("scale", [1e-6, 1e-20, 1e-38])
+def test_small_queries_and_scales(q, scale):
+    """Scores of next to nothing: every key weighs the same, and a masked one nothing."""
+    c = Step(4, 2, 64, 16, [5, 200, 33], seed=1)
+    c.a = kvi.attention(4, 2, 64, scale=scale)
+    c.q = torch.full_like(c.q, q)
+    c.run()
+    c.check()  # (its own scale matters as little)
