@@ -118,8 +118,9 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 // Every kernel of these calls may begin while the previous kernel of the
 // stream drains, waits for it before it touches memory (pdl_wait), and lets
 // the next one begin (pdl_launch_dependents): what a launch costs is hidden
-// behind the work before it.  `blocks` > 1: the blocks along x form clusters of so
-// many.
+// behind the work before it.  What they read may thus be written during their
+// lifetime, so none of it goes through the read-only path (__ldg).  `blocks` > 1:
+// the blocks along x form clusters of so many.
 template <typename P, typename... Args>
 inline cudaError_t launch_chained_clusters(void (*kernel)(P, Args...), int blocks, dim3 grid, dim3 block, size_t smem,
                                            cudaStream_t s, const std::decay_t<P> &p, const std::decay_t<Args> &...args)

@@ -195,7 +195,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
                               (part == 0 ? 0 : part == 1 ? p.page.v_codes() : part == 2 ? p.page.k_steps() : p.page.v_steps());
     int c_tile = 2 * pair0 + ((lane >> 2) & 1), c_page = c_tile / per_page, c_sub = c_tile % per_page;
     const int d_page = 2 * kWarps4 / per_page, d_sub = 2 * kWarps4 % per_page;
-    int c_block = c_tile < t1 ? __ldg(table + c_page) : -1;
+    int c_block = c_tile < t1 ? table[c_page] : -1;
     int issued = 0;     // stages that copies went out for
     uint32_t dead = 0;  // bits 2 stage, + 1: a tile whose block lies outside the pool
     auto issue = [&](int stage) {
@@ -222,7 +222,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
             c_sub -= per_page;
             ++c_page;
         }
-        c_block = c_tile < t1 ? __ldg(table + c_page) : -1;
+        c_block = c_tile < t1 ? table[c_page] : -1;
     };
     const int pairs = max(0, ((t1 + 1) / 2 - pair0 + kWarps4 - 1) / kWarps4);  // of this warp
 #pragma unroll
@@ -245,7 +245,7 @@ decode4_kernel(const __grid_constant__ Decode4Params p)
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
             v[j] = make_uint4(0, 0, 0, 0);
-            if (head < p.G) v[j] = __ldg(reinterpret_cast<const uint4 *>(q + 32 * j));
+            if (head < p.G) v[j] = *reinterpret_cast<const uint4 *>(q + 32 * j);
             const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));

@@ -410,7 +410,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     int at_token = 0, at_block = 0;
     auto block_of = [&](int j) {
         const int key = from + j * kM + box * box_keys;
-        return key < rq.ctx ? __ldg(table + (uint32_t)key / (uint32_t)p.B) : -1;
+        return key < rq.ctx ? table[(uint32_t)key / (uint32_t)p.B] : -1;
     };
     auto look_up = [&](int j, int block) {
         const int key = from + j * kM + box * box_keys;

@@ -31,3 +31,9 @@ def test_warps_come_together_before_aligned_instructions():
         assert re.search(r"\*= f;\s*}\s*}\s*__syncwarp\(\);\s*}", rescale), name
     added = source("kvi_attn_prompt.cu").split("if (__any_sync(0xffffffffu, bad != 0)) {")[1].split("mma16816")[0]
     assert re.search(r"\+= x;\s*}\s*__syncwarp\(\);\s*}", added)
+
+
+def test_nothing_is_read_as_read_only():
+    """These kernels begin while the previous one may still write what they read."""
+    for name in ("kvi_attn.cuh", "kvi_attn_prompt.cu", "kvi_attn_tile.cu", "kvi_attn_decode4.cu", "kvi_attn_join.cu", "kvi_cache4.cu"):
+        assert not re.search(r"__ldg\b|ld\.global\.nc", source(name)), name
