@@ -23,6 +23,8 @@
 
 namespace kvi {
 
+constexpr int kPlanSms = 152;  // SMs that work is shared out over
+
 // ------------------------------------------------------- 4-bit page layout
 //
 // One page holds B tokens (a multiple of 16) of one KV head: the codes of K

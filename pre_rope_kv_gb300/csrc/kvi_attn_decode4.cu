@@ -28,8 +28,9 @@
 //
 // What bounds it is the decoding, not the bytes: with the softmax a tile of 2304
 // bytes (D = 128) takes nearly 400 warp instructions, and HBM delivers a tile in
-// the time of 390; 128 registers leave 16 warps an SM, which fill two thirds of
-// the issue slots.  Measured at 16 requests x 28 k keys, D = 128, 8 KV heads (0.53
+// the time of 390.  128 registers leave 16 warps an SM, four a scheduler, and an
+// iteration is a chain (scores, softmax, weights, output): two thirds of the issue
+// slots are used, the rest goes into its fixed latencies and the ALU pipe (59 %).  Measured at 16 requests x 28 k keys, D = 128, 8 KV heads (0.53
 // GB): 125 us, 4.2 TB/s.  On the way there: one tile an iteration 152 us; two,
 // which share the bookkeeping and run independently of one another, 140, later
 // 132; K in f16 129; more and shorter pieces 125.  Against the 140:
@@ -49,7 +50,6 @@ namespace {
 constexpr int kWarps4 = 4;
 constexpr int kStages4 = 2;  // pairs of tiles of 16 keys that a warp has in flight
 constexpr uint64_t kWait4Ns = 1000000000ull;
-constexpr int kPlanSms = 152;
 
 struct Decode4Params {
     const __nv_bfloat16 *q;
@@ -578,8 +578,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) finish_kernel(const __grid_co
     if (!request_span(r, nullptr, jp.total_q, 1, jp.ctx_lens, jp.max_ctx, jp.max_blocks, jp.block_size, rq)) return;
     const int key0 = (x % p.key_blocks) * kKeysBlock;
     if (key0 >= rq.ctx) return;
-    // the scores of two keys and up to eight heads are asked for before the sums
-    // that they are measured against
+    // the scores of a thread's keys, up to eight heads of each, are asked for before
+    // the sums that they are measured against
     const float *sc = p.scores + ((int64_t)r * p.H + h) * jp.max_ctx * p.score_stride;
     float *w = p.w + ((int64_t)r * p.H + h) * p.stride;
     constexpr int kAhead = 4;

@@ -55,7 +55,6 @@ struct RowParams {
 };
 
 constexpr int kRowThreads = 256;
-constexpr int kPlanSms4 = 152;
 
 // The 16-bit pieces of channels 32 g + 4 s .. + 3 of the token at `off`.
 __device__ __forceinline__ int64_t k_piece(const Page4 &pg, int off, int g, int s)
@@ -336,8 +335,8 @@ __global__ void __launch_bounds__(kRowThreads, 6) cache4_read_kernel(const __gri
 // Per request and head: the budget-th largest rank is found 11 bits at a time
 // (three counting passes over the ranks), then one ordered pass marks the kept
 // slots (ties in slot order) and lists the freed slots below the budget and
-// the kept ones above it.  Both lists have the same length; the second
-// kernel copies row for row.
+// the kept ones above it.  Both lists have the same length; the rows are moved
+// by the same block, or, where heads are few and rows many, by a second kernel.
 
 struct EvictParams {
     int32_t R, H, budget, sink, recent;
@@ -404,6 +403,16 @@ __device__ __forceinline__ int warp_sum_before(int v, int *warp_sums)
 
 // One moved row, by eight lanes (`lane`); 16-bit pieces, as two tokens share each
 // word of the V codes and steps.
+//
+// What moving costs is latency: a turn is a chain of list, block table and page,
+// with nothing asked for ahead.  Neither HBM (29 % of its peak) nor the issue slots
+// (48 %) are full.  A pair of tokens' V is D contiguous bytes, at D = 128 four
+// sectors, and each of a lane's G two-byte loads and stores touches them all again.
+// 64 requests x 8 KV heads, 1.9 to 4.1 k -> 2000 slots, D = 128: 62 us with the
+// finding, in 1.7 waves of blocks (64 registers at 512 threads leave two an SM).
+// Moved by a second kernel, 3000 -> 2000 slots took 61 us, of which finding them 19;
+// with two rows a thread at once 70, with 32 or 56 registers a thread instead of 48
+// 63 to 67.
 __device__ __forceinline__ void move_row(const EvictParams &p, const int32_t *table, int h, int dst, int src, int lane)
 {
     const int G = p.page.groups();
@@ -613,11 +622,7 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const __grid_cons
     }
 }
 
-// What bounds moving is the pages' sectors: a row's V lies in 2-byte pieces over
-// all 32 sectors of its pair tile, each read and partly written.  64 requests x
-// 8 KV heads, 3000 -> 2000 slots, D = 128 (340 k rows moved): 61 us, of which
-// finding them takes 19; two rows a thread at once 70, 32 or 56 registers a
-// thread instead of 48 63 to 67.
+// The rows of few heads that have many each.
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p)
 {
     pdl_wait();
@@ -695,7 +700,7 @@ void row_shape(RowParams &p, dim3 &grid, dim3 &block)
     // 8 heads of 128 channels: 65 k rows 145 us with one head a thread, 123 with two,
     // 117 with four, 153 with eight; 64 rows 5.5 us with one, 13 with four)
     const int64_t threads = (p.T / 2 + 1) * p.H * (p.D / 8);
-    p.heads_apart = threads <= (int64_t)kPlanSms4 * 2048 ? p.H : (p.H + 3) / 4;
+    p.heads_apart = threads <= (int64_t)kPlanSms * 2048 ? p.H : (p.H + 3) / 4;
     p.lanes = p.heads_apart * (p.D / 8);  // a multiple of 4: a group never leaves its warp
     // whole warps: eight pairs together are one, or a pair is rounded up
     const int x = p.lanes <= 32 ? p.lanes : std::min((p.lanes + 31) & ~31, kRowThreads);
