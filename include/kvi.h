@@ -686,7 +686,8 @@ KVI_API size_t kvi_attn_decode4_workspace_bytes(const kvi_attention *a, int32_t 
  * 0 .. d_ctx_lens[r]-1 of block table row r.  d_out as d_q.  With d_weights
  * (float32 [R][H][weights_stride]) the softmax weight of every slot, summed
  * over the query heads of its KV head, is added to d_weights[r][h][slot]:
- * the score kvi_cache4_evict ranks by.  d_ws and the device-side errors are as
+ * the score kvi_cache4_evict ranks by.  Stored keys are smaller than 2^100 (the
+ * products of a group are taken of q scaled to 2^13, in float32).  d_ws and the device-side errors are as
  * for kvi_attn_prompt.  Errors: KVI_ERR_INVALID_ARG (also weights_stride <
  * max_ctx), KVI_ERR_CUDA. */
 KVI_API kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const void *d_q,
@@ -710,6 +711,9 @@ KVI_API size_t kvi_cache4_evict_workspace_bytes(int32_t kv_heads, int32_t R, int
  * i-th such row); the others stay where they are, so attention over the slots
  * 0 .. min(ctx, budget)-1 sees exactly the kept keys (their rotary positions
  * are in the keys already).  Rows at slots >= budget are read, never written.
+ * Rows move in place, so a block of an evicted request belongs to it alone: none
+ * that another request's table holds too (a shared prefix is copied first), and
+ * none that stands twice among the table entries of its ctx slots.
  *   d_weights, d_pos          float32 / int32 [R][H][stride], read
  *   d_weights_out, d_pos_out  likewise, written for slots < ctx: those of the
  *                             kept rows, then 0 and -1; other buffers than

@@ -803,7 +803,8 @@ def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_t
                      sink: int, recent: int, weights, pos, weights_out, pos_out, ctx_out, ws, status,
                      stream=None) -> None:
     """Cut a layer of the 4-bit cache back to `budget` slots per request and
-    head by accumulated weight (weights float32, pos int32: [R][H][slots])."""
+    head by accumulated weight (weights float32, pos int32: [R][H][slots]).  In
+    place: the requests share no blocks with each other or with any other."""
     R, H = ctx_lens.shape[0], cache.kv_heads
     ptrs = [_weights(weights, R, H, "weights")]
     shape = weights.shape
