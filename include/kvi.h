@@ -687,9 +687,9 @@ KVI_API size_t kvi_attn_decode4_workspace_bytes(const kvi_attention *a, int32_t 
  * (float32 [R][H][weights_stride]) the softmax weight of every slot, summed
  * over the query heads of its KV head, is added to d_weights[r][h][slot]:
  * the score kvi_cache4_evict ranks by.  Stored keys are smaller than 2^100 (the
- * products of a group are taken of q scaled to 2^13, in float32).  d_ws and the device-side errors are as
- * for kvi_attn_prompt.  Errors: KVI_ERR_INVALID_ARG (also weights_stride <
- * max_ctx), KVI_ERR_CUDA. */
+ * products of a group are taken of q scaled to 2^13, in float32).  d_ws and the
+ * device-side errors are as for kvi_attn_prompt.  Errors: KVI_ERR_INVALID_ARG
+ * (also weights_stride < max_ctx), KVI_ERR_CUDA. */
 KVI_API kvi_status kvi_attn_decode4(const kvi_attention *a, int32_t R, const void *d_q,
                                     int64_t q_row_stride, const int32_t *d_ctx_lens, int32_t max_ctx,
                                     const int32_t *d_block_tables, int32_t max_blocks,
