@@ -308,13 +308,17 @@ __device__ __forceinline__ void mask_scores(float *s, int vis)
     for (int c = 0; c < kM; ++c) s[c] = c < vis ? s[c] : neg_inf();
 }
 
-// This warp's part of P has reached tensor memory
+// This warp's part of P has reached tensor memory.  (The arrival is lane 0's by a
+// predicate, not a branch: what follows wants the warp as one.)
 __device__ __forceinline__ void announce(uint64_t &bar)
 {
     tmem_wait_st();
     fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
+    asm volatile("{\n.reg .pred q;\nsetp.eq.u32 q, %1, 0;\n@q mbarrier.arrive.shared::cta.b64 _, [%0];\n}\n" ::"r"(
+                     smem_u32(&bar)),
+                 "r"(threadIdx.x & 31)
+                 : "memory");
 }
 
 template <int DP>
@@ -649,6 +653,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 ok = false;
+                __syncwarp();
                 break;
             }
             fence_after();
@@ -691,6 +696,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     ref = top * p.scale;
                     sum *= f;
                 }
+                __syncwarp();
                 if (j > 0) {
 #pragma unroll
                     for (int c = 0; c < DP; c += 32) {
@@ -728,7 +734,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             announce(tl.p_full[i][1]);
         }
         // ---- the rows' results; the values have been looked over
-        __syncwarp();  // (a lane of its own announced P; the barrier wants the warp as one)
         asm volatile("bar.sync 1, 288;" ::: "memory");
         if (n > 0 && ok) {
             // (without products of its own the tile's Q may still be on its way, and its
@@ -766,6 +771,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                         if (tl.first[1][c + e] <= last) v[e] -= inf;
                         if (tl.first[2][c + e] <= last) v[e] += inf - inf;
                     }
+                    __syncwarp();
                 }
             };
             auto packed = [&](const float *v) {

@@ -22,10 +22,15 @@ def test_warps_come_together_before_aligned_instructions():
     """Lanes that went their own way (a lane's own store, a column's own rescaling) meet before a barrier or
     matrix instruction that wants the warp as one."""
     tile = source("kvi_attn_tile.cu")
-    for name in ("bar.sync 1, 288", "bar.sync 3, 128"):
-        before = tile.split(f'asm volatile("{name};"')[0].rstrip()
-        before = before.removesuffix("if (i == 0)").rstrip()
-        assert before.endswith("__syncwarp();"), name
+    before = tile.split('asm volatile("bar.sync 3, 128;"')[0].rstrip().removesuffix("if (i == 0)").rstrip()
+    assert before.endswith("__syncwarp();")
+    announce = tile.split("void announce(uint64_t &bar)")[1].split("template")[0]
+    assert "@q mbarrier.arrive" in announce and "if (" not in announce
+    softmax = tile.split("setmaxnreg.inc")[1]
+    wait = softmax.split("tl.s_full[i]")[1].split("break;")[0].rstrip()
+    assert wait.endswith("__syncwarp();")
+    assert re.search(r"sum \*= f;\s*}\s*__syncwarp\(\);\s*if \(j > 0\)", softmax)
+    assert re.search(r"\+= inf - inf;\s*}\s*__syncwarp\(\);\s*}", softmax)
     for name in ("kvi_attn_prompt.cu", "kvi_attn_decode4.cu"):
         rescale = source(name).split("if (__any_sync(0xffffffffu, move)) {")[1].split("pack_bf16(p0, p1)")[0]
         assert re.search(r"\*= f;\s*}\s*}\s*__syncwarp\(\);\s*}", rescale), name
