@@ -325,6 +325,7 @@ class _Cache:
         nb = layer_tensors[0].shape[1]
         self.struct = PagedCache(ctypes.cast(self._arr, ctypes.POINTER(ctypes.c_void_p)),
                                  len(ptrs), nb, block_size)
+        self.ref = ctypes.byref(self.struct)
         self.layer_tensors = list(layer_tensors)
         self.fits = set()  # (layer, kv_heads, head_dim) that attention found its tensor laid out for
 
@@ -675,49 +676,46 @@ def _ints(t, n: int, name: str, wide: bool = False):
 
 
 def _scratch(t):
-    """Address and bytes of a workspace."""
-    if not t.is_contiguous():
-        raise ValueError("ws must be contiguous")
-    return t.data_ptr(), t.nbytes
+    """Address of a workspace."""
+    if t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("ws must be contiguous")
 
 
 def _word(t):
     """Address of a status word."""
     if t is None:
         return None
-    if t.dtype is not (_types or _dtypes())[1] or t.numel() < 1:
-        raise ValueError("status must be int32")
-    return t.data_ptr()
+    if t.dtype is (_types or _dtypes())[1] and t.numel():
+        return t.data_ptr()
+    raise ValueError("status must be int32")
 
 
 def _log_sums(t, rows: int, heads: int):
     """Address of float32 [rows][heads] (a misaligned one is the library's own
     to refuse)."""
-    if t is None:
-        return None
     p = t.data_ptr()
     if p % 4 == 0 and (t.dtype is not (_types or _dtypes())[3] or t.shape != (rows, heads) or not t.is_contiguous()):
         raise ValueError(f"lse must be contiguous float32 [{rows}][{heads}]")
     return p
 
 
-def _pool(a: Attention, cache, layer: int) -> PagedCache:
-    """The bf16 pool's struct, where the layer's tensor is one for these heads
-    (an invalid attention or layer is the library's own to refuse)."""
+def _pool(a: Attention, cache, layer: int):
+    """A reference to the bf16 pool, where the layer's tensor is one for these
+    heads (an invalid attention or layer is the library's own to refuse)."""
     if isinstance(cache, _Cache4):
         raise ValueError("kvi_attn_prompt reads a bf16 pool (paged_cache), not a 4-bit one")
     if not isinstance(cache, _Cache):
-        return cache  # a struct filled in by the caller
+        return ctypes.byref(cache)  # a struct filled in by the caller
     c = cache.struct
-    key = (layer, a.kv_heads, a.head_dim)
-    if key not in cache.fits and 0 <= layer < c.layers:
+    if 0 <= layer < c.layers:
         t = cache.layer_tensors[layer]
         want = (2, c.num_blocks, c.block_size, a.kv_heads, a.head_dim)
         if (t.shape != want or t.element_size() != 2 or not t.is_contiguous()) and \
                 kvi_attn_prompt_workspace_bytes(a, 1, 1, 1, 1):
             raise ValueError(f"layer {layer} of the cache must be a contiguous bfloat16 {list(want)}, not {list(t.shape)}")
-        cache.fits.add(key)
-    return c
+        cache.fits.add((layer, a.kv_heads, a.head_dim))
+    return cache.ref
 
 
 def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int) -> int:
@@ -730,15 +728,17 @@ def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
     """Causal attention of packed prompts over the paged bf16 cache: q and out
     [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
     int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
-    c = _pool(a, cache, layer)
+    heads, dim = a.q_heads, a.head_dim
+    known = type(cache) is _Cache and (layer, a.kv_heads, dim) in cache.fits
     total, R = q.shape[0], ctx_lens.shape[0]
-    qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
-    op, os_ = _rows(out, a.q_heads, a.head_dim, "out", total)
+    qp, qs = _rows(q, heads, dim, "q")
+    op, os_ = _rows(out, heads, dim, "out", total)
     _check(load_library().kvi_attn_prompt(
         ctypes.byref(a), R, qp, qs, _ints(q_start, R + 1, "q_start"), total, max_q,
         _ints(ctx_lens, R, "ctx_lens"), max_ctx, _ints(block_tables, R, "block_tables"),
-        block_tables.shape[1], ctypes.byref(c), layer, op, os_,
-        _log_sums(lse, total, a.q_heads), *_scratch(ws), _word(status), _stream(stream)), "kvi_attn_prompt")
+        block_tables.shape[1], cache.ref if known else _pool(a, cache, layer), layer, op, os_,
+        None if lse is None else _log_sums(lse, total, heads), _scratch(ws), ws.nbytes, _word(status),
+        _stream(stream)), "kvi_attn_prompt")
 
 
 def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:
@@ -782,16 +782,17 @@ def kvi_attn_decode4(a: Attention, q, ctx_lens, max_ctx: int, block_tables, cach
                      out, ws, status, weights=None, stream=None) -> None:
     """One decoding step over the 4-bit cache: q and out [R][Hq][D] bf16;
     weights float32 [R][H][slots] accumulates each slot's softmax weight."""
-    if (a.kv_heads, a.head_dim) != (cache.kv_heads, cache.head_dim):
+    heads, dim, H = a.q_heads, cache.head_dim, cache.kv_heads
+    if a.kv_heads != H or a.head_dim != dim:
         raise ValueError("the attention and the 4-bit cache have different heads")
     R = ctx_lens.shape[0]
-    qp, qs = _rows(q, a.q_heads, a.head_dim, "q", R)
-    op, os_ = _rows(out, a.q_heads, a.head_dim, "out", R)
-    wp = None if weights is None else _weights(weights, R, a.kv_heads, "weights")
+    qp, qs = _rows(q, heads, dim, "q", R)
+    op, os_ = _rows(out, heads, dim, "out", R)
+    wp = None if weights is None else _weights(weights, R, H, "weights")
     _check(load_library().kvi_attn_decode4(
         ctypes.byref(a), R, qp, qs, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
         _ints(block_tables, R, "block_tables"), block_tables.shape[1], cache.ref, layer, op, os_, wp,
-        0 if weights is None else weights.shape[2], *_scratch(ws), _word(status),
+        0 if weights is None else weights.shape[2], _scratch(ws), ws.nbytes, _word(status),
         _stream(stream)), "kvi_attn_decode4")
 
 
@@ -806,16 +807,15 @@ def kvi_cache4_evict(cache: _Cache4, layer: int, ctx_lens, max_ctx: int, block_t
     head by accumulated weight (weights float32, pos int32: [R][H][slots]).  In
     place: the requests share no blocks with each other or with any other."""
     R, H = ctx_lens.shape[0], cache.kv_heads
-    ptrs = [_weights(weights, R, H, "weights")]
-    shape = weights.shape
-    for t, dtype in ((pos, _types[1]), (weights_out, _types[3]), (pos_out, _types[1])):
-        if t.shape != shape or not t.is_contiguous() or t.dtype is not dtype:
-            raise ValueError("weights (float32) and positions (int32), in and out, must be contiguous and of one shape")
-        ptrs.append(t.data_ptr())
+    wp, wo = _weights(weights, R, H, "weights"), _weights(weights_out, R, H, "weights_out")
+    slots, ints = weights.shape, _types[1]
+    if weights_out.shape != slots or pos.shape != slots or pos_out.shape != slots or pos.dtype is not ints or \
+            pos_out.dtype is not ints or not (pos.is_contiguous() and pos_out.is_contiguous()):
+        raise ValueError("weights (float32) and positions (int32), in and out, must be contiguous and of one shape")
     _check(load_library().kvi_cache4_evict(
         H, cache.head_dim, R, cache.ref, layer, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
-        _ints(block_tables, R, "block_tables"), block_tables.shape[1], budget, sink, recent, ptrs[0],
-        ptrs[1], shape[2], ptrs[2], ptrs[3], _ints(ctx_out, R, "ctx_out"), *_scratch(ws),
+        _ints(block_tables, R, "block_tables"), block_tables.shape[1], budget, sink, recent, wp,
+        pos.data_ptr(), slots[2], wo, pos_out.data_ptr(), _ints(ctx_out, R, "ctx_out"), _scratch(ws), ws.nbytes,
         _word(status), _stream(stream)), "kvi_cache4_evict")
 
 
