@@ -34,7 +34,7 @@
 // them (Q and the first keys, the rows' results), which nothing overlaps as a
 // block fills its SM and its softmax warps store the results themselves.  32 heads over 8 of 128 channels: one prompt of 8192 tokens
 // 0.33 ms, 1670 TFLOP/s; 16 prompts of 1 to 2048 tokens and up to 1600 keys of
-// memory 0.19 ms, 1120 TFLOP/s.  No faster: blocks that stay and take several
+// memory 0.19 ms, 1130 TFLOP/s.  No faster: blocks that stay and take several
 // pairs of tiles, the softmax warps storing the results all the same (0.35 and
 // 0.19 ms), the pairs with the most keys first (0.34 and
 // 0.195 ms); slower: two warps issuing matrix instructions, copies by cp.async
