@@ -635,6 +635,118 @@ KVI_API kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const void
                                    int64_t out_row_stride, float *d_lse, void *d_ws, size_t ws_bytes,
                                    int32_t *d_status, kvi_stream_t stream);
 
+/* kvi_attn_prompt with a window: the row at position i sees the positions j <= i
+ * with j > i - window (its own and the window - 1 before it) or j < sink (a few
+ * first tokens, or a system prefix, that stay visible).  window >= 1, <= 2^30
+ * unless it reaches max_ctx; sink >= 0.  Blocks that no row sees are not read, so
+ * their table entries may be anything.  Everything else, workspace
+ * (kvi_attn_prompt_workspace_bytes) and errors included, is as there; where the
+ * window or the sink covers max_ctx, so is the result, bit for bit. */
+KVI_API kvi_status kvi_attn_window(const kvi_attention *a, int32_t R, const void *d_q,
+                                   int64_t q_row_stride, const int32_t *d_q_start, int32_t total_q,
+                                   int32_t max_q, const int32_t *d_ctx_lens, int32_t max_ctx,
+                                   const int32_t *d_block_tables, int32_t max_blocks,
+                                   const kvi_paged_cache *cache, int32_t layer, int32_t window,
+                                   int32_t sink, void *d_out, int64_t out_row_stride, float *d_lse,
+                                   void *d_ws, size_t ws_bytes, int32_t *d_status, kvi_stream_t stream);
+
+/* Device scratch bytes of kvi_attn_shared for these sizes and any smaller ones; 0
+ * for invalid ones. */
+KVI_API size_t kvi_attn_shared_workspace_bytes(const kvi_attention *a, int32_t R, int32_t total_q,
+                                               int32_t max_q, int32_t max_ctx, int32_t shared);
+
+/* kvi_attn_prompt for a batch whose requests share their first `shared` keys (users
+ * of one memory, Section 6.4; requests behind one system prefix): those keys are
+ * read once for all rows of the batch instead of once per request, and each
+ * request's other keys as ever.  The block tables are the same as for
+ * kvi_attn_prompt: positions 0 .. ctx-1 of each request, the first shared /
+ * block_size entries the same in every row (those of the first request that has
+ * rows are read).  shared is a multiple of block_size, in [0, max_ctx) and in the
+ * tables (0: this is kvi_attn_prompt), and each request that has rows has ctx -
+ * n >= shared, so that its rows see the whole prefix.  Rows, outputs and errors
+ * are as for kvi_attn_prompt; also KVI_ERR_OUT_OF_RANGE for a request with fewer
+ * keys before its rows than the prefix has (its outputs are not written). */
+KVI_API kvi_status kvi_attn_shared(const kvi_attention *a, int32_t R, const void *d_q,
+                                   int64_t q_row_stride, const int32_t *d_q_start, int32_t total_q,
+                                   int32_t max_q, const int32_t *d_ctx_lens, int32_t max_ctx,
+                                   const int32_t *d_block_tables, int32_t max_blocks,
+                                   const kvi_paged_cache *cache, int32_t layer, int32_t shared,
+                                   void *d_out, int64_t out_row_stride, float *d_lse, void *d_ws,
+                                   size_t ws_bytes, int32_t *d_status, kvi_stream_t stream);
+
+/* A step's own rows, ready for attention: queries and keys normalised per head,
+ * rotated to their positions as injected keys are (Section 5.1), and K and V
+ * written to the pages (Section 3.4), in one pass.
+ *   y = x / sqrt(mean x^2 + eps) * weight   over a head's D channels, or y = x where
+ *                                           the weight is NULL
+ *   out = y rotated by *rope to its row's position
+ * in float32 with one rounding of each result; a head with an infinity or NaN is
+ * NaN throughout where it is normalised.  Without a weight a key gets the bits
+ * that kvi_inject_paged_ex gives it.
+ *   a            heads and head size (its scale is not used)
+ *   d_positions  int32 [T], each in [0, max_position); a caller's table ends with
+ *                its own rows.  max_position <= 2^22; the table is built as by
+ *                kvi_prepare_rope_ex where it is missing
+ *   d_q          bf16 [T][Hq][D], rows q_row_stride elements apart (like all rows
+ *                here); to d_q_out, which may be d_q.  Both NULL: keys alone
+ *   d_k          bf16 [T][H][D]; rotated to d_k_out (may be d_k, or NULL) and to the
+ *                pages; normalised but not rotated, as a store keeps keys, to
+ *                d_k_plain (or NULL; another buffer than d_k_out)
+ *   d_q_weight, d_k_weight  bf16 [D], or NULL.  1e-12 <= eps <= 1
+ *   d_v, cache, layer, d_slots   V, unchanged, and K go to the slots d_slots (int64
+ *                [T], block * block_size + offset) of the layer's pages; a negative
+ *                slot leaves them out.  No slot twice.  All NULL: no pages
+ * Pointers of rows and weights, and strides, are 16-byte aligned.  T <= 2^28.
+ * Device-side errors: KVI_ERR_OUT_OF_RANGE for a position out of range (the row is
+ * skipped) or a slot beyond the pool (nothing goes to the pages).
+ * Errors: KVI_ERR_INVALID_ARG, KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_norm_rope(const kvi_attention *a, const kvi_rope *rope, int32_t max_position,
+                                 int64_t T, const int32_t *d_positions, const void *d_q,
+                                 int64_t q_row_stride, const void *d_k, int64_t k_row_stride,
+                                 const void *d_q_weight, const void *d_k_weight, float eps,
+                                 void *d_q_out, int64_t q_out_row_stride, void *d_k_out,
+                                 int64_t k_out_row_stride, void *d_k_plain, int64_t k_plain_row_stride,
+                                 const void *d_v, int64_t v_row_stride, const kvi_paged_cache *cache,
+                                 int32_t layer, const int64_t *d_slots, int32_t *d_status,
+                                 kvi_stream_t stream);
+
+/* A step's block tables, row starts, positions and slots, from the requests'
+ * lengths (the engine's allocation of Section 3.4, on the GPU: a captured step
+ * needs no host in between).  Free blocks are a ring d_free [num_blocks] of block
+ * ids: those at the running numbers d_free_at[0] .. d_free_at[1]-1, number i in
+ * element i mod num_blocks.  Request r holds ctx = d_ctx_lens[r] keys in row r of
+ * d_block_tables [R][max_blocks]; with n = d_new_lens[r]
+ *   n >= 0  it gets n rows, at the positions ctx .. ctx+n-1, and for them the next
+ *           free blocks, which are appended to its row of the tables;
+ *   n < 0   it has finished: its blocks from entry shared / block_size on (the
+ *           first `shared` keys, whole blocks, are not its own) go back to the ring
+ *           in order, free from the next call on.
+ * Blocks are given and taken in the order of the requests.  Outputs:
+ *   d_block_tables  the new entries; the others are left as they are
+ *   d_free          the returned blocks, at the ring's end
+ *   d_free_at_out   [2], d_ctx_out [R] (0 for a finished request), both other
+ *                   buffers than the inputs
+ *   d_q_start       [R + 1] first row of each request, and the end
+ *   d_positions, d_slots   int32 and int64 [total_rows]: each row's position, and
+ *                   its slot block * block_size + offset.  Rows past the last
+ *                   request's get position 0 and slot -1, which kvi_norm_rope and
+ *                   kvi_cache4_write leave out of the cache
+ * Device-side errors: KVI_ERR_CAPACITY for a request that does not fit its table,
+ * the free blocks or total_rows together with those before it (it gets no rows and
+ * keeps its length; one whose last block has room needs no free block), and for
+ * more returned blocks than the ring can hold (none is returned, and no request
+ * ends); KVI_ERR_OUT_OF_RANGE for a ctx that is negative or exceeds its table, one below
+ * `shared` that asks for rows (no rows), running numbers that are no ring (no
+ * blocks), and a block id outside the pool (its rows have slot -1).
+ * Errors: KVI_ERR_INVALID_ARG, KVI_ERR_CUDA. */
+KVI_API kvi_status kvi_batch_tables(int32_t R, const int32_t *d_ctx_lens, const int32_t *d_new_lens,
+                                    int32_t *d_block_tables, int32_t max_blocks, int32_t num_blocks,
+                                    int32_t block_size, int32_t shared, int32_t *d_free,
+                                    const int64_t *d_free_at, int64_t *d_free_at_out,
+                                    int32_t *d_ctx_out, int32_t *d_q_start, int32_t total_rows,
+                                    int32_t *d_positions, int64_t *d_slots, int32_t *d_status,
+                                    kvi_stream_t stream);
+
 /* The 4-bit cache: a paged pool at 4.5 bits per element instead of 16.  It is
  * described by a kvi_paged_cache whose block_size is a multiple of 16 and
  * whose layer_base buffers each hold [num_blocks][H] pages of

@@ -33,5 +33,6 @@ from ._binding import (  # noqa: F401
     MAX_ATTN_HEAD_DIM, MAX_ATTN_GROUP, Attention, attention, cache4, kvi_attn_prompt_workspace_bytes,
     kvi_attn_prompt, kvi_cache4_layer_bytes, kvi_cache4_write, kvi_cache4_read,
     kvi_attn_decode4_workspace_bytes, kvi_attn_decode4, kvi_cache4_evict_workspace_bytes,
-    kvi_cache4_evict,
+    kvi_cache4_evict, kvi_attn_window, kvi_attn_shared_workspace_bytes, kvi_attn_shared, kvi_norm_rope,
+    kvi_batch_tables,
 )

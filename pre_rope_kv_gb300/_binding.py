@@ -43,7 +43,8 @@ EXPORTED_SYMBOLS = (
     "kvi_selftest_bounded_wait", "kvi_selftest_stream_read", "kvi_attn_prompt_workspace_bytes",
     "kvi_attn_prompt", "kvi_cache4_layer_bytes", "kvi_cache4_write", "kvi_cache4_read",
     "kvi_attn_decode4_workspace_bytes", "kvi_attn_decode4", "kvi_cache4_evict_workspace_bytes",
-    "kvi_cache4_evict",
+    "kvi_cache4_evict", "kvi_attn_window", "kvi_attn_shared_workspace_bytes", "kvi_attn_shared",
+    "kvi_norm_rope", "kvi_batch_tables",
 )
 MAX_ATTN_HEAD_DIM = 256
 MAX_ATTN_GROUP = 128
@@ -197,6 +198,15 @@ def open_library(path: str):
         "kvi_cache4_evict_workspace_bytes": (sz, [i32, i32, i32]),
         "kvi_cache4_evict": (S, [i32, i32, i32, ctypes.POINTER(PagedCache), i32, P, i32, P, i32, i32,
                                  i32, i32, P, P, i64, P, P, P, P, sz, P, P]),
+        "kvi_attn_window": (S, [ctypes.POINTER(Attention), i32, P, i64, P, i32, i32, P, i32, P, i32,
+                                ctypes.POINTER(PagedCache), i32, i32, i32, P, i64, P, P, sz, P, P]),
+        "kvi_attn_shared_workspace_bytes": (sz, [ctypes.POINTER(Attention), i32, i32, i32, i32, i32]),
+        "kvi_attn_shared": (S, [ctypes.POINTER(Attention), i32, P, i64, P, i32, i32, P, i32, P, i32,
+                                ctypes.POINTER(PagedCache), i32, i32, P, i64, P, P, sz, P, P]),
+        "kvi_norm_rope": (S, [ctypes.POINTER(Attention), ctypes.POINTER(Rope), i32, i64, P, P, i64, P, i64, P, P,
+                              ctypes.c_float, P, i64, P, i64, P, i64, P, i64, ctypes.POINTER(PagedCache), i32, P,
+                              P, P]),
+        "kvi_batch_tables": (S, [i32, P, P, P, i32, i32, i32, i32, P, P, P, P, P, i32, P, P, P, P]),
         "kvi_status_str": (ctypes.c_char_p, [S]),
         "kvi_last_error": (ctypes.c_char_p, []),
     }
@@ -705,7 +715,7 @@ def _pool(a: Attention, cache, layer: int):
     """The bf16 pool's struct, where the layer's tensor is one for these
     heads (an invalid attention or layer is the library's own to refuse)."""
     if isinstance(cache, _Cache4):
-        raise ValueError("kvi_attn_prompt reads a bf16 pool (paged_cache), not a 4-bit one")
+        raise ValueError("this call wants a bf16 pool (paged_cache), not a 4-bit one")
     if not isinstance(cache, _Cache):
         return cache  # a struct filled in by the caller
     c = cache.struct
@@ -724,22 +734,115 @@ def kvi_attn_prompt_workspace_bytes(a: Attention, R: int, total_q: int, max_q: i
                                                           int(max_q), int(max_ctx))
 
 
+def _prompt_args(a: Attention, q, q_start, max_q, ctx_lens, max_ctx, block_tables, cache, layer):
+    """The leading arguments that the calls on prompts share."""
+    known = type(cache) is _Cache and (layer, a.kv_heads, a.head_dim) in cache.fits
+    R = ctx_lens.shape[0]
+    qp, qs = _rows(q, a.q_heads, a.head_dim, "q")
+    return (a, R, qp, qs, _ints(q_start, R + 1, "q_start"), q.shape[0], max_q, _ints(ctx_lens, R, "ctx_lens"), max_ctx,
+            _ints(block_tables, R, "block_tables"), block_tables.shape[1],
+            cache.struct if known else _pool(a, cache, layer), layer)
+
+
+def _prompt_results(a: Attention, q, out, lse, ws, status, stream):
+    """The trailing ones."""
+    total = q.shape[0]
+    op, os_ = _rows(out, a.q_heads, a.head_dim, "out", total)
+    return (op, os_, None if lse is None else _log_sums(lse, total, a.q_heads), _scratch(ws), ws.nbytes, _word(status),
+            _stream(stream))
+
+
 def kvi_attn_prompt(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int, block_tables, cache,
                     layer: int, out, ws, status, lse=None, stream=None) -> None:
     """Causal attention of packed prompts over the paged bf16 cache: q and out
     [total_q][Hq][D], q_start int32 [R + 1], ctx_lens int32 [R], block_tables
     int32 [R][max_blocks], lse float32 [total_q][Hq] or None."""
-    heads, dim = a.q_heads, a.head_dim
-    known = type(cache) is _Cache and (layer, a.kv_heads, dim) in cache.fits
-    total, R = q.shape[0], ctx_lens.shape[0]
-    qp, qs = _rows(q, heads, dim, "q")
-    op, os_ = _rows(out, heads, dim, "out", total)
     _check(load_library().kvi_attn_prompt(
-        a, R, qp, qs, _ints(q_start, R + 1, "q_start"), total, max_q,
-        _ints(ctx_lens, R, "ctx_lens"), max_ctx, _ints(block_tables, R, "block_tables"),
-        block_tables.shape[1], cache.struct if known else _pool(a, cache, layer), layer, op, os_,
-        None if lse is None else _log_sums(lse, total, heads), _scratch(ws), ws.nbytes, _word(status),
-        _stream(stream)), "kvi_attn_prompt")
+        *_prompt_args(a, q, q_start, max_q, ctx_lens, max_ctx, block_tables, cache, layer),
+        *_prompt_results(a, q, out, lse, ws, status, stream)), "kvi_attn_prompt")
+
+
+def kvi_attn_window(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int, block_tables, cache,
+                    layer: int, window: int, sink: int, out, ws, status, lse=None, stream=None) -> None:
+    """kvi_attn_prompt in which a row sees its own key and the window - 1 before
+    it, and the first `sink`; the workspace is that of kvi_attn_prompt."""
+    _check(load_library().kvi_attn_window(
+        *_prompt_args(a, q, q_start, max_q, ctx_lens, max_ctx, block_tables, cache, layer), window, sink,
+        *_prompt_results(a, q, out, lse, ws, status, stream)), "kvi_attn_window")
+
+
+def kvi_attn_shared_workspace_bytes(a: Attention, R: int, total_q: int, max_q: int, max_ctx: int, shared: int) -> int:
+    return load_library().kvi_attn_shared_workspace_bytes(a, int(R), int(total_q), int(max_q), int(max_ctx), int(shared))
+
+
+def kvi_attn_shared(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int, block_tables, cache,
+                    layer: int, shared: int, out, ws, status, lse=None, stream=None) -> None:
+    """kvi_attn_prompt for requests whose first `shared` keys (whole blocks) are
+    the same, read once for all of them."""
+    _check(load_library().kvi_attn_shared(
+        *_prompt_args(a, q, q_start, max_q, ctx_lens, max_ctx, block_tables, cache, layer), shared,
+        *_prompt_results(a, q, out, lse, ws, status, stream)), "kvi_attn_shared")
+
+
+def _norm_weight(t, head_dim: int, name: str):
+    if t is None:
+        return None
+    if t.dtype is not (_types or _dtypes())[0] or t.shape != (head_dim,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous bfloat16 [{head_dim}]")
+    return t.data_ptr()
+
+
+def kvi_norm_rope(a: Attention, spec: Rope, max_position: int, positions, q, k, q_out, k_out, status, q_weight=None,
+                  k_weight=None, eps: float = 1e-6, k_plain=None, v=None, cache: _Cache | None = None, layer: int = 0,
+                  slots=None, stream=None) -> None:
+    """Rows q [T][Hq][D] and k [T][H][D] normalised per head (where there is a
+    weight [D]), rotated to positions int32 [T], to q_out and k_out (None: not
+    wanted) and, with v, to slots int64 [T] of a layer of the paged cache;
+    k_plain takes the keys before rotation.  q and q_out None: keys alone."""
+    T, heads, kv, dim = positions.shape[0], a.q_heads, a.kv_heads, a.head_dim
+
+    def rows(t, n, name):
+        return (None, 0) if t is None else _rows(t, n, dim, name, T)
+
+    pool = None
+    if cache is not None:
+        pool = cache.struct if (layer, kv, dim) in getattr(cache, "fits", ()) else _pool(a, cache, layer)
+    if positions.dtype is not (_types or _dtypes())[1] or not positions.is_contiguous():
+        raise ValueError("positions must be contiguous int32")
+    if slots is not None and (slots.dtype is not _types[2] or not slots.is_contiguous() or slots.shape[0] < T):
+        raise ValueError(f"slots must be contiguous int64, at least {T} long")
+    _check(load_library().kvi_norm_rope(
+        a, spec, max_position, T, positions.data_ptr(), *rows(q, heads, "q"), *rows(k, kv, "k"),
+        _norm_weight(q_weight, dim, "q_weight"), _norm_weight(k_weight, dim, "k_weight"), eps, *rows(q_out, heads, "q_out"),
+        *rows(k_out, kv, "k_out"), *rows(k_plain, kv, "k_plain"), *rows(v, kv, "v"), pool, layer, _ptr(slots),
+        _word(status), _stream(stream)), "kvi_norm_rope")
+
+
+def _ring_numbers(t, name: str):
+    if t.dtype is not (_types or _dtypes())[2] or t.numel() != 2 or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous int64 [2]")
+    return t.data_ptr()
+
+
+def kvi_batch_tables(ctx_lens, new_lens, block_tables, block_size: int, shared: int, free, free_at, free_at_out, ctx_out,
+                     q_start, positions, slots, status, stream=None) -> None:
+    """A step's tables from the requests' lengths: new_lens int32 [R] (negative:
+    finished), block_tables int32 [R][max_blocks] (new entries written), the ring
+    of free blocks `free` int32 [num_blocks] with its running numbers free_at
+    int64 [2]; q_start int32 [R + 1], positions int32 and slots int64 [rows]."""
+    R, rows, ints = ctx_lens.shape[0], slots.shape[0], (_types or _dtypes())[1]
+    if block_tables.dim() != 2 or block_tables.shape[0] != R:
+        raise ValueError(f"block_tables must be [{R}][max_blocks]")
+    if positions.dtype is not ints or positions.shape != (rows,) or not positions.is_contiguous() or \
+            slots.dtype is not _types[2] or slots.dim() != 1 or not slots.is_contiguous():
+        raise ValueError("positions must be contiguous int32 [rows], slots int64 [rows]")
+    if free.dtype is not ints or free.dim() != 1 or not free.is_contiguous():
+        raise ValueError("free must be contiguous int32 [num_blocks]")
+    _check(load_library().kvi_batch_tables(
+        R, _ints(ctx_lens, R, "ctx_lens"), _ints(new_lens, R, "new_lens"), _ints(block_tables, R, "block_tables"),
+        block_tables.shape[1], free.shape[0], block_size, shared, free.data_ptr(), _ring_numbers(free_at, "free_at"),
+        _ring_numbers(free_at_out, "free_at_out"), _ints(ctx_out, R, "ctx_out"), _ints(q_start, R + 1, "q_start"), rows,
+        positions.data_ptr(), slots.data_ptr(), _word(status), _stream(stream)), "kvi_batch_tables")
 
 
 def kvi_cache4_layer_bytes(kv_heads: int, head_dim: int, num_blocks: int, block_size: int) -> int:

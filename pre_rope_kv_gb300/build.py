@@ -25,9 +25,11 @@ LIB_PATH = os.path.join(OUT_DIR, "libkvi.so")
 DEBUG_LIB_PATH = os.path.join(OUT_DIR, "libkvi_debug.so")
 SOURCES = ["kvi_host.cu", "kvi_retrieve.cu", "kvi_inject.cu", "kvi_noalloc.cu", "kvi_shared.cu",
            "kvi_store_io.cu", "kvi_graph.cu", "kvi_selftest.cu", "kvi_attn_prompt.cu",
-           "kvi_attn_tile.cu", "kvi_attn_decode4.cu", "kvi_attn_join.cu", "kvi_cache4.cu"]
+           "kvi_attn_tile.cu", "kvi_attn_decode4.cu", "kvi_attn_join.cu", "kvi_cache4.cu",
+           "kvi_batch.cu", "kvi_norm_rope.cu"]
 HEADERS = [os.path.join(CSRC, "kvi_internal.cuh"), os.path.join(CSRC, "kvi_dot2.cuh"),
            os.path.join(CSRC, "kvi_sync.cuh"), os.path.join(CSRC, "kvi_attn.cuh"),
+           os.path.join(CSRC, "kvi_rotate.cuh"),
            os.path.join(INCLUDE, "kvi.h"), os.path.join(INCLUDE, "kvi_debug.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

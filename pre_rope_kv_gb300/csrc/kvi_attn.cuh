@@ -52,6 +52,8 @@ struct JoinParams {
     const float2 *ml;        // [rows][S] (m in log2 units, l)
     int32_t by_request;
     int32_t S, span;         // splits, keys per split
+    int32_t cap = 0x7fffffff;  // keys that a row's pieces cover at most (windows)
+    int32_t shared, first;   // leading keys that are in `first` pieces of their own
     int32_t R, q_heads, D;
     const int32_t *q_start;  // [R + 1] or null: one row per request
     int32_t total_q, max_q;
@@ -84,6 +86,12 @@ struct PromptParams {
     int32_t S, span;
     int32_t per;                // (tiles) tokens of a row tile
     int32_t joined;             // (rows) a chunk's pieces are a cluster, which joins them
+    // (kWindow) the keys that a row sees, and how many of them a row's pieces cover at most
+    int32_t window, sink, cap;
+    // (kShared) a batch whose requests share their first keys.  flat: those keys, of all
+    // rows as one request's; else each request's other keys.  Pieces from `first` on
+    // of `parts` of a row.
+    int32_t shared, flat, first, parts;
     // Partial results of row i of request r: at its place in q, or, where q has
     // more rows than R * max_q, at r * max_q + i; so they take no more of the
     // workspace than there can be rows that are split.
@@ -93,11 +101,16 @@ struct PromptParams {
     int32_t *status;
 };
 
+// The keys that a row at position i sees: i and all before it; those of the
+// window (i - window, i] and the first `sink`; or (of a batch with a shared
+// prefix) the prefix, or i and those before it from the prefix on.
+enum : int { kCausal = 0, kWindow = 1, kShared = 2 };
+
 // The tensor-core form (kvi_attn_tile.cu): two tiles of 128 rows a block.
 // Tokens that a tile holds, and the launch (p.chunks: no fewer than the tile
 // pairs of all requests together).
 inline int tile_tokens(int G) { return 128 / G; }
-cudaError_t launch_tiles(const PromptParams &p, cudaStream_t s);
+cudaError_t launch_tiles(const PromptParams &p, int mode, cudaStream_t s);
 
 // A tensor map of bf16 boxes with the 128-byte swizzle (rank <= 5; pitches in
 // bytes of the dimensions past the first); out-of-range elements read as 0.
@@ -314,6 +327,38 @@ __device__ __forceinline__ bool request_span(int r, const int32_t *q_start, int 
            (int64_t)o.ctx <= (int64_t)max_blocks * block_size;
 }
 
+// The rows and keys of request r in a batch with a shared prefix: its keys past
+// the prefix, and only rows among those the batch's partial results are for.
+__device__ __forceinline__ bool request_past_prefix(int r, const int32_t *q_start, int R, int total_q, int max_q,
+                                                    const int32_t *ctx_lens, int max_ctx, int max_blocks,
+                                                    int block_size, int shared, RequestSpan &o, int &part0)
+{
+    const int b0 = q_start[0], b1 = q_start[R];
+    bool good = request_span(r, q_start, total_q, max_q, ctx_lens, max_ctx, max_blocks, block_size, o);
+    part0 = o.q0 - b0;
+    good = good && b0 >= 0 && part0 >= 0 && o.q0 + o.n_q <= b1 && (int64_t)b1 - b0 <= (int64_t)R * max_q;
+    if (good && o.n_q > 0 && o.ctx - o.n_q < shared) good = false;
+    o.ctx = max(0, o.ctx - shared);
+    return good;
+}
+
+// The rows of all requests of a batch as one request's, over the shared prefix,
+// which is read through the table of the first request that has rows (its
+// number; without any, no rows).  Every warp for itself.
+__device__ __forceinline__ int batch_rows(const PromptParams &p, RequestSpan &o)
+{
+    const int lane = threadIdx.x & 31, b0 = p.q_start[0], b1 = p.q_start[p.R];
+    const bool good = b0 >= 0 && b1 >= b0 && b1 <= p.total_q && (int64_t)b1 - b0 <= (int64_t)p.R * p.max_q;
+    o = RequestSpan{b0, good ? b1 - b0 : 0, p.shared};
+    for (int r0 = 0; r0 < p.R; r0 += 32) {
+        const int r = r0 + lane;
+        const uint32_t some = __ballot_sync(0xffffffffu, r < p.R && p.q_start[r + 1] > p.q_start[r]);
+        if (some) return r0 + __ffs((int)some) - 1;
+    }
+    o.n_q = 0;
+    return 0;
+}
+
 namespace {
 
 constexpr int kJoinWarps = 4;
@@ -323,13 +368,22 @@ __device__ __forceinline__ void join_rows(const JoinParams &p, int x, int r)
 {
     const int lane = threadIdx.x & 31;
     RequestSpan q;
-    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q)) return;
-    const int pieces = (q.ctx + p.span - 1) / p.span;
+    int part0 = 0;
+    if (p.first) {
+        if (!request_past_prefix(r, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size,
+                                 p.shared, q, part0))
+            return;
+    } else if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q)) {
+        return;
+    }
+    const int pieces = p.first + (min(q.ctx, p.cap) + p.span - 1) / p.span;
     if (pieces <= 1) return;
     const int64_t i = (int64_t)x * kJoinWarps + (threadIdx.x >> 5);
     if (i >= (int64_t)q.n_q * p.q_heads) return;
     const int64_t row = (int64_t)q.q0 * p.q_heads + i;
-    const int64_t part = p.by_request ? (int64_t)r * p.max_q * p.q_heads + i : row;
+    const int64_t part = p.first        ? (int64_t)part0 * p.q_heads + i
+                         : p.by_request ? (int64_t)r * p.max_q * p.q_heads + i
+                                        : row;
     const float2 *ml = p.ml + part * p.S;
     const float *po = p.po + part * p.S * p.D;
     const int d0 = 4 * lane;

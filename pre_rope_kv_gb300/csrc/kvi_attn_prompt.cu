@@ -71,7 +71,7 @@ struct RowsSmem {
 
 // DP: the head size rounded up to 32, 64, 128 or 256 (the rest reads as zero);
 // 8 * NT rows per block.  JOINED: a chunk's pieces are a cluster, which joins them.
-template <int DP, int NT, bool JOINED>
+template <int DP, int NT, bool JOINED, int MODE>
 __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ PromptParams p)
 {
     using Sm = RowsSmem<DP, NT>;
@@ -82,17 +82,23 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     __shared__ float2 s_ml[8 * NT];  // of the block
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
-    const int r = blockIdx.y;
+    int r = blockIdx.y;
     pdl_wait();
     pdl_launch_dependents();
     RequestSpan rq;
-    if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
+    int part0 = 0;
+    const bool flat = MODE == kShared && p.flat;
+    if (flat) {
+        r = batch_rows(p, rq);
+    } else if (MODE == kShared ? !request_past_prefix(r, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
+                                                      p.max_blocks, p.B, p.shared, rq, part0)
+                               : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         return;
     }
     const int rows = rq.n_q * p.G, row0 = chunk * 8 * NT;
     if (row0 >= rows) return;
-    const int pieces = max(1, (rq.ctx + p.span - 1) / p.span);
+    const int pieces = max(1, ((MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx) + p.span - 1) / p.span);
     if (split >= pieces) {
         if (JOINED && pieces > 1) {  // (the others of the cluster count on it)
             cluster_sync();
@@ -100,10 +106,23 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         }
         return;
     }
-    const int seen_by_0 = rq.ctx - rq.n_q;  // last position that token 0 sees
-    const int end = min(rq.ctx, seen_by_0 + (min(rows, row0 + 8 * NT) - 1) / p.G + 1);
+    const int seen_by_0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
+    int end = flat ? rq.ctx : min(rq.ctx, seen_by_0 + (min(rows, row0 + 8 * NT) - 1) / p.G + 1);
+    // With a window the tiles of 16 keys are those of the first `sink` keys and
+    // those from the block's first window on: tile i is tile i + skip of the keys
+    // from `kept` on.
+    // Keys before that window (no row sees them) are not read.
+    const int low = MODE == kWindow ? seen_by_0 + row0 / p.G - p.window + 1 : 0;
+    int skip = 0, kept = 0;
+    if (MODE == kWindow) {
+        const int start = max(0, low) / 16;
+        kept = min(start, (int)(((int64_t)p.sink + 15) / 16));
+        skip = start - kept;
+        end -= skip * 16;
+    }
+    auto place_of = [&](int tile) { return MODE == kWindow && tile >= kept ? tile + skip : tile; };
     const int from = split * p.span, to = min(end, from + p.span);
-    const bool whole = pieces == 1;
+    const bool whole = MODE != kShared && pieces == 1;
 
     // the rows' last visible positions: columns 2 t, 2 t + 1 of each n-tile
     int last[NT][2];
@@ -113,11 +132,16 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int row = row0 + 8 * nt + 2 * t + c;
-            last[nt][c] = row < rows ? seen_by_0 + row / p.G : -1;
+            last[nt][c] = row < rows ? seen_by_0 + (flat ? 0 : row / p.G) : -1;
             if (row < rows) least = min(least, last[nt][c]);
         }
 #pragma unroll
     for (int o = 1; o < 4; o <<= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    // with a window: keys below it are not seen by the block's last row
+    const int held = MODE == kWindow ? seen_by_0 + (min(rows, row0 + 8 * NT) - 1) / p.G - p.window + 1 : 0;
+    auto sees = [&](int key, int upto) {
+        return key <= upto && (MODE != kWindow || key > upto - p.window || key < p.sink);
+    };
 
     uint32_t qf[NT][KS][2];
 #pragma unroll
@@ -151,19 +175,20 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
             for (int c = p.D / 8; c < CH; ++c)
                 *reinterpret_cast<uint4 *>(ring + i * Sm::kPitch + c * 16) = make_uint4(0, 0, 0, 0);
     }
-    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks + (MODE == kShared && !flat ? p.shared / p.B : 0);
     const int64_t plane = (int64_t)p.num_blocks * p.B * p.H * p.D;
     const int t0 = from / 16 + warp, t1 = (to + 15) / 16;
     const uint32_t ring_a = smem_addr(ring);
 
+    auto wanted = [&](int key) { return key < rq.ctx && (MODE != kWindow || key >= low || key < p.sink); };
     // block of key `lane` (mod 16) of a tile; -1 outside
     auto block_of = [&](int tile) {
-        const int key = tile * 16 + (lane & 15);
-        return tile < t1 && key < rq.ctx ? table[key / p.B] : -1;
+        const int key = place_of(tile) * 16 + (lane & 15);
+        return tile < t1 && wanted(key) ? table[key / p.B] : -1;
     };
     auto issue = [&](int tile, int stage, int block) {
-        const int key = tile * 16 + (lane & 15);
-        const bool asked = tile < t1 && key < rq.ctx;
+        const int key = place_of(tile) * 16 + (lane & 15);
+        const bool asked = tile < t1 && wanted(key);
         const bool here = asked && block >= 0 && block < p.num_blocks;
         if (asked && !here) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         const int64_t at = here ? (((int64_t)block * p.B + key % p.B) * p.H + h) * p.D : -1;
@@ -208,7 +233,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a[0], a[1], a[2], a[3], qf[nt][k][0], qf[nt][k][1]);
         }
-        const int key = tile * 16 + g;
+        const int key0 = place_of(tile) * 16, key = key0 + g;
         const uint32_t here = s_here[warp][stage];
         bool move = false;
 #pragma unroll
@@ -216,7 +241,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int kk = key + (i >> 1) * 8;
-                const bool see = kk <= last[nt][i & 1] && ((here >> (g + (i >> 1) * 8)) & 1u);
+                const bool see = sees(kk, last[nt][i & 1]) && ((here >> (g + (i >> 1) * 8)) & 1u);
                 s[nt][i] = see ? s[nt][i] * p.scale : neg_inf();
             }
             move |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kLazy || fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kLazy;
@@ -259,7 +284,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         }
         // a tile that some row sees only in part: an infinity or NaN among its
         // values must not reach the rows that do not see it (0 * inf)
-        const bool partly = tile * 16 + 15 > least;
+        const bool partly = key0 + 15 > least || (MODE == kWindow && key0 < held && key0 + 16 > p.sink);
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             uint32_t a[4];
@@ -284,7 +309,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
                             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                                 for (int c = 0; c < 2; ++c)
-                                    if (tile * 16 + kk <= last[nt][c]) o[nt][i][2 * j + c] += x;
+                                    if (sees(key0 + kk, last[nt][c])) o[nt][i][2 * j + c] += x;
                         }
                     __syncwarp();
                 }
@@ -350,9 +375,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
             *reinterpret_cast<float2 *>(smem + Sm::kSum + (n * DP + d) * 4) = acc;
             if (d == 0) s_ml[n] = make_float2(M, L);
         } else {
-            const int64_t part = ((p.by_request ? (int64_t)r * p.max_q : rq.q0) + row / p.G) * p.Hq + head;
-            *reinterpret_cast<float2 *>(p.po + (part * p.S + split) * p.D + d) = acc;
-            if (d == 0) p.ml[part * p.S + split] = make_float2(M, L);
+            const int64_t first_row = MODE == kShared ? part0 : p.by_request ? (int64_t)r * p.max_q : rq.q0;
+            const int64_t part = (first_row + row / p.G) * p.Hq + head;
+            const int parts = MODE == kShared ? p.parts : p.S, piece_no = MODE == kShared ? p.first + split : split;
+            *reinterpret_cast<float2 *>(p.po + (part * parts + piece_no) * p.D + d) = acc;
+            if (d == 0) p.ml[part * parts + piece_no] = make_float2(M, L);
         }
     }
     if (!JOINED || whole) return;
@@ -485,41 +512,71 @@ bool tiles_fit(const kvi_attention &a, int32_t R, int32_t max_q, int32_t max_ctx
 //   + n - 1 then; the rows of a block are 8 nt, of all KV heads together;
 //   tiles: n S <= kPlanSms, and no more than `per` tokens of G heads a block.
 // Also no row has more pieces than there are 128 keys.
-size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
+int64_t most_parts(const kvi_attention &a, int32_t R, int64_t tokens, int32_t max_q, int32_t max_ctx)
 {
-    const int64_t G = a.q_heads / a.kv_heads, rows = part_rows(R, total_q, max_q) * a.q_heads;
+    const int64_t G = a.q_heads / a.kv_heads, rows = tokens * a.q_heads;
     const int64_t pieces = ((int64_t)max_ctx + 127) / 128;
     int64_t parts = max_ctx > kLongest ? 2 * rows : 0;
     auto at_most = [&](int64_t cap) { parts = std::max(parts, rows > cap ? cap : std::min(rows * pieces, cap)); };
     if (max_ctx > kRowsAlone) at_most(8 * (a.head_dim <= 128 && max_q * G > 8 ? 2 : 1) * (2 * kRowsWanted - 2));
     if (max_ctx > kTilesAlone && tiles_fit(a, R, max_q, max_ctx, 1, 8)) at_most(2 * tile_tokens((int)G) * G * kPlanSms);
+    return parts;
+}
+
+size_t part_bytes(const kvi_attention &a, int64_t parts)
+{
     return std::max<size_t>(256, up256((size_t)parts * a.head_dim * 4) + up256((size_t)parts * 8));
 }
 
-template <int DP, int NT, bool JOINED>
+size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
+{
+    return part_bytes(a, most_parts(a, R, part_rows(R, total_q, max_q), max_q, max_ctx));
+}
+
+// The same of a batch with a shared prefix: its keys' pieces and the others', of
+// which a row has one of each at least.
+size_t shared_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx, int32_t shared)
+{
+    const int64_t tokens = part_rows(R, total_q, max_q), rows = tokens * a.q_heads;
+    return part_bytes(a, std::max(rows, most_parts(a, 1, tokens, (int32_t)tokens, shared)) +
+                             std::max(rows, most_parts(a, R, tokens, max_q, max_ctx)));
+}
+
+template <int DP, int NT, bool JOINED, int MODE>
 cudaError_t run_rows_as(const PromptParams &p, int32_t R, cudaStream_t s)
 {
     const int bytes = RowsSmem<DP, NT>::kBytes;
-    const cudaError_t e = smem_opt_in(rows_kernel<DP, NT, JOINED>, bytes);
+    const cudaError_t e = smem_opt_in(rows_kernel<DP, NT, JOINED, MODE>, bytes);
     if (e != cudaSuccess) return e;
-    return launch_chained_clusters(rows_kernel<DP, NT, JOINED>, JOINED ? p.S : 1,
+    return launch_chained_clusters(rows_kernel<DP, NT, JOINED, MODE>, JOINED ? p.S : 1,
                                    dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes, s, p);
 }
 
-template <int DP, int NT>
+template <int DP, int NT, int MODE>
 cudaError_t run_rows(const PromptParams &p, int32_t R, cudaStream_t s)
 {
-    return p.joined ? run_rows_as<DP, NT, true>(p, R, s) : run_rows_as<DP, NT, false>(p, R, s);
+    if constexpr (MODE != kShared) {  // (whose pieces a second kernel joins)
+        if (p.joined) return run_rows_as<DP, NT, true, MODE>(p, R, s);
+    }
+    return run_rows_as<DP, NT, false, MODE>(p, R, s);
 }
 
+template <int MODE>
 cudaError_t launch_rows(const PromptParams &p, const PromptPlan &pl, int32_t R, cudaStream_t s)
 {
     switch (pl.dp) {
-    case 32: return pl.nt == 2 ? run_rows<32, 2>(p, R, s) : run_rows<32, 1>(p, R, s);
-    case 64: return pl.nt == 2 ? run_rows<64, 2>(p, R, s) : run_rows<64, 1>(p, R, s);
-    case 128: return pl.nt == 2 ? run_rows<128, 2>(p, R, s) : run_rows<128, 1>(p, R, s);
-    default: return run_rows<256, 1>(p, R, s);
+    case 32: return pl.nt == 2 ? run_rows<32, 2, MODE>(p, R, s) : run_rows<32, 1, MODE>(p, R, s);
+    case 64: return pl.nt == 2 ? run_rows<64, 2, MODE>(p, R, s) : run_rows<64, 1, MODE>(p, R, s);
+    case 128: return pl.nt == 2 ? run_rows<128, 2, MODE>(p, R, s) : run_rows<128, 1, MODE>(p, R, s);
+    default: return run_rows<256, 1, MODE>(p, R, s);
     }
+}
+
+cudaError_t launch_rows(const PromptParams &p, const PromptPlan &pl, int32_t R, int mode, cudaStream_t s)
+{
+    if (mode == kWindow) return launch_rows<kWindow>(p, pl, R, s);
+    if (mode == kShared) return launch_rows<kShared>(p, pl, R, s);
+    return launch_rows<kCausal>(p, pl, R, s);
 }
 
 bool sizes_ok(int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx)
@@ -540,6 +597,201 @@ extern "C" size_t kvi_attn_prompt_workspace_bytes(const kvi_attention *a, int32_
     return prompt_bytes(*a, R, total_q, max_q, max_ctx);
 }
 
+namespace {
+
+// The arguments that the calls on prompts share.
+struct PromptCall {
+    const char *name;
+    const kvi_attention *a;
+    int32_t R;
+    const void *q;
+    int64_t q_stride;
+    const int32_t *q_start;
+    int32_t total_q, max_q;
+    const int32_t *ctx_lens;
+    int32_t max_ctx;
+    const int32_t *tables;
+    int32_t max_blocks;
+    const kvi_paged_cache *cache;
+    int32_t layer;
+    void *out;
+    int64_t out_stride;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    int32_t *status;
+    kvi_stream_t stream;
+};
+
+kvi_status check_prompt(const PromptCall &c)
+{
+    kvi_status st = check_attention(c.a);
+    if (st != KVI_OK) return st;
+    st = check_pages(c.cache, c.layer, c.R, c.max_blocks, c.tables);
+    if (st != KVI_OK) return st;
+    if (!sizes_ok(c.R, c.total_q, c.max_q, c.max_ctx))
+        return arg_error("total_q=%d, max_q=%d (0..total_q) and max_ctx=%d must be >= 0", c.total_q, c.max_q, c.max_ctx);
+    if (unusable(c.q_start, 4) || unusable(c.ctx_lens, 4) || unusable(c.status, 4) || (c.total_q && (!c.q || !c.out)) ||
+        (c.lse && unusable(c.lse, 4)))
+        return arg_error("a required pointer (q, q_start, ctx_lens, out, status) is NULL, or one is misaligned");
+    const int64_t wide = (int64_t)c.a->q_heads * c.a->head_dim;
+    if (reinterpret_cast<uintptr_t>(c.q) % 16 || reinterpret_cast<uintptr_t>(c.out) % 16 || c.q_stride % 8 ||
+        c.out_stride % 8 || c.q_stride < wide || c.out_stride < wide)
+        return arg_error("q and out rows must be 16-byte aligned, with strides of at least q_heads * head_dim elements");
+    return KVI_OK;
+}
+
+kvi_status check_room(const PromptCall &c, int64_t blocks, int64_t rows, size_t need)
+{
+    if (blocks > 0x7fffffff || rows > (1 << 30)) return arg_error("max_q=%d is too large for this call", c.max_q);
+    if (!c.ws || c.ws_bytes < need || reinterpret_cast<uintptr_t>(c.ws) % 256)
+        return arg_error("workspace of %zu bytes (256-byte aligned) needed, %zu given", need, c.ws_bytes);
+    return KVI_OK;
+}
+
+PromptParams params_of(const PromptCall &c, const PromptPlan &pl)
+{
+    PromptParams p{};
+    p.q = static_cast<const __nv_bfloat16 *>(c.q);
+    p.q_stride = c.q_stride;
+    p.q_start = c.q_start;
+    p.R = c.R;
+    p.total_q = c.total_q;
+    p.max_q = c.max_q;
+    p.G = c.a->q_heads / c.a->kv_heads;
+    p.per = tile_tokens(p.G);
+    p.ctx_lens = c.ctx_lens;
+    p.max_ctx = c.max_ctx;
+    p.max_blocks = c.max_blocks;
+    p.block_tables = c.tables;
+    p.num_blocks = c.cache->num_blocks;
+    p.B = c.cache->block_size;
+    p.H = c.a->kv_heads;
+    p.Hq = c.a->q_heads;
+    p.D = c.a->head_dim;
+    p.pool = static_cast<const __nv_bfloat16 *>(c.cache->layer_base[c.layer]);
+    p.scale = c.a->scale * kLog2e;
+    p.out = static_cast<__nv_bfloat16 *>(c.out);
+    p.out_stride = c.out_stride;
+    p.lse = c.lse;
+    p.chunks = (int)pl.chunks;
+    p.S = pl.S;
+    p.span = pl.span;
+    p.joined = pl.joined;
+    p.by_request = c.total_q > (int64_t)c.R * c.max_q;
+    p.po = static_cast<float *>(c.ws);
+    p.status = c.status;
+    return p;
+}
+
+JoinParams join_of(const PromptCall &c, const PromptParams &p)
+{
+    JoinParams j{};
+    j.po = p.po;
+    j.ml = p.ml;
+    j.by_request = p.by_request;
+    j.S = p.S;
+    j.span = p.span;
+    j.R = c.R;
+    j.q_heads = p.Hq;
+    j.D = p.D;
+    j.q_start = c.q_start;
+    j.total_q = c.total_q;
+    j.max_q = c.max_q;
+    j.ctx_lens = c.ctx_lens;
+    j.max_ctx = c.max_ctx;
+    j.max_blocks = c.max_blocks;
+    j.block_size = p.B;
+    j.out = p.out;
+    j.out_stride = c.out_stride;
+    j.lse = c.lse;
+    return j;
+}
+
+cudaError_t launch_form(const PromptParams &p, const PromptPlan &pl, int32_t R, int mode, cudaStream_t s)
+{
+    return pl.tiles ? launch_tiles(p, mode, s) : launch_rows(p, pl, R, mode, s);
+}
+
+// Keys that the pieces of a row with a window cover at most: the blocks' tiles of
+// `unit` keys from the first window of `tokens` tokens on, and the first ones.
+int32_t window_cap(int32_t window, int32_t sink, int unit, int tokens)
+{
+    const int64_t cap = ((int64_t)sink + unit - 1) / unit * unit + window + tokens + 2 * unit;
+    return (int32_t)std::min<int64_t>(cap, 0x7fffffff);
+}
+
+kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t sink)
+{
+    const kvi_attention &a = *c.a;
+    // The tiles' windows are no shorter than a block's rows, which check_values
+    // counts on (shorter ones have few keys to a row, and suit the other form).
+    const int tokens = 2 * tile_tokens(a.q_heads / a.kv_heads);
+    const int32_t tile_cap = mode == kWindow ? window_cap(window, sink, 128, tokens) : 0x7fffffff;
+    int32_t cap = tile_cap;
+    PromptPlan pl{};
+    if ((mode != kWindow || window >= tokens) &&
+        tiles_fit(a, c.R, c.max_q, std::min(c.max_ctx, tile_cap), c.cache->num_blocks, c.cache->block_size)) {
+        pl = plan_tiles(a, c.R, c.total_q, c.max_q, std::min(c.max_ctx, cap));
+    } else {
+        if (mode == kWindow) cap = window_cap(window, sink, 16, 16);
+        pl = plan_rows(a, c.R, c.total_q, c.max_q, std::min(c.max_ctx, cap));
+    }
+    kvi_status st = check_room(c, pl.chunks * pl.S * a.kv_heads, (int64_t)c.max_q * (a.q_heads / a.kv_heads),
+                               std::max<size_t>(256, pl.total));
+    if (st != KVI_OK || c.max_q == 0) return st;  // (or no rows)
+    PromptParams p = params_of(c, pl);
+    p.ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(c.ws) + pl.ml);
+    p.window = window;
+    p.sink = sink;
+    p.cap = cap;
+    st = cuda_status(launch_form(p, pl, c.R, mode, c.stream), c.name);
+    if (st != KVI_OK || pl.S == 1 || pl.joined) return st;
+    JoinParams j = join_of(c, p);
+    j.cap = cap;
+    return cuda_status(launch_join(j, c.stream), c.name);
+}
+
+kvi_status attend_shared(const PromptCall &c, int32_t shared)
+{
+    const kvi_attention &a = *c.a;
+    const int32_t blocks = c.cache->num_blocks, B = c.cache->block_size, own = c.max_ctx - shared;
+    const int64_t tokens = part_rows(c.R, c.total_q, c.max_q), rows = tokens * a.q_heads;
+    const int32_t all = (int32_t)tokens;
+    const PromptPlan first = tiles_fit(a, 1, all, shared, blocks, B) ? plan_tiles(a, 1, all, all, shared)
+                                                                     : plan_rows(a, 1, all, all, shared);
+    const PromptPlan rest = tiles_fit(a, c.R, c.max_q, own, blocks, B) ? plan_tiles(a, c.R, c.total_q, c.max_q, own)
+                                                                       : plan_rows(a, c.R, c.total_q, c.max_q, own);
+    const int parts = first.S + rest.S;
+    const size_t ml = up256((size_t)rows * parts * a.head_dim * 4);
+    kvi_status st = check_room(c, std::max(first.chunks * first.S, rest.chunks * rest.S) * a.kv_heads,
+                               tokens * (a.q_heads / a.kv_heads),
+                               std::max<size_t>(256, ml + up256((size_t)rows * parts * 8)));
+    if (st != KVI_OK || c.max_q == 0) return st;
+    PromptParams p = params_of(c, first);
+    p.ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(c.ws) + ml);
+    p.shared = shared;
+    p.parts = parts;
+    p.flat = 1;
+    st = cuda_status(launch_form(p, first, 1, kShared, c.stream), c.name);
+    if (st != KVI_OK) return st;
+    p.flat = 0;
+    p.first = first.S;
+    p.chunks = (int)rest.chunks;
+    p.S = rest.S;
+    p.span = rest.span;
+    p.joined = 0;
+    st = cuda_status(launch_form(p, rest, c.R, kShared, c.stream), c.name);
+    if (st != KVI_OK) return st;
+    JoinParams j = join_of(c, p);
+    j.S = parts;
+    j.first = first.S;
+    j.shared = shared;
+    return cuda_status(launch_join(j, c.stream), c.name);
+}
+
+}  // namespace
+
 extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,
                                       const int32_t *d_q_start, int32_t total_q, int32_t max_q,
                                       const int32_t *d_ctx_lens, int32_t max_ctx, const int32_t *d_block_tables,
@@ -547,80 +799,53 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
                                       int64_t out_row_stride, float *d_lse, void *d_ws, size_t ws_bytes,
                                       int32_t *d_status, kvi_stream_t stream)
 {
-    kvi_status st = check_attention(a);
+    const PromptCall c{"kvi_attn_prompt", a, R, d_q, q_row_stride, d_q_start, total_q, max_q, d_ctx_lens, max_ctx,
+                       d_block_tables, max_blocks, cache, layer, d_out, out_row_stride, d_lse, d_ws, ws_bytes, d_status,
+                       stream};
+    const kvi_status st = check_prompt(c);
+    return st != KVI_OK ? st : attend_prompts(c, kCausal, 0, 0);
+}
+
+extern "C" kvi_status kvi_attn_window(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,
+                                      const int32_t *d_q_start, int32_t total_q, int32_t max_q,
+                                      const int32_t *d_ctx_lens, int32_t max_ctx, const int32_t *d_block_tables,
+                                      int32_t max_blocks, const kvi_paged_cache *cache, int32_t layer, int32_t window,
+                                      int32_t sink, void *d_out, int64_t out_row_stride, float *d_lse, void *d_ws,
+                                      size_t ws_bytes, int32_t *d_status, kvi_stream_t stream)
+{
+    const PromptCall c{"kvi_attn_window", a, R, d_q, q_row_stride, d_q_start, total_q, max_q, d_ctx_lens, max_ctx,
+                       d_block_tables, max_blocks, cache, layer, d_out, out_row_stride, d_lse, d_ws, ws_bytes, d_status,
+                       stream};
+    const kvi_status st = check_prompt(c);
     if (st != KVI_OK) return st;
-    st = check_pages(cache, layer, R, max_blocks, d_block_tables);
+    if (window < 1 || sink < 0) return arg_error("window=%d must be >= 1 and sink=%d >= 0", window, sink);
+    if (window >= max_ctx || sink >= max_ctx) return attend_prompts(c, kCausal, 0, 0);  // every row sees all before it
+    if (window > (1 << 30)) return arg_error("window=%d is above 2^30", window);
+    return attend_prompts(c, kWindow, window, sink);
+}
+
+extern "C" size_t kvi_attn_shared_workspace_bytes(const kvi_attention *a, int32_t R, int32_t total_q, int32_t max_q,
+                                                  int32_t max_ctx, int32_t shared)
+{
+    if (check_attention(a) != KVI_OK || !sizes_ok(R, total_q, max_q, max_ctx) || shared < 0) return 0;
+    return shared_bytes(*a, R, total_q, max_q, max_ctx, std::min(shared, max_ctx));
+}
+
+extern "C" kvi_status kvi_attn_shared(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,
+                                      const int32_t *d_q_start, int32_t total_q, int32_t max_q,
+                                      const int32_t *d_ctx_lens, int32_t max_ctx, const int32_t *d_block_tables,
+                                      int32_t max_blocks, const kvi_paged_cache *cache, int32_t layer, int32_t shared,
+                                      void *d_out, int64_t out_row_stride, float *d_lse, void *d_ws, size_t ws_bytes,
+                                      int32_t *d_status, kvi_stream_t stream)
+{
+    const PromptCall c{"kvi_attn_shared", a, R, d_q, q_row_stride, d_q_start, total_q, max_q, d_ctx_lens, max_ctx,
+                       d_block_tables, max_blocks, cache, layer, d_out, out_row_stride, d_lse, d_ws, ws_bytes, d_status,
+                       stream};
+    const kvi_status st = check_prompt(c);
     if (st != KVI_OK) return st;
-    if (!sizes_ok(R, total_q, max_q, max_ctx))
-        return arg_error("total_q=%d, max_q=%d (0..total_q) and max_ctx=%d must be >= 0", total_q, max_q, max_ctx);
-    if (unusable(d_q_start, 4) || unusable(d_ctx_lens, 4) || unusable(d_status, 4) || (total_q && (!d_q || !d_out)) ||
-        (d_lse && unusable(d_lse, 4)))
-        return arg_error("a required pointer (q, q_start, ctx_lens, out, status) is NULL, or one is misaligned");
-    const int64_t wide = (int64_t)a->q_heads * a->head_dim;
-    if (reinterpret_cast<uintptr_t>(d_q) % 16 || reinterpret_cast<uintptr_t>(d_out) % 16 || q_row_stride % 8 ||
-        out_row_stride % 8 || q_row_stride < wide || out_row_stride < wide)
-        return arg_error("q and out rows must be 16-byte aligned, with strides of at least q_heads * head_dim elements");
-    const PromptPlan pl = tiles_fit(*a, R, max_q, max_ctx, cache->num_blocks, cache->block_size)
-                              ? plan_tiles(*a, R, total_q, max_q, max_ctx)
-                              : plan_rows(*a, R, total_q, max_q, max_ctx);
-    const size_t need = std::max<size_t>(256, pl.total);
-    if (pl.chunks * pl.S * a->kv_heads > 0x7fffffff || (int64_t)max_q * (a->q_heads / a->kv_heads) > (1 << 30))
-        return arg_error("max_q=%d is too large for this call", max_q);
-    if (!d_ws || ws_bytes < need || reinterpret_cast<uintptr_t>(d_ws) % 256)
-        return arg_error("workspace of %zu bytes (256-byte aligned) needed, %zu given", need, ws_bytes);
-    uint8_t *ws = static_cast<uint8_t *>(d_ws);
-    PromptParams p{};
-    p.q = static_cast<const __nv_bfloat16 *>(d_q);
-    p.q_stride = q_row_stride;
-    p.q_start = d_q_start;
-    p.R = R;
-    p.total_q = total_q;
-    p.max_q = max_q;
-    p.per = tile_tokens(a->q_heads / a->kv_heads);
-    p.ctx_lens = d_ctx_lens;
-    p.max_ctx = max_ctx;
-    p.max_blocks = max_blocks;
-    p.block_tables = d_block_tables;
-    p.num_blocks = cache->num_blocks;
-    p.B = cache->block_size;
-    p.H = a->kv_heads;
-    p.Hq = a->q_heads;
-    p.G = a->q_heads / a->kv_heads;
-    p.D = a->head_dim;
-    p.pool = static_cast<const __nv_bfloat16 *>(cache->layer_base[layer]);
-    p.scale = a->scale * kLog2e;
-    p.out = static_cast<__nv_bfloat16 *>(d_out);
-    p.out_stride = out_row_stride;
-    p.lse = d_lse;
-    p.chunks = (int)pl.chunks;
-    p.S = pl.S;
-    p.span = pl.span;
-    p.joined = pl.joined;
-    p.by_request = total_q > (int64_t)R * max_q;
-    p.po = reinterpret_cast<float *>(ws);
-    p.ml = reinterpret_cast<float2 *>(ws + pl.ml);
-    p.status = d_status;
-    if (max_q == 0) return KVI_OK;  // no rows
-    st = cuda_status(pl.tiles ? launch_tiles(p, stream) : launch_rows(p, pl, R, stream), "kvi_attn_prompt");
-    if (st != KVI_OK || pl.S == 1 || pl.joined) return st;
-    JoinParams j{};
-    j.po = p.po;
-    j.ml = p.ml;
-    j.by_request = p.by_request;
-    j.S = pl.S;
-    j.span = pl.span;
-    j.R = R;
-    j.q_heads = a->q_heads;
-    j.D = a->head_dim;
-    j.q_start = d_q_start;
-    j.total_q = total_q;
-    j.max_q = max_q;
-    j.ctx_lens = d_ctx_lens;
-    j.max_ctx = max_ctx;
-    j.max_blocks = max_blocks;
-    j.block_size = cache->block_size;
-    j.out = p.out;
-    j.out_stride = out_row_stride;
-    j.lse = d_lse;
-    return cuda_status(launch_join(j, stream), "kvi_attn_prompt");
+    if (shared < 0 || shared % cache->block_size || (int64_t)shared > (int64_t)max_blocks * cache->block_size ||
+        (shared && shared >= max_ctx))
+        return arg_error("shared=%d must be whole blocks of %d, fewer keys than max_ctx=%d and in the block tables", shared,
+                         cache->block_size, max_ctx);
+    return shared == 0 ? attend_prompts(c, kCausal, 0, 0) : attend_shared(c, shared);
 }

@@ -81,6 +81,7 @@ struct TileTail {
     int32_t odd;            // `first` holds something
     int32_t lost;           // a key's block lies outside the pool
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
+    int32_t newest[3][DP];  // (windows) of the keys up to the block's first row, the last such
     int32_t part0;          // row of token 0 among the partial results
 };
 
@@ -249,8 +250,13 @@ __device__ __forceinline__ void box3_out(const CUtensorMap *map, int x, int y, i
 // The warp that copies V looks over a tile of it before the products.  An infinity or NaN
 // becomes zero, noted with its key for the rows that see it (a key past the end
 // is seen by none).  The rule is that there is none: one maximum a word.
-template <int DP>
-__device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> &tl)
+// With a window the rows that see a key are those from its position on, if that
+// lies past the block's first row (`row0`), and else those whose window still
+// reaches it: no window is shorter than a block's rows.  So of the former the
+// first key says who sees any, of the latter the last (the first `sink` keys
+// count as the latest of all).
+template <int DP, int MODE>
+__device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> &tl, int row0, int sink)
 {
     constexpr int kChunks = TileSmem<DP>::kTile / 16;
     const int lane = threadIdx.x & 31;
@@ -267,7 +273,10 @@ __device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> 
     const bool odd = (bits & 0x7f80u) == 0x7f80u || (bits & 0x7f800000u) == 0x7f800000u;
     if (!__any_sync(0xffffffffu, odd)) return;
     if (!tl.odd)
-        for (int i = lane; i < 3 * DP; i += 32) (&tl.first[0][0])[i] = INT32_MAX;
+        for (int i = lane; i < 3 * DP; i += 32) {
+            (&tl.first[0][0])[i] = INT32_MAX;
+            if (MODE == kWindow) (&tl.newest[0][0])[i] = INT32_MIN;
+        }
     __syncwarp();
     if (lane == 0) tl.odd = 1;
     uint16_t *e = reinterpret_cast<uint16_t *>(v);
@@ -278,7 +287,11 @@ __device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> 
         for (int k = 0; k < 8; ++k) {
             const uint32_t b = e[8 * i + k];
             if ((b & 0x7f80u) != 0x7f80u) continue;
-            atomicMin(&tl.first[b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2][64 * half + 8 * chunk + k], key0 + row);
+            const int key = key0 + row, which = b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2, channel = 64 * half + 8 * chunk + k;
+            if (MODE == kWindow && key <= row0)
+                atomicMax(&tl.newest[which][channel], key < sink ? INT32_MAX : key);
+            else
+                atomicMin(&tl.first[which][channel], key);
             e[8 * i + k] = 0;
         }
     }
@@ -301,6 +314,13 @@ __device__ __forceinline__ float largest64(const float *s)
     return fmaxf(max3(t[0], t[1], t[2]), t[3]);
 }
 
+// Scores of columns from `past` on that are below `low` are not seen
+__device__ __forceinline__ void mask_low_scores(float *s, int past, int low)
+{
+#pragma unroll
+    for (int c = 0; c < kM; ++c) s[c] = c >= past && c < low ? neg_inf() : s[c];
+}
+
 // Scores from column `vis` on are not seen
 __device__ __forceinline__ void mask_scores(float *s, int vis)
 {
@@ -321,7 +341,7 @@ __device__ __forceinline__ void announce(uint64_t &bar)
                  : "memory");
 }
 
-template <int DP>
+template <int DP, int MODE>
 __global__ void __launch_bounds__(kTileThreads, 1)
 tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
             const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ PromptParams p, int box_shift)
@@ -365,11 +385,22 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     int item = (int)(rest / (uint32_t)p.H), r = -1, pair = 0;
     const int h = (int)(rest - (uint32_t)item * (uint32_t)p.H);
     RequestSpan rq{0, 0, 0};
-    for (int r0 = 0; r0 < p.R; r0 += 32) {
+    int part0 = 0;
+    const bool flat = MODE == kShared && p.flat;
+    if (flat) {
+        pair = item;
+        r = batch_rows(p, rq);
+        if (pair * 2 * per >= rq.n_q) return;
+    }
+    for (int r0 = 0; !flat && r0 < p.R; r0 += 32) {
         RequestSpan c{0, 0, 0};
         const bool asked = r0 + lane < p.R;
-        const bool good = asked && request_span(r0 + lane, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
-                                                p.max_blocks, p.B, c);
+        int c_part0 = 0;
+        const bool good = asked && (MODE == kShared
+                                        ? request_past_prefix(r0 + lane, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens,
+                                                              p.max_ctx, p.max_blocks, p.B, p.shared, c, c_part0)
+                                        : request_span(r0 + lane, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
+                                                       p.max_blocks, p.B, c));
         if (asked && !good && h == 0 && split == 0 && warp == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         const int pairs = good ? (c.n_q + 2 * per - 1) / (2 * per) : 0;
         int sum = pairs;
@@ -386,29 +417,55 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             rq.q0 = __shfl_sync(0xffffffffu, c.q0, from_lane);
             rq.n_q = __shfl_sync(0xffffffffu, c.n_q, from_lane);
             rq.ctx = __shfl_sync(0xffffffffu, c.ctx, from_lane);
+            if (MODE == kShared) part0 = __shfl_sync(0xffffffffu, c_part0, from_lane);
             break;
         }
         item -= __shfl_sync(0xffffffffu, sum, 31);
     }
     if (r < 0) return;
     const int tok0 = pair * 2 * per;  // the block's first token
-    const bool whole = rq.ctx <= p.span;  // its keys are one piece
-    if (split > 0 && (int64_t)split * p.span >= rq.ctx) return;
-    const int seen0 = rq.ctx - rq.n_q;  // last position that token 0 sees
+    const int keys = MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx;  // that its pieces are for
+    const bool whole = MODE != kShared && keys <= p.span;            // they are one piece
+    if (split > 0 && (int64_t)split * p.span >= keys) return;
+    const int seen0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
+    // With a window the tiles are those of the first `sink` keys and those from the
+    // block's first window on: tile j from `from` on is at key from + 128 j, or
+    // `skip` keys further from tile `skip_at` on.
+    // Boxes before that window (no row sees them) are not read.
+    const int low = MODE == kWindow ? seen0 + tok0 - p.window + 1 : 0;
+    int skip = 0, skip_at = 0;
+    if (MODE == kWindow) {
+        const int start = max(0, low) / kM;
+        const int kept = min(start, (int)(((int64_t)p.sink + kM - 1) / kM));
+        skip = (start - kept) * kM;
+        skip_at = kept - from / kM;
+    }
+    auto key_of = [&](int j) { return from + j * kM + (MODE == kWindow && j >= skip_at ? skip : 0); };
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
     int n_tiles[2];  // (indexed by constants alone: they stay in registers)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t0 = tok0 + i * per, t1 = min(rq.n_q, t0 + per);
-        const int end = t0 < rq.n_q ? min(seen0 + t1, from + p.span) : 0;
+        const int seen = (flat ? rq.ctx : seen0 + t1) - skip;
+        const int end = t0 < rq.n_q ? min(seen, from + p.span) : 0;
         n_tiles[i] = max(0, (end - from + kM - 1) / kM);
     }
     const int n = max(n_tiles[0], n_tiles[1]);
-    const int sure = seen0 + tok0 + 1;  // keys below it are seen by every row
-    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks;
+    const int sure = seen0 + (flat ? 0 : tok0) + 1;  // keys below it are seen by every row
+    // with a window, those from `held` on, too, and the first `sink`
+    const int held = MODE == kWindow ? seen0 + min(rq.n_q, tok0 + 2 * per) - p.window : 0;
+    // whether some row sees a tile's keys in part (0: all tiles from `first_partly` on)
+    const int first_partly = sure > from ? (sure - from) / kM : 0;
+    auto partly = [&](int j) {
+        if (MODE != kWindow) return j >= first_partly;
+        const int key0 = key_of(j);
+        return key0 + kM > sure || (key0 < held && key0 + kM > p.sink);
+    };
+    const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks + (MODE == kShared && !flat ? p.shared / p.B : 0);
 
-    if (tid == 0) tl.part0 = p.by_request ? r * p.max_q : rq.q0;  // (below total_q; here, as r is not kept to the end)
+    // (below total_q; here, as r is not kept to the end)
+    if (tid == 0) tl.part0 = MODE == kShared ? part0 : p.by_request ? r * p.max_q : rq.q0;
 
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
@@ -416,15 +473,18 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int half = lane >> box_shift, box = lane & ((1 << box_shift) - 1), box_keys = kM >> box_shift;
     // (Its block is asked for a tile ahead.)
     int at_token = 0, at_block = 0;
+    auto wanted = [&](int key) {
+        return key < rq.ctx && (MODE != kWindow || key + box_keys > low || key < p.sink);
+    };
     auto block_of = [&](int j) {
-        const int key = from + j * kM + box * box_keys;
-        return key < rq.ctx ? table[(uint32_t)key / (uint32_t)p.B] : -1;
+        const int key = key_of(j) + box * box_keys;
+        return wanted(key) ? table[(uint32_t)key / (uint32_t)p.B] : -1;
     };
     auto look_up = [&](int j, int block) {
-        const int key = from + j * kM + box * box_keys;
+        const int key = key_of(j) + box * box_keys;
         const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
         // (noted before the copy is asked for, so before its scores are looked at)
-        if (warp == kCopyK && __any_sync(0xffffffffu, key < rq.ctx && !there) && lane == 0) {
+        if (warp == kCopyK && __any_sync(0xffffffffu, wanted(key) && !there) && lane == 0) {
             tl.lost = 1;
             record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         }
@@ -479,16 +539,15 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         // V of the tiles that some row sees in part is looked over before the next
         // V is asked for (it has been there for a while by then)
-        const int first_partly = sure > from ? (sure - from) / kM : 0;
         auto look_over = [&](int j) {
-            if (plane == 0 || j < first_partly) return true;
+            if (plane == 0 || !partly(j)) return true;
             const int slot = 2 * j + 1;  // (V's stages are the odd ones)
             const bool got = mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, got)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 return false;
             }
-            check_values<DP>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl);
+            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, key_of(j), tl, sure - 1, p.sink);
             if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
             return true;
         };
@@ -560,14 +619,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                            add || half > 0 || k > 0);
             };
             const int n0 = n_tiles[0], n1 = n_tiles[1];
-            const int first_partly = sure > from ? (sure - from) / kM : 0;  // first tile that some row sees in part
             uint32_t fixes = 0;  // the phase of each v_fixed, a bit a stage
             // Tile j of the keys, V in stage `vs` and K of j + 1 in stage `ks`; V's
             // copy has been waited for.
             auto step = [&](int j, uint32_t vs, uint32_t vnext, uint32_t ks, uint32_t kph, uint32_t vnph) {
                 const uint32_t par = (uint32_t)(j & 1);
                 const bool more0 = j + 1 < n0, more1 = j + 1 < n1, more = more0 || more1;
-                if (j >= first_partly) {
+                if (partly(j)) {
                     if (!wait(fixed_bar + 4 * (vs - 1), (fixes >> vs) & 1u)) return false;
                     fixes ^= 1u << vs;
                 }
@@ -642,13 +700,13 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t t_s = tmem + lanes + i * kM, t_o = tmem + lanes + kColO + i * DP;
         const int token = tok0 + i * per + row / p.G;
         const bool real = row < per * p.G && token < rq.n_q;
-        const int last = seen0 + token;
+        const int last = seen0 + (flat ? 0 : token);
         float m = neg_inf(), limit = real ? neg_inf() : __int_as_float(0x7f800000), ref = 0.f, sum = 0.f;
         const float lazy = kLazy / p.scale;
         bool ok = true;
         for (int j = 0; j < my; ++j) {
-            const int key0 = from + j * kM;
-            const bool partly = key0 + kM > sure;
+            const int key0 = key_of(j);
+            const bool in_part = MODE == kWindow ? partly(j) : key0 + kM > sure;
             ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
@@ -668,10 +726,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tmem_load32(t_s + 96, s + 96);
             float top;
             const bool lost = *reinterpret_cast<volatile int32_t *>(&tl.lost) != 0;
-            if (partly || lost) {
+            if (in_part || lost) {
                 tmem_wait_ld(s + 64);
                 tmem_wait_ld(s + 96);
                 mask_scores(s, last + 1 - key0);
+                if (MODE == kWindow) mask_low_scores(s, p.sink - key0, last - p.window + 1 - key0);
                 if (lost) {
                     uint32_t gone[4] = {0, 0, 0, 0};
                     for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
@@ -752,6 +811,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int head = h * p.G + row % p.G;
             const int64_t tok = rq.q0 + token, at = tok * p.Hq + head;
             const int64_t part = ((int64_t)tl.part0 + token) * p.Hq + head;
+            const int parts = MODE == kShared ? p.parts : p.S, piece_no = MODE == kShared ? p.first + split : split;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
             // 32 channels of the row
@@ -765,11 +825,15 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 if (odd) {
                     const float inf = __int_as_float(0x7f800000);
+                    auto sees = [&](int which, int channel) {
+                        return tl.first[which][channel] <= last ||
+                               (MODE == kWindow && tl.newest[which][channel] > last - p.window);
+                    };
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        if (tl.first[0][c + e] <= last) v[e] += inf;
-                        if (tl.first[1][c + e] <= last) v[e] -= inf;
-                        if (tl.first[2][c + e] <= last) v[e] += inf - inf;
+                        if (sees(0, c + e)) v[e] += inf;
+                        if (sees(1, c + e)) v[e] -= inf;
+                        if (sees(2, c + e)) v[e] += inf - inf;
                     }
                     __syncwarp();
                 }
@@ -797,7 +861,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 uint4 *stage = reinterpret_cast<uint4 *>(base + Sm::kQ + i * Sm::kTile) + (warp & 3) * 32 * kPieces;
                 const uint64_t mine = reinterpret_cast<uint64_t>(
                     whole ? static_cast<void *>(p.out + tok * p.out_stride + (int64_t)head * p.D)
-                          : static_cast<void *>(p.po + (part * p.S + split) * p.D));
+                          : static_cast<void *>(p.po + (part * parts + piece_no) * p.D));
                 const uint32_t rows_there = __ballot_sync(0xffffffffu, real);
 #pragma unroll 1
                 for (int pass = 0; pass < (whole ? 1 : 2); ++pass) {
@@ -834,7 +898,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (real) {
                 const float M = m * p.scale;
                 if (!whole)
-                    p.ml[part * p.S + split] = make_float2(M, sum);
+                    p.ml[part * parts + piece_no] = make_float2(M, sum);
                 else if (p.lse)
                     p.lse[at] = sum == 0.f ? neg_inf() : (M + log2f(sum)) * kLn2;
             }
@@ -866,7 +930,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 
 }  // namespace
 
-template <int DP>
+template <int DP, int MODE>
 static cudaError_t run_tiles(const PromptParams &p, cudaStream_t s)
 {
     CUtensorMap tq, tkv, to;
@@ -893,15 +957,17 @@ static cudaError_t run_tiles(const PromptParams &p, cudaStream_t s)
     if (e != cudaSuccess) return e;
     constexpr int bytes = TileSmem<DP>::kTail + (int)sizeof(TileTail<DP>) + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory");
-    e = smem_opt_in(tile_kernel<DP>, bytes);
+    e = smem_opt_in(tile_kernel<DP, MODE>, bytes);
     if (e != cudaSuccess) return e;
-    return launch_chained(tile_kernel<DP>, dim3((unsigned)(p.S * p.H * p.chunks)), kTileThreads, bytes, s, tq,
+    return launch_chained(tile_kernel<DP, MODE>, dim3((unsigned)(p.S * p.H * p.chunks)), kTileThreads, bytes, s, tq,
                           tkv, to, p, shift);
 }
 
-cudaError_t launch_tiles(const PromptParams &p, cudaStream_t s)
+cudaError_t launch_tiles(const PromptParams &p, int mode, cudaStream_t s)
 {
-    return p.D <= 64 ? run_tiles<64>(p, s) : run_tiles<128>(p, s);
+    if (mode == kWindow) return p.D <= 64 ? run_tiles<64, kWindow>(p, s) : run_tiles<128, kWindow>(p, s);
+    if (mode == kShared) return p.D <= 64 ? run_tiles<64, kShared>(p, s) : run_tiles<128, kShared>(p, s);
+    return p.D <= 64 ? run_tiles<64, kCausal>(p, s) : run_tiles<128, kCausal>(p, s);
 }
 
 }  // namespace kvi

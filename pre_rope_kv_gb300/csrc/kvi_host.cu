@@ -13,6 +13,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <string>
 #include <thread>
@@ -299,9 +300,14 @@ kvi_status rope_get(const kvi_rope &spec, int32_t D, int32_t needed, cudaStream_
     const unsigned hw = std::max(1u, std::min(16u, std::thread::hardware_concurrency()));
     const int32_t nthr = (int32_t)std::min<unsigned>(hw, (unsigned)((P + 1023) / 1024));
     std::vector<std::thread> pool;
+    pool.reserve(nthr);
     for (int32_t t = 0; t < nthr; ++t) {
         const int32_t a = (int32_t)((int64_t)P * t / nthr), b = (int32_t)((int64_t)P * (t + 1) / nthr);
-        pool.emplace_back(fill_rope_rows, omega.data(), given ? &spec : nullptr, D, a, b, host.data());
+        try {
+            pool.emplace_back(fill_rope_rows, omega.data(), given ? &spec : nullptr, D, a, b, host.data());
+        } catch (const std::exception &) {  // no further thread to be had
+            fill_rope_rows(omega.data(), given ? &spec : nullptr, D, a, b, host.data());
+        }
     }
     for (auto &th : pool) th.join();
     float4 *d = nullptr;
@@ -432,6 +438,20 @@ SharedWs shared_layout(int32_t R, int64_t n_facts, int32_t k)
     x.cand_n = at; at = up(at + (size_t)R * 4);
     x.total = at;
     return x;
+}
+
+kvi_status rope_table(const kvi_rope *rope, int32_t head_dim, int32_t max_position, cudaStream_t stream,
+                      const float4 **table, int32_t *positions)
+{
+    const kvi_status st = check_rope(rope);
+    if (st != KVI_OK) return st;
+    if (max_position <= 0 || max_position > kMaxRopePositions)
+        return fail(KVI_ERR_INVALID_ARG, "max_position=%d outside [1, 2^22]", max_position);
+    try {
+        return rope_get(*rope, head_dim, max_position, stream, table, positions);
+    } catch (const std::exception &e) {  // (no memory or no thread for a new table)
+        return fail(KVI_ERR_CUDA, "RoPE table: %s", e.what());
+    }
 }
 
 }  // namespace kvi

@@ -243,6 +243,11 @@ kvi_status check_full_store(const kvi_store_view *s);
 // The library's compile-time geometry limits (records a message on failure).
 kvi_status check_store_geometry(const kvi_geometry *g);
 
+// The current device's RoPE table of *rope (checked here) for positions
+// [0, max_position), or a caller's table's own rows.
+kvi_status rope_table(const kvi_rope *rope, int32_t head_dim, int32_t max_position, cudaStream_t stream,
+                      const float4 **table, int32_t *positions);
+
 // Device facts cached per device (SM count).
 struct DeviceInfo {
     int sms;
