@@ -785,9 +785,7 @@ def kvi_attn_shared(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
 
 
 def _norm_weight(t, head_dim: int, name: str):
-    if t is None:
-        return None
-    if t.dtype is not (_types or _dtypes())[0] or t.shape != (head_dim,) or not t.is_contiguous():
+    if t.dtype is not _types[0] or t.dim() != 1 or t.numel() != head_dim or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous bfloat16 [{head_dim}]")
     return t.data_ptr()
 
@@ -799,29 +797,40 @@ def kvi_norm_rope(a: Attention, spec: Rope, max_position: int, positions, q, k, 
     weight [D]), rotated to positions int32 [T], to q_out and k_out (None: not
     wanted) and, with v, to slots int64 [T] of a layer of the paged cache;
     k_plain takes the keys before rotation.  q and q_out None: keys alone."""
-    T, heads, kv, dim = positions.shape[0], a.q_heads, a.kv_heads, a.head_dim
-
-    def rows(t, n, name):
-        return (None, 0) if t is None else _rows(t, n, dim, name, T)
-
-    pool = None
-    if cache is not None:
-        pool = cache.struct if (layer, kv, dim) in getattr(cache, "fits", ()) else _pool(a, cache, layer)
-    if positions.dtype is not (_types or _dtypes())[1] or not positions.is_contiguous():
+    bf16, ints, longs, _ = _types or _dtypes()
+    T, heads, kv, dim = positions.numel(), a.q_heads, a.kv_heads, a.head_dim
+    none = (None, 0)
+    if cache is None:
+        pool = None
+    elif type(cache) is _Cache and (layer, kv, dim) in cache.fits:
+        pool = cache.struct
+    else:
+        pool = _pool(a, cache, layer)
+    if positions.dtype is not ints or positions.dim() != 1 or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int32")
-    if slots is not None and (slots.dtype is not _types[2] or not slots.is_contiguous() or slots.shape[0] < T):
+    if slots is not None and (slots.dtype is not longs or slots.dim() != 1 or not slots.is_contiguous() or slots.numel() < T):
         raise ValueError(f"slots must be contiguous int64, at least {T} long")
     _check(load_library().kvi_norm_rope(
-        a, spec, max_position, T, positions.data_ptr(), *rows(q, heads, "q"), *rows(k, kv, "k"),
-        _norm_weight(q_weight, dim, "q_weight"), _norm_weight(k_weight, dim, "k_weight"), eps, *rows(q_out, heads, "q_out"),
-        *rows(k_out, kv, "k_out"), *rows(k_plain, kv, "k_plain"), *rows(v, kv, "v"), pool, layer, _ptr(slots),
+        a, spec, max_position, T, positions.data_ptr(), *(none if q is None else _rows(q, heads, dim, "q", T)),
+        *_rows(k, kv, dim, "k", T), None if q_weight is None else _norm_weight(q_weight, dim, "q_weight"),
+        None if k_weight is None else _norm_weight(k_weight, dim, "k_weight"), eps,
+        *(none if q_out is None else _rows(q_out, heads, dim, "q_out", T)),
+        *(none if k_out is None else _rows(k_out, kv, dim, "k_out", T)),
+        *(none if k_plain is None else _rows(k_plain, kv, dim, "k_plain", T)),
+        *(none if v is None else _rows(v, kv, dim, "v", T)), pool, layer, None if slots is None else slots.data_ptr(),
         _word(status), _stream(stream)), "kvi_norm_rope")
 
 
-def _ring_numbers(t, name: str):
-    if t.dtype is not (_types or _dtypes())[2] or t.numel() != 2 or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous int64 [2]")
-    return t.data_ptr()
+def _batch_fault(R, rows, ctx_lens, new_lens, block_tables, free, free_at, free_at_out, ctx_out, q_start, positions, slots):
+    """Raise for the first tensor that kvi_batch_tables does not take."""
+    _, ints, longs, _ = _types
+    for t, name, kind, n in ((ctx_lens, "ctx_lens", ints, R), (new_lens, "new_lens", ints, R), (ctx_out, "ctx_out", ints, R),
+                             (q_start, "q_start", ints, R + 1), (free, "free", ints, free.numel()),
+                             (free_at, "free_at", longs, 2), (free_at_out, "free_at_out", longs, 2),
+                             (positions, "positions", ints, rows), (slots, "slots", longs, rows)):
+        if t.dtype is not kind or t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous int{32 if kind is ints else 64} [{n}]")
+    raise ValueError(f"block_tables must be contiguous int32 [{R}][max_blocks]")
 
 
 def kvi_batch_tables(ctx_lens, new_lens, block_tables, block_size: int, shared: int, free, free_at, free_at_out, ctx_out,
@@ -830,18 +839,23 @@ def kvi_batch_tables(ctx_lens, new_lens, block_tables, block_size: int, shared: 
     finished), block_tables int32 [R][max_blocks] (new entries written), the ring
     of free blocks `free` int32 [num_blocks] with its running numbers free_at
     int64 [2]; q_start int32 [R + 1], positions int32 and slots int64 [rows]."""
-    R, rows, ints = ctx_lens.shape[0], slots.shape[0], (_types or _dtypes())[1]
-    if block_tables.dim() != 2 or block_tables.shape[0] != R:
-        raise ValueError(f"block_tables must be [{R}][max_blocks]")
-    if positions.dtype is not ints or positions.shape != (rows,) or not positions.is_contiguous() or \
-            slots.dtype is not _types[2] or slots.dim() != 1 or not slots.is_contiguous():
-        raise ValueError("positions must be contiguous int32 [rows], slots int64 [rows]")
-    if free.dtype is not ints or free.dim() != 1 or not free.is_contiguous():
-        raise ValueError("free must be contiguous int32 [num_blocks]")
+    _, ints, longs, _ = _types or _dtypes()
+    R, rows = ctx_lens.numel(), slots.numel()
+    # (ten tensors: looked over at once, as a function's call for each costs more than the launch)
+    if not (ctx_lens.dtype is ints and new_lens.dtype is ints and block_tables.dtype is ints and free.dtype is ints and
+            ctx_out.dtype is ints and q_start.dtype is ints and positions.dtype is ints and slots.dtype is longs and
+            free_at.dtype is longs and free_at_out.dtype is longs and
+            ctx_lens.is_contiguous() and new_lens.is_contiguous() and block_tables.is_contiguous() and
+            free.is_contiguous() and ctx_out.is_contiguous() and q_start.is_contiguous() and
+            positions.is_contiguous() and slots.is_contiguous() and free_at.is_contiguous() and
+            free_at_out.is_contiguous() and
+            new_lens.numel() == R and ctx_out.numel() == R and q_start.numel() == R + 1 and positions.numel() == rows and
+            free_at.numel() == 2 and free_at_out.numel() == 2 and block_tables.dim() == 2 and
+            block_tables.shape[0] == R):
+        _batch_fault(R, rows, ctx_lens, new_lens, block_tables, free, free_at, free_at_out, ctx_out, q_start, positions, slots)
     _check(load_library().kvi_batch_tables(
-        R, _ints(ctx_lens, R, "ctx_lens"), _ints(new_lens, R, "new_lens"), _ints(block_tables, R, "block_tables"),
-        block_tables.shape[1], free.shape[0], block_size, shared, free.data_ptr(), _ring_numbers(free_at, "free_at"),
-        _ring_numbers(free_at_out, "free_at_out"), _ints(ctx_out, R, "ctx_out"), _ints(q_start, R + 1, "q_start"), rows,
+        R, ctx_lens.data_ptr(), new_lens.data_ptr(), block_tables.data_ptr(), block_tables.shape[1], free.numel(), block_size,
+        shared, free.data_ptr(), free_at.data_ptr(), free_at_out.data_ptr(), ctx_out.data_ptr(), q_start.data_ptr(), rows,
         positions.data_ptr(), slots.data_ptr(), _word(status), _stream(stream)), "kvi_batch_tables")
 
 
