@@ -314,18 +314,20 @@ __device__ __forceinline__ float largest64(const float *s)
     return fmaxf(max3(t[0], t[1], t[2]), t[3]);
 }
 
-// Scores of columns from `past` on that are below `low` are not seen
-__device__ __forceinline__ void mask_low_scores(float *s, int past, int low)
+// Scores from column `vis` on are not seen, nor (windows) those from `past` on that
+// are below `low`.  A warp's rows are a few tokens, so few of its quarters of 32
+// columns are seen in part.
+template <int MODE>
+__device__ __forceinline__ void mask_scores(float *s, int vis, int past, int low)
 {
 #pragma unroll
-    for (int c = 0; c < kM; ++c) s[c] = c >= past && c < low ? neg_inf() : s[c];
-}
-
-// Scores from column `vis` on are not seen
-__device__ __forceinline__ void mask_scores(float *s, int vis)
-{
+    for (int q = 0; q < kM; q += 32) {
+        const bool cut = vis < q + 32 || (MODE == kWindow && low > q && past < q + 32);
+        if (!__any_sync(0xffffffffu, cut)) continue;
 #pragma unroll
-    for (int c = 0; c < kM; ++c) s[c] = c < vis ? s[c] : neg_inf();
+        for (int c = q; c < q + 32; ++c)
+            s[c] = c < vis && (MODE != kWindow || c >= low || c < past) ? s[c] : neg_inf();
+    }
 }
 
 // This warp's part of P has reached tensor memory.  (The arrival is lane 0's by a
@@ -729,8 +731,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (in_part || lost) {
                 tmem_wait_ld(s + 64);
                 tmem_wait_ld(s + 96);
-                mask_scores(s, last + 1 - key0);
-                if (MODE == kWindow) mask_low_scores(s, p.sink - key0, last - p.window + 1 - key0);
+                mask_scores<MODE>(s, last + 1 - key0, p.sink - key0, last - p.window + 1 - key0);
                 if (lost) {
                     uint32_t gone[4] = {0, 0, 0, 0};
                     for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
