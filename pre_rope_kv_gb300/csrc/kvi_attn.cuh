@@ -311,6 +311,15 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 }  // namespace
 
+// A batch's own keys need nothing of the kernel before, which is that of its
+// shared prefix and began when all work before it had ended: they begin beside
+// it, and wait for it before they end, so that what follows finds both done.
+template <int MODE>
+__device__ __forceinline__ bool waits_last(const PromptParams &p)
+{
+    return MODE == kShared && !p.flat;
+}
+
 // The rows and keys of request r, or false when its lengths are not usable.
 struct RequestSpan {
     int32_t q0, n_q, ctx;

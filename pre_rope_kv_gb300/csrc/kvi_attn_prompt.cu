@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
     int r = blockIdx.y;
-    pdl_wait();
+    if (!waits_last<MODE>(p)) pdl_wait();
     pdl_launch_dependents();
     RequestSpan rq;
     int part0 = 0;
@@ -94,16 +94,21 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
                                                       p.max_blocks, p.B, p.shared, rq, part0)
                                : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
+        if (waits_last<MODE>(p)) pdl_wait();
         return;
     }
     const int rows = rq.n_q * p.G, row0 = chunk * 8 * NT;
-    if (row0 >= rows) return;
+    if (row0 >= rows) {
+        if (waits_last<MODE>(p)) pdl_wait();
+        return;
+    }
     const int pieces = max(1, ((MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx) + p.span - 1) / p.span);
     if (split >= pieces) {
         if (JOINED && pieces > 1) {  // (the others of the cluster count on it)
             cluster_sync();
             cluster_sync();
         }
+        if (waits_last<MODE>(p)) pdl_wait();
         return;
     }
     const int seen_by_0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
@@ -382,6 +387,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
             if (d == 0) p.ml[part * parts + piece_no] = make_float2(M, L);
         }
     }
+    if (waits_last<MODE>(p)) pdl_wait();
     if (!JOINED || whole) return;
     // ---- each block of the cluster that has keys joins a part of the channels
     cluster_sync();

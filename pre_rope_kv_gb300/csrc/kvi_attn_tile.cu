@@ -379,7 +379,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const uint32_t rest = p.S == 1 ? blockIdx.x : blockIdx.x / (uint32_t)p.S;
     const int split = (int)(blockIdx.x - rest * (uint32_t)p.S);
     const int per = p.per;
-    pdl_wait();
+    const bool flat = MODE == kShared && p.flat;
+    if (!waits_last<MODE>(p)) pdl_wait();
     pdl_launch_dependents();
     // Blocks are for the tile pairs that there are, numbered request after request
     // and from a request's end (its heaviest) to its start; a warp looks over 32
@@ -388,7 +389,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int h = (int)(rest - (uint32_t)item * (uint32_t)p.H);
     RequestSpan rq{0, 0, 0};
     int part0 = 0;
-    const bool flat = MODE == kShared && p.flat;
     if (flat) {
         pair = item;
         r = batch_rows(p, rq);
@@ -424,11 +424,17 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         }
         item -= __shfl_sync(0xffffffffu, sum, 31);
     }
-    if (r < 0) return;
+    if (r < 0) {
+        if (waits_last<MODE>(p)) pdl_wait();
+        return;
+    }
     const int tok0 = pair * 2 * per;  // the block's first token
     const int keys = MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx;  // that its pieces are for
     const bool whole = MODE != kShared && keys <= p.span;            // they are one piece
-    if (split > 0 && (int64_t)split * p.span >= keys) return;
+    if (split > 0 && (int64_t)split * p.span >= keys) {
+        if (waits_last<MODE>(p)) pdl_wait();
+        return;
+    }
     const int seen0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
     // With a window the tiles are those of the first `sink` keys and those from the
@@ -921,6 +927,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
     }
+    if (waits_last<MODE>(p)) pdl_wait();
     fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {
