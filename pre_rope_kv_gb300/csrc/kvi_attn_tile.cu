@@ -14,8 +14,8 @@
 // where its own rounding to bf16 alone leaves 0.0017.
 // The two tiles alternate: while one tile's scores go through the softmax the
 // tensor cores work on the other's products.  Two warps copy, K and V (a box per
-// lane: a piece of a cache page, 64 channels wide), one issues the matrix
-// instructions, four per tile do the softmax.
+// lane: a piece of a cache page, 64 channels wide), one looks over V where it has
+// to be, one issues the matrix instructions, four per tile do the softmax.
 //
 // The running reference m moves only when a score passes it by 2^kLazy (O is
 // rescaled in tensor memory then, which a row needs a few times in all).
@@ -53,7 +53,7 @@ namespace kvi {
 namespace {
 
 constexpr int kM = 128;           // rows of a tile, keys of a tile
-constexpr int kCopyK = 8, kMmaWarp = 9, kCopyV = 10;  // after four softmax warps per tile; one warp idles
+constexpr int kCopyK = 8, kMmaWarp = 9, kCopyV = 10, kLookOver = 11;  // after four softmax warps per tile
 constexpr int kTileThreads = 12 * 32;
 // Registers: the launch gives 168 a thread (65536 / 384); the third warpgroup
 // keeps 72 of them, so that the softmax's hold a row of scores: 2 * 216 + 72 =
@@ -79,6 +79,7 @@ struct TileTail {
     uint64_t drained;
     uint32_t tmem;
     int32_t odd;            // `first` holds something
+    int32_t asked;          // V's tiles that have been asked for
     int32_t lost;           // a key's block lies outside the pool
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
     int32_t newest[3][DP];  // (windows) of the keys up to the block's first row, the last such
@@ -247,7 +248,7 @@ __device__ __forceinline__ void box3_out(const CUtensorMap *map, int x, int y, i
                  : "memory");
 }
 
-// The warp that copies V looks over a tile of it before the products.  An infinity or NaN
+// A warp looks over a tile of V before the products.  An infinity or NaN
 // becomes zero, noted with its key for the rows that see it (a key past the end
 // is seen by none).  The rule is that there is none: one maximum a word.
 // With a window the rows that see a key are those from its position on, if that
@@ -297,6 +298,21 @@ __device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> 
     }
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
+}
+
+// Wait until a count in shared memory has reached `n`.
+__device__ __forceinline__ bool wait_count(uint32_t count, int n, uint64_t limit_ns)
+{
+    uint64_t t0 = 0;
+    for (uint32_t i = 0;; ++i) {
+        int32_t have;
+        asm volatile("ld.acquire.cta.shared.s32 %0, [%1];" : "=r"(have) : "r"(count) : "memory");
+        if (have >= n) return true;
+        if ((i & 31u) != 31u) continue;
+        const uint64_t t = global_ns();
+        if (t0 == 0) t0 = t;
+        if (t - t0 > limit_ns) return false;
+    }
 }
 
 // The largest of 64 scores
@@ -371,6 +387,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         for (int s = 0; s < Sm::kStages / 2; ++s) mbar_init(smem_u32(&tl.v_fixed[s]), 1);
         mbar_init(smem_u32(&tl.drained), 1);
         tl.odd = 0;
+        tl.asked = 0;
         tl.lost = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -545,25 +562,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 box3(smem_u32(base + Sm::kQ) + (lane / Sm::kHalves) * Sm::kTile + (lane % Sm::kHalves) * kHalf, &tm_q,
                      64 * (lane % Sm::kHalves), h * p.G, rq.q0 + tok0 + (lane / Sm::kHalves) * per, bar);
         }
-        // V of the tiles that some row sees in part is looked over before the next
-        // V is asked for (it has been there for a while by then)
-        auto look_over = [&](int j) {
-            if (plane == 0 || !partly(j)) return true;
-            const int slot = 2 * j + 1;  // (V's stages are the odd ones)
-            const bool got = mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
-            if (!__all_sync(0xffffffffu, got)) {
-                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
-                return false;
-            }
-            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, key_of(j), tl, sure - 1, p.sink);
-            if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
-            return true;
-        };
         for (int j = 0; j < n; ++j) {
             look_up(j, block);
             if (j + 1 < n) block = block_of(j + 1);
-            ok = j == 0 || look_over(j - 1);
-            if (!ok) break;
             if (stage >= Sm::kStages) {
                 stage = plane;
                 phase ^= 1u;
@@ -578,8 +579,9 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             copy_tile(plane, stage);
             ++slots;
             stage += 2;
+            if (plane == 1 && lane == 0)
+                asm volatile("st.release.cta.shared.s32 [%0], %1;" ::"r"(smem_u32(&tl.asked)), "r"(slots) : "memory");
         }
-        if (ok && n > 0) ok = look_over(n - 1);
         // no copy may still be writing when the block ends
         if (!ok) {
             constexpr int kOwn = Sm::kStages / 2;
@@ -590,7 +592,26 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (lane == 0 && plane == 0 && n > 0) (void)mbar_wait_brisk(smem_u32(&tl.q_full), 0, kTileWaitNs);
         }
         __syncwarp();
-        if (plane == 1) asm volatile("bar.arrive 1, 288;" ::: "memory");
+    } else if (warp == kLookOver) {
+        // ------------------------------------------- values seen in part
+        // (a warp of its own: the copies run ahead of it)
+        for (int j = 0; j < n; ++j) {
+            if (!partly(j)) continue;
+            // V's copy is on its way (so its barrier is in this copy's phase, and stays there
+            // until the products of this tile have been, which wait for this warp)
+            bool got = wait_count(smem_u32(&tl.asked), j + 1, kTileWaitNs);
+            const int slot = 2 * j + 1;  // (V's stages are the odd ones)
+            got = got && mbar_wait_brisk(smem_u32(&tl.full[slot % Sm::kStages]), (uint32_t)((slot / Sm::kStages) & 1), kTileWaitNs);
+            if (!__all_sync(0xffffffffu, got)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                break;
+            }
+            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, key_of(j), tl, sure - 1, p.sink);
+            if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
+            __syncwarp();
+        }
+        __syncwarp();
+        asm volatile("bar.arrive 1, 288;" ::: "memory");
     } else if (warp == kMmaWarp) {
         // -------------------------------------------------- matrix products
         if (n > 0) {
