@@ -84,6 +84,7 @@ struct TileTail {
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
     int32_t newest[3][DP];  // (windows) of the keys up to the block's first row, the last such
     int32_t part0;          // row of token 0 among the partial results
+    int32_t skip, skip_at;  // (windows) keys left out, and the tile from which on
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -330,6 +331,14 @@ __device__ __forceinline__ float largest64(const float *s)
     return fmaxf(max3(t[0], t[1], t[2]), t[3]);
 }
 
+// The lowest n bits (none below 0, all from 32 on)
+__device__ __forceinline__ uint32_t low_bits(int n)
+{
+    uint32_t m;
+    asm("bmsk.clamp.b32 %0, 0, %1;" : "=r"(m) : "r"(max(n, 0)));
+    return m;
+}
+
 // Scores from column `vis` on are not seen, nor (windows) those from `past` on that
 // are below `low`.  A warp's rows are a few tokens, so few of its quarters of 32
 // columns are seen in part.
@@ -338,11 +347,17 @@ __device__ __forceinline__ void mask_scores(float *s, int vis, int past, int low
 {
 #pragma unroll
     for (int q = 0; q < kM; q += 32) {
-        const bool cut = vis < q + 32 || (MODE == kWindow && low > q && past < q + 32);
-        if (!__any_sync(0xffffffffu, cut)) continue;
+        if (MODE == kWindow) {
+            // (a bit a column: three comparisons each take a tile 1.6 us longer)
+            const uint32_t seen = low_bits(vis - q) & (~low_bits(low - q) | low_bits(past - q));
+            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
 #pragma unroll
-        for (int c = q; c < q + 32; ++c)
-            s[c] = c < vis && (MODE != kWindow || c >= low || c < past) ? s[c] : neg_inf();
+            for (int c = 0; c < 32; ++c) s[q + c] = (seen >> c) & 1u ? s[q + c] : neg_inf();
+            continue;
+        }
+        if (!__any_sync(0xffffffffu, vis < q + 32)) continue;
+#pragma unroll
+        for (int c = q; c < q + 32; ++c) s[c] = c < vis ? s[c] : neg_inf();
     }
 }
 
@@ -478,19 +493,26 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     const int n = max(n_tiles[0], n_tiles[1]);
     const int sure = seen0 + (flat ? 0 : tok0) + 1;  // keys below it are seen by every row
-    // with a window, those from `held` on, too, and the first `sink`
-    const int held = MODE == kWindow ? seen0 + min(rq.n_q, tok0 + 2 * per) - p.window : 0;
-    // whether some row sees a tile's keys in part (0: all tiles from `first_partly` on)
-    const int first_partly = sure > from ? (sure - from) / kM : 0;
-    auto partly = [&](int j) {
-        if (MODE != kWindow) return j >= first_partly;
-        const int key0 = key_of(j);
-        return key0 + kM > sure || (key0 < held && key0 + kM > p.sink);
-    };
+    // Tiles that some row sees in part: all from `first_partly` on; with a window also
+    // those from `low_from` to `low_end`, past the first `sink` keys and before the
+    // first key that every row's window holds.
+    const int first_partly = sure - skip > from ? (sure - skip - from) / kM : 0;
+    int low_from = 0, low_end = 0;
+    if (MODE == kWindow) {
+        const int held = seen0 + min(rq.n_q, tok0 + 2 * per) - p.window;
+        low_from = max(0, p.sink / kM - from / kM);
+        if (low_from >= skip_at && skip > 0) low_from = max(0, skip_at);
+        low_end = held <= 0 ? 0 : max(0, (held - skip - from + kM - 1) / kM);
+    }
+    auto partly = [&](int j) { return j >= first_partly || (MODE == kWindow && j >= low_from && j < low_end); };
     const int32_t *table = p.block_tables + (int64_t)r * p.max_blocks + (MODE == kShared && !flat ? p.shared / p.B : 0);
 
     // (below total_q; here, as r is not kept to the end)
-    if (tid == 0) tl.part0 = MODE == kShared ? part0 : p.by_request ? r * p.max_q : rq.q0;
+    if (tid == 0) {
+        tl.part0 = MODE == kShared ? part0 : p.by_request ? r * p.max_q : rq.q0;
+        tl.skip = skip;
+        tl.skip_at = skip_at;
+    }
 
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
@@ -734,8 +756,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const float lazy = kLazy / p.scale;
         bool ok = true;
         for (int j = 0; j < my; ++j) {
-            const int key0 = key_of(j);
-            const bool in_part = MODE == kWindow ? partly(j) : key0 + kM > sure;
+            const bool in_part = partly(j);
             ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
             if (!__all_sync(0xffffffffu, ok)) {
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
@@ -758,6 +779,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (in_part || lost) {
                 tmem_wait_ld(s + 64);
                 tmem_wait_ld(s + 96);
+                const int key0 = from + j * kM + (MODE == kWindow && j >= tl.skip_at ? tl.skip : 0);
                 mask_scores<MODE>(s, last + 1 - key0, p.sink - key0, last - p.window + 1 - key0);
                 if (lost) {
                     uint32_t gone[4] = {0, 0, 0, 0};
