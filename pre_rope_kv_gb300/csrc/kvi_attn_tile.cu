@@ -263,15 +263,19 @@ __device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> 
     constexpr int kChunks = TileSmem<DP>::kTile / 16;
     const int lane = threadIdx.x & 31;
     const uint4 *at = reinterpret_cast<const uint4 *>(v);
-    __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);
-#pragma unroll 4
+    // (four maxima, as each waits for the one before it)
+    __nv_bfloat162 tops[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) tops[j] = __floats2bfloat162_rn(0.f, 0.f);
+#pragma unroll 8
     for (int i = lane; i < kChunks; i += 32) {
         const uint4 x = at[i];
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j])));
+        for (int j = 0; j < 4; ++j) tops[j] = __hmax2_nan(tops[j], __habs2(*reinterpret_cast<const __nv_bfloat162 *>(&w[j])));
     }
-    const uint32_t bits = *reinterpret_cast<const uint32_t *>(&top);
+    tops[0] = __hmax2_nan(__hmax2_nan(tops[0], tops[1]), __hmax2_nan(tops[2], tops[3]));
+    const uint32_t bits = *reinterpret_cast<const uint32_t *>(&tops[0]);
     const bool odd = (bits & 0x7f80u) == 0x7f80u || (bits & 0x7f800000u) == 0x7f800000u;
     if (!__any_sync(0xffffffffu, odd)) return;
     if (!tl.odd)
