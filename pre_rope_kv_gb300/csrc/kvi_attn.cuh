@@ -88,7 +88,7 @@ struct PromptParams {
     int32_t joined;             // (rows) a chunk's pieces are a cluster, which joins them
     // (kWindow) the keys that a row sees, and how many of them a row's pieces cover at most
     int32_t window, sink, cap;
-    // (kShared) a batch whose requests share their first keys.  flat: those keys, of all
+    // A batch whose requests share their first keys.  (kShared) flat: those keys, of all
     // rows as one request's; else each request's other keys.  Pieces from `first` on
     // of `parts` of a row.
     int32_t shared, flat, first, parts;
@@ -336,6 +336,12 @@ __device__ __forceinline__ bool request_span(int r, const int32_t *q_start, int 
            (int64_t)o.ctx <= (int64_t)max_blocks * block_size;
 }
 
+// Whether a request's rows see all of a prefix that they share (0: none).
+__device__ __forceinline__ bool sees_prefix(const RequestSpan &o, int shared)
+{
+    return shared == 0 || o.n_q == 0 || o.ctx - o.n_q >= shared;
+}
+
 // The rows and keys of request r in a batch with a shared prefix: its keys past
 // the prefix, and only rows among those the batch's partial results are for.
 __device__ __forceinline__ bool request_past_prefix(int r, const int32_t *q_start, int R, int total_q, int max_q,
@@ -346,7 +352,7 @@ __device__ __forceinline__ bool request_past_prefix(int r, const int32_t *q_star
     bool good = request_span(r, q_start, total_q, max_q, ctx_lens, max_ctx, max_blocks, block_size, o);
     part0 = o.q0 - b0;
     good = good && b0 >= 0 && part0 >= 0 && o.q0 + o.n_q <= b1 && (int64_t)b1 - b0 <= (int64_t)R * max_q;
-    if (good && o.n_q > 0 && o.ctx - o.n_q < shared) good = false;
+    good = good && sees_prefix(o, shared);
     o.ctx = max(0, o.ctx - shared);
     return good;
 }
@@ -382,7 +388,8 @@ __device__ __forceinline__ void join_rows(const JoinParams &p, int x, int r)
         if (!request_past_prefix(r, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size,
                                  p.shared, q, part0))
             return;
-    } else if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q)) {
+    } else if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q) ||
+               !sees_prefix(q, p.shared)) {
         return;
     }
     const int pieces = p.first + (min(q.ctx, p.cap) + p.span - 1) / p.span;

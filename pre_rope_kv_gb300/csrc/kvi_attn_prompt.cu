@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         r = batch_rows(p, rq);
     } else if (MODE == kShared ? !request_past_prefix(r, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
                                                       p.max_blocks, p.B, p.shared, rq, part0)
-                               : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq)) {
+                               : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq) ||
+                                     !sees_prefix(rq, p.shared)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         if (waits_last<MODE>(p)) pdl_wait();
         return;
@@ -544,8 +545,9 @@ size_t prompt_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t 
 size_t shared_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t max_q, int32_t max_ctx, int32_t shared)
 {
     const int64_t tokens = part_rows(R, total_q, max_q), rows = tokens * a.q_heads;
-    return part_bytes(a, std::max(rows, most_parts(a, 1, tokens, (int32_t)tokens, shared)) +
-                             std::max(rows, most_parts(a, R, tokens, max_q, max_ctx)));
+    return std::max(prompt_bytes(a, R, total_q, max_q, max_ctx),
+                    part_bytes(a, std::max(rows, most_parts(a, 1, tokens, (int32_t)tokens, shared)) +
+                                      std::max(rows, most_parts(a, R, tokens, max_q, max_ctx))));
 }
 
 template <int DP, int NT, bool JOINED, int MODE>
@@ -727,7 +729,7 @@ int32_t window_cap(int32_t window, int32_t sink, int unit, int tokens)
     return (int32_t)std::min<int64_t>(cap, 0x7fffffff);
 }
 
-kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t sink)
+kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t sink, int32_t shared)
 {
     const kvi_attention &a = *c.a;
     // The tiles' windows are no shorter than a block's rows, which check_values
@@ -751,11 +753,26 @@ kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t
     p.window = window;
     p.sink = sink;
     p.cap = cap;
+    p.shared = shared;
     st = cuda_status(launch_form(p, pl, c.R, mode, c.stream), c.name);
     if (st != KVI_OK || pl.S == 1 || pl.joined) return st;
     JoinParams j = join_of(c, p);
     j.cap = cap;
+    j.shared = shared;
     return cuda_status(launch_join(j, c.stream), c.name);
+}
+
+// Whether the prefix is worth kernels of its own.  Not where a request's rows fill
+// a block's two tiles by themselves, and so read it as often one way as the other
+// (us, with and without; 8 KV heads of 4 heads of 128 channels, prefix 10240: 24
+// requests x 37 tokens 67, 193; 8 x 37 58, 67; 4 x 64 51, 43; 16 x 128 274, 226),
+// nor below 32 MB less to read, which cost what a launch and a join do (single
+// tokens: 8 requests x 256 keys 12.0, 7.4; 4 x 1600, 20 MB, 13.3, 10.9; 16 x 512, 31
+// MB, 14.4, 17.7; 2 x 10240, 42 MB, 19.1, 18.1; 64 x 256, 66 MB, 22.8, 25.8).
+bool shares(const kvi_attention &a, int32_t R, int64_t tokens, int32_t shared)
+{
+    const int64_t less = ((int64_t)R - 1) * shared * a.kv_heads * a.head_dim * 4;
+    return tokens * (a.q_heads / a.kv_heads) < 256 * (int64_t)R && less >= (32 << 20);
 }
 
 kvi_status attend_shared(const PromptCall &c, int32_t shared)
@@ -809,7 +826,7 @@ extern "C" kvi_status kvi_attn_prompt(const kvi_attention *a, int32_t R, const v
                        d_block_tables, max_blocks, cache, layer, d_out, out_row_stride, d_lse, d_ws, ws_bytes, d_status,
                        stream};
     const kvi_status st = check_prompt(c);
-    return st != KVI_OK ? st : attend_prompts(c, kCausal, 0, 0);
+    return st != KVI_OK ? st : attend_prompts(c, kCausal, 0, 0, 0);
 }
 
 extern "C" kvi_status kvi_attn_window(const kvi_attention *a, int32_t R, const void *d_q, int64_t q_row_stride,
@@ -825,9 +842,9 @@ extern "C" kvi_status kvi_attn_window(const kvi_attention *a, int32_t R, const v
     const kvi_status st = check_prompt(c);
     if (st != KVI_OK) return st;
     if (window < 1 || sink < 0) return arg_error("window=%d must be >= 1 and sink=%d >= 0", window, sink);
-    if (window >= max_ctx || sink >= max_ctx) return attend_prompts(c, kCausal, 0, 0);  // every row sees all before it
+    if (window >= max_ctx || sink >= max_ctx) return attend_prompts(c, kCausal, 0, 0, 0);  // every row sees all before it
     if (window > (1 << 30)) return arg_error("window=%d is above 2^30", window);
-    return attend_prompts(c, kWindow, window, sink);
+    return attend_prompts(c, kWindow, window, sink, 0);
 }
 
 extern "C" size_t kvi_attn_shared_workspace_bytes(const kvi_attention *a, int32_t R, int32_t total_q, int32_t max_q,
@@ -853,5 +870,6 @@ extern "C" kvi_status kvi_attn_shared(const kvi_attention *a, int32_t R, const v
         (shared && shared >= max_ctx))
         return arg_error("shared=%d must be whole blocks of %d, fewer keys than max_ctx=%d and in the block tables", shared,
                          cache->block_size, max_ctx);
-    return shared == 0 ? attend_prompts(c, kCausal, 0, 0) : attend_shared(c, shared);
+    const int64_t tokens = part_rows(R, total_q, max_q);
+    return shared > 0 && shares(*a, R, tokens, shared) ? attend_shared(c, shared) : attend_prompts(c, kCausal, 0, 0, shared);
 }

@@ -42,6 +42,7 @@ LAYOUTS = [(1, 1, 16, 1), (4, 2, 64, 16), (8, 2, 128, 16), (32, 8, 128, 16), (10
            (128, 1, 128, 16), (2, 2, 112, 64)]
 
 
+# (prefixes below some 32 MB less to read are attended with each request's other keys; test_many below has larger ones)
 @pytest.mark.parametrize("blocks", [1, 7, 40])
 @pytest.mark.parametrize("Hq,H,D,B", LAYOUTS)
 def test_layouts(Hq, H, D, B, blocks):
@@ -64,17 +65,34 @@ def test_lengths(Hq, H, D, B, shared, n_q, ctx):
     assert torch.equal(c.out, first)
 
 
+@pytest.mark.parametrize("more", [0, 3])
+@pytest.mark.parametrize("Hq,H,D,B", LAYOUTS)
+def test_many(Hq, H, D, B, more):
+    """Enough requests that the prefix is read by itself: single tokens, and a few questions among them."""
+    R = 90 if H * D > 64 else 200
+    n_q = [1 if i % 7 else 0 for i in range(R)]
+    n_q[5:5 + more] = [9, 4, 13][:more]
+    blocks = -(-(9 << 20) // ((R - 1) * H * D) // B) + 1
+    c = Case(Hq, H, D, B, n_q, [n + (37 * i) % 150 for i, n in enumerate(n_q)], blocks * B, seed=Hq * D + B)
+    c.run()
+    c.check()
+    first = c.out.clone()
+    c.run()
+    assert torch.equal(c.out, first)
+
+
 def test_strided_rows_without_lse():
-    c = Case(8, 2, 128, 16, [9, 1, 40], [39, 5, 70], 640, seed=5, wide=4, lse=False)
+    c = Case(8, 2, 128, 16, [9, 1, 40] * 4, [39, 5, 70] * 4, 4096, seed=5, wide=4, lse=False)
     c.run()
     c.check()
     assert bool((c.out._base[:, :4] == 7).all()), "written outside the rows"
 
 
+@pytest.mark.parametrize("shared", [800, 16000])
 @pytest.mark.parametrize("n_q", [[1, 1, 1], [30, 2, 5]])
-def test_rows_of_a_larger_buffer(n_q):
+def test_rows_of_a_larger_buffer(n_q, shared):
     """The batch's rows begin and end inside q; the others are left as they are."""
-    c = Case(8, 2, 128, 16, n_q, [n + 50 for n in n_q], 800, seed=6)
+    c = Case(8, 2, 128, 16, n_q, [n + 50 for n in n_q], shared, seed=6)
     c.run()
     want, total = c.out.clone(), sum(n_q)
     q = torch.full((total + 200, 8, 128), math.nan, dtype=torch.bfloat16, device=DEV)
@@ -88,8 +106,9 @@ def test_rows_of_a_larger_buffer(n_q):
     assert bool((c.lse[:90] == 7).all()) and bool((c.lse[90 + total:] == 7).all())
 
 
-def test_large_scores_and_late_maximum():
-    c = Case(4, 1, 64, 16, [3, 1, 20], [100, 1, 30], 1008, seed=8, poison=False)
+@pytest.mark.parametrize("shared", [1008, 70000])
+def test_large_scores_and_late_maximum(shared):
+    c = Case(4, 1, 64, 16, [3, 1, 20], [100, 1, 30], shared, seed=8, poison=False)
     grow = torch.linspace(0, 1, c.pool.shape[1] * c.B, device=DEV).view(1, -1, 1, 1)
     c.q = c.q * 0.1
     c.q[..., 0] = 8
@@ -98,8 +117,9 @@ def test_large_scores_and_late_maximum():
     c.check()
 
 
-def test_values_past_the_prefix_and_past_a_row_have_no_effect():
-    c = Case(4, 1, 128, 16, [6, 1], [26, 4], 208, seed=7)
+@pytest.mark.parametrize("shared", [208, 70000])
+def test_values_past_the_prefix_and_past_a_row_have_no_effect(shared):
+    c = Case(4, 1, 128, 16, [6, 1], [26, 4], shared, seed=7)
     c.run()
     clean = c.out.clone()
     p = c.ctx[0] - 6 + 3  # the position of row 3
@@ -116,11 +136,12 @@ def test_values_past_the_prefix_and_past_a_row_have_no_effect():
         flat[slot] = keep
 
 
+@pytest.mark.parametrize("shared", [304, 24000])
 @pytest.mark.parametrize("n_q", [[2, 3], [40, 60]])
-def test_bad_requests_are_skipped(n_q):
+def test_bad_requests_are_skipped(n_q, shared):
     """Keys that are fewer than the prefix, too many, rows outside q; a block of the prefix and of a request."""
     def case():
-        return Case(4, 2, 128, 16, n_q + [1], [n + 40 for n in n_q] + [20], 304, seed=9)
+        return Case(4, 2, 128, 16, n_q + [1], [n + 40 for n in n_q] + [20], shared, seed=9)
 
     good = case()
     good.run()
@@ -128,13 +149,13 @@ def test_bad_requests_are_skipped(n_q):
     for what in ("few", "many", "rows", "own block", "shared block"):
         c = case()
         if what == "few":
-            c.ctx_lens[1] = 304 + n_q[1] - 1
+            c.ctx_lens[1] = shared + n_q[1] - 1
         elif what == "many":
             c.ctx_lens[1] = c.max_ctx + 1
         elif what == "rows":
             c.q_start[2] = c.q.shape[0] + 5
         elif what == "own block":
-            c.table[1, 20] = c.pool.shape[1]
+            c.table[1, shared // 16 + 1] = c.pool.shape[1]
         else:
             c.table[:, 3] = -1
         c.run()
@@ -153,14 +174,15 @@ def test_bad_requests_are_skipped(n_q):
             assert torch.equal(c.out[:a], good.out[:a]) and bool((c.out[a:b] == 7).all())
 
 
-def test_starts_that_are_no_starts():
-    """Row starts out of order or outside q: recorded, nothing written."""
+@pytest.mark.parametrize("shared", [304, 32000])
+def test_starts_that_are_no_starts(shared):
+    """Row starts out of order or outside q: recorded, nothing written past them."""
     for starts in ([3, 1, 2, 0], [-4, 0, 1, 3], [0, 1, 2, 900], [900, 900, 900, 900]):
-        c = Case(4, 2, 128, 16, [1, 1, 1], [9, 10, 11], 304, seed=9)
+        c = Case(4, 2, 128, 16, [1, 1, 1], [9, 10, 11], shared, seed=9)
         c.q_start = torch.tensor(starts, dtype=torch.int32, device=DEV)
         c.run()
         assert int(c.status) == kvi.ERR_OUT_OF_RANGE
-        assert bool((c.out == 7).all())
+        assert bool((c.out == 7).all()) or shared == 304  # (a request with a good start and end is attended there)
 
 
 def test_no_prefix_is_the_plain_call():
@@ -173,17 +195,17 @@ def test_no_prefix_is_the_plain_call():
 
 
 def test_other_stream_and_graph():
-    c = Case(8, 2, 128, 16, [5, 0, 1, 20], [70, 0, 33, 20], 1600, seed=10)
+    c = Case(8, 2, 128, 16, [5, 0, 1, 20], [70, 0, 33, 20], 16000, seed=10)
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(s):
         c.run()
     s.synchronize()
     c.check()
-    ws = ac.workspace(kvi.kvi_attn_shared_workspace_bytes(c.a, 4, 26, 20, c.max_ctx, 1600))
+    ws = ac.workspace(kvi.kvi_attn_shared_workspace_bytes(c.a, 4, 26, 20, c.max_ctx, 16000))
     cache, g = kvi.paged_cache([c.pool], 16), torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        kvi.kvi_attn_shared(c.a, c.q, c.q_start, 20, c.ctx_lens, c.max_ctx, c.table, cache, 0, 1600, c.out, ws, c.status, lse=c.lse)
+        kvi.kvi_attn_shared(c.a, c.q, c.q_start, 20, c.ctx_lens, c.max_ctx, c.table, cache, 0, 16000, c.out, ws, c.status, lse=c.lse)
     for seed in (1, 2):
         c.q.copy_(ac.randn(ac.gen(seed), *c.q.shape).to(torch.bfloat16))
         g.replay()
@@ -201,7 +223,7 @@ def test_offsets_past_32_bits():
     blocks = (1 << 31) // (B * H * D) + 64
     if torch.cuda.mem_get_info()[0] < 2 * blocks * B * H * D * 2 + (4 << 30):
         pytest.skip("not enough device memory")
-    c = Case(8, 8, D, B, [3, 1], [50, 20], 320, seed=11, poison=False)
+    c = Case(8, 8, D, B, [3, 1, 1], [50, 20, 30], 4800, seed=11, poison=False)
     pool = torch.empty(2, blocks, B, H, D, dtype=torch.bfloat16, device=DEV)
     small, table = c.pool, c.table.clone()
     used = table[table >= 0].long()
