@@ -90,8 +90,9 @@ struct PromptParams {
     int32_t window, sink, cap;
     // A batch whose requests share their first keys.  (kShared) flat: those keys, of all
     // rows as one request's; else each request's other keys.  Pieces from `first` on
-    // of `parts` of a row.
-    int32_t shared, flat, first, parts;
+    // of `parts` of a row.  merges: these keys are one piece, whose block joins the prefix's
+    // pieces to it.
+    int32_t shared, flat, first, parts, merges;
     // Partial results of row i of request r: at its place in q, or, where q has
     // more rows than R * max_q, at r * max_q + i; so they take no more of the
     // workspace than there can be rows that are split.

@@ -81,6 +81,17 @@ def test_many(Hq, H, D, B, more):
     assert torch.equal(c.out, first)
 
 
+@pytest.mark.parametrize("Hq,H,D,B", [(6, 1, 256, 8), (3, 1, 80, 5), (40, 2, 32, 16), (10, 2, 96, 24), (4, 1, 128, 16)])
+def test_a_wave_of_requests(Hq, H, D, B):
+    """So many that each block joins the prefix's pieces to its request's keys."""
+    R = 420
+    n_q = [1 if i % 11 else 0 for i in range(R)]
+    blocks = -(-(9 << 20) // ((R - 1) * H * D) // B) + 1
+    c = Case(Hq, H, D, B, n_q, [n + (29 * i) % 90 for i, n in enumerate(n_q)], blocks * B, seed=D + B)
+    c.run()
+    c.check()
+
+
 def test_strided_rows_without_lse():
     c = Case(8, 2, 128, 16, [9, 1, 40] * 4, [39, 5, 70] * 4, 4096, seed=5, wide=4, lse=False)
     c.run()
