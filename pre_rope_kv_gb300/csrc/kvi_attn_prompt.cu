@@ -24,7 +24,12 @@ namespace kvi {
 
 namespace {
 
-constexpr int kRowWarps = 4;
+// Warps of a block.  Three where a window's keys are long beside what a block takes
+// to begin and end, so that four blocks fit an SM (64 windows of 1024 keys, 128
+// channels, 54 us instead of 58.5, of 4096 keys 170 instead of 182, of 256 keys 26
+// instead of 25; whole prefixes and their rests are as they were measured with four).
+template <int DP, int MODE>
+constexpr int kRowWarps = MODE == kWindow && DP == 128 ? 3 : 4;
 constexpr int kRowStages = 2;  // (three blocks fit an SM; with 3: two blocks, 64 x 1.5 k keys 78 us instead of 71)
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -59,14 +64,14 @@ __device__ __forceinline__ uint32_t not_finite(uint32_t w)  // bits 15 / 31: tha
 
 // Shared memory of a block: the warps' rings (rows padded by 16 bytes, so that
 // the 8 rows of a matrix load fall into different banks), reused for the join.
-template <int DP, int NT>
+template <int DP, int NT, int WARPS = 4>
 struct RowsSmem {
     static constexpr int kPitch = DP * 2 + 16;
     static constexpr int kStage = 2 * 16 * kPitch;  // K then V of 16 keys
     static constexpr int kRing = kRowStages * kStage;
-    static constexpr int kSum = kRowWarps * 8 * NT * (DP + 4) * 4;  // then the block's own
+    static constexpr int kSum = WARPS * 8 * NT * (DP + 4) * 4;  // then the block's own
     static constexpr int kJoin = kSum + 8 * NT * DP * 4;
-    static constexpr int kBytes = kRowWarps * kRing > kJoin ? kRowWarps * kRing : kJoin;
+    static constexpr int kBytes = WARPS * kRing > kJoin ? WARPS * kRing : kJoin;
 };
 
 // The prefix's pieces of a row joined to (M, L, acc), of channels d and d + 1.
@@ -98,13 +103,14 @@ __device__ __forceinline__ void join_prefix(const PromptParams &p, int64_t row, 
 // DP: the head size rounded up to 32, 64, 128 or 256 (the rest reads as zero);
 // 8 * NT rows per block.  JOINED: a chunk's pieces are a cluster, which joins them.
 template <int DP, int NT, bool JOINED, int MODE>
-__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ PromptParams p)
+__global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __grid_constant__ PromptParams p)
 {
-    using Sm = RowsSmem<DP, NT>;
+    constexpr int kWarps = kRowWarps<DP, MODE>;
+    using Sm = RowsSmem<DP, NT, kWarps>;
     constexpr int KS = DP / 16, CH = DP / 8;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint32_t s_here[kRowWarps][kRowStages];
-    __shared__ float s_m[kRowWarps][8 * NT], s_l[kRowWarps][8 * NT];
+    __shared__ uint32_t s_here[kWarps][kRowStages];
+    __shared__ float s_m[kWarps][8 * NT], s_l[kWarps][8 * NT];
     __shared__ float2 s_ml[8 * NT];  // of the block
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
@@ -200,7 +206,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         l[nt][0] = l[nt][1] = 0.f;
     }
 
-    // ---- this warp's tiles: from / 16 + warp, + kRowWarps, ...
+    // ---- this warp's tiles: from / 16 + warp, + kWarps, ...
     uint8_t *ring = smem + warp * Sm::kRing;
     if (p.D < DP) {  // channels past D: copied never, zero for good
         for (int i = lane; i < kRowStages * 32; i += 32)
@@ -242,13 +248,13 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 #pragma unroll
-    for (int s = 0; s < kRowStages - 1; ++s) issue(t0 + s * kRowWarps, s, block_of(t0 + s * kRowWarps));
-    int next_block = block_of(t0 + (kRowStages - 1) * kRowWarps);
+    for (int s = 0; s < kRowStages - 1; ++s) issue(t0 + s * kWarps, s, block_of(t0 + s * kWarps));
+    int next_block = block_of(t0 + (kRowStages - 1) * kWarps);
     int stage = 0;
-    for (int tile = t0; tile < t1; tile += kRowWarps) {
-        const int ahead = tile + (kRowStages - 1) * kRowWarps;
+    for (int tile = t0; tile < t1; tile += kWarps) {
+        const int ahead = tile + (kRowStages - 1) * kWarps;
         issue(ahead, stage == 0 ? kRowStages - 1 : stage - 1, next_block);
-        next_block = block_of(ahead + kRowWarps);
+        next_block = block_of(ahead + kWarps);
         asm volatile("cp.async.wait_group %0;" ::"n"(kRowStages - 1) : "memory");
         __syncwarp();
         const uint32_t ka = ring_a + stage * Sm::kStage, va = ka + 16 * Sm::kPitch;
@@ -380,17 +386,17 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     const bool merges = MODE == kShared && !flat && p.merges;
     if (merges) pdl_wait();
     const int half = p.D / 2;
-    for (int i = tid; i < 8 * NT * half; i += kRowWarps * 32) {
+    for (int i = tid; i < 8 * NT * half; i += kWarps * 32) {
         const int n = i / half, d = (i % half) * 2, row = row0 + n;
         if (row >= rows) break;
         float M = neg_inf();
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, s_m[w][n]);
+        for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][n]);
         const float ref = M == neg_inf() ? 0.f : M;
         float L = 0.f;
         float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
             const float f = exp2_fast(s_m[w][n] - ref);
             const float *src = s_o + (w * 8 * NT + n) * kO + d;
             L += s_l[w][n] * f;
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_const
     if (!JOINED || whole) return;
     // ---- each block of the cluster that has keys joins a part of the channels
     cluster_sync();
-    for (int i = split * kRowWarps * 32 + tid; i < 8 * NT * half; i += pieces * kRowWarps * 32) {
+    for (int i = split * kWarps * 32 + tid; i < 8 * NT * half; i += pieces * kWarps * 32) {
         const int n = i / half, d = (i % half) * 2, row = row0 + n;
         if (row >= rows) break;
         float2 ml[kMostJoined], part[kMostJoined];
@@ -582,11 +588,11 @@ size_t shared_bytes(const kvi_attention &a, int32_t R, int32_t total_q, int32_t 
 template <int DP, int NT, bool JOINED, int MODE>
 cudaError_t run_rows_as(const PromptParams &p, int32_t R, cudaStream_t s)
 {
-    const int bytes = RowsSmem<DP, NT>::kBytes;
+    const int bytes = RowsSmem<DP, NT, kRowWarps<DP, MODE>>::kBytes;
     const cudaError_t e = smem_opt_in(rows_kernel<DP, NT, JOINED, MODE>, bytes);
     if (e != cudaSuccess) return e;
     return launch_chained_clusters(rows_kernel<DP, NT, JOINED, MODE>, JOINED ? p.S : 1,
-                                   dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps * 32, bytes, s, p);
+                                   dim3((unsigned)(p.S * p.chunks * p.H), (unsigned)R), kRowWarps<DP, MODE> * 32, bytes, s, p);
 }
 
 template <int DP, int NT, int MODE>
