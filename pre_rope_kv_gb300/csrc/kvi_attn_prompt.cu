@@ -778,7 +778,19 @@ kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t
         pl = plan_tiles(a, c.R, c.total_q, c.max_q, std::min(c.max_ctx, cap));
     } else {
         if (mode == kWindow) cap = window_cap(window, sink, 16, 16);
-        pl = plan_rows(a, c.R, c.total_q, c.max_q, std::min(c.max_ctx, cap));
+        const int32_t keys = std::min(c.max_ctx, cap);
+        pl = plan_rows(a, c.R, c.total_q, c.max_q, keys);
+        // Windows are of one length, so that blocks that find room at once end together:
+        // one piece each where they are many, or the keys few (us, in pieces and in one,
+        // 8 KV heads of 128 channels: 24 users x 1024 keys 24.9, 30.0; 40 x 1024 45.0, 35.9;
+        // 64 x 1024 54.3, 50.1, x 256 26.1, 17.2; 16 x 256 13.0, 11.0; 8 x 256 9.0, 10.7).
+        const int64_t n = (int64_t)c.R * a.kv_heads * pl.chunks;
+        if (mode == kWindow && (n >= 250 || (n >= 96 && keys <= 384))) {
+            pl.S = 1;
+            pl.span = kLongest;
+            pl.joined = false;
+            pl.ml = pl.total = 0;
+        }
     }
     kvi_status st = check_room(c, pl.chunks * pl.S * a.kv_heads, (int64_t)c.max_q * (a.q_heads / a.kv_heads),
                                std::max<size_t>(256, pl.total));
