@@ -783,9 +783,9 @@ kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t
         // Windows are of one length, so that blocks that find room at once end together:
         // one piece each where they are many, or the keys few (us, in pieces and in one,
         // 8 KV heads of 128 channels: 24 users x 1024 keys 24.9, 30.0; 40 x 1024 45.0, 35.9;
-        // 64 x 1024 54.3, 50.1, x 256 26.1, 17.2; 16 x 256 13.0, 11.0; 8 x 256 9.0, 10.7).
+        // 64 x 1024 54.3, 50.1, x 256 26.1, 17.2, x 4096 170, 177; 16 x 256 13.0, 11.0; 8 x 256 9.0, 10.7).
         const int64_t n = (int64_t)c.R * a.kv_heads * pl.chunks;
-        if (mode == kWindow && (n >= 250 || (n >= 96 && keys <= 384))) {
+        if (mode == kWindow && ((n >= 250 && keys <= 2560) || (n >= 96 && keys <= 384))) {
             pl.S = 1;
             pl.span = kLongest;
             pl.joined = false;
