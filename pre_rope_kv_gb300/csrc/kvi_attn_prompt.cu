@@ -74,32 +74,6 @@ struct RowsSmem {
     static constexpr int kBytes = WARPS * kRing > kJoin ? WARPS * kRing : kJoin;
 };
 
-// The prefix's pieces of a row joined to (M, L, acc), of channels d and d + 1.
-__device__ __forceinline__ void join_prefix(const PromptParams &p, int64_t row, int d, float &M, float &L, float2 &acc)
-{
-    const float2 *ml = p.ml + row * p.parts;
-    const float *po = p.po + row * p.parts * p.D + d;
-    float top = M;
-#pragma unroll 8
-    for (int s = 0; s < p.first; ++s) top = fmaxf(top, ml[s].x);
-    const float ref = top == neg_inf() ? 0.f : top;
-    const float f = exp2_fast(M - ref);
-    L *= f;
-    acc.x *= f;
-    acc.y *= f;
-#pragma unroll 8
-    for (int s = 0; s < p.first; ++s) {
-        const float2 piece = ml[s], o = *reinterpret_cast<const float2 *>(po + (int64_t)s * p.D);
-        const float g = exp2_fast(piece.x - ref);
-        L += piece.y * g;
-        if (g != 0.f) {  // (a piece without a visible key: its output may be anything)
-            acc.x += o.x * g;
-            acc.y += o.y * g;
-        }
-    }
-    M = top;
-}
-
 // DP: the head size rounded up to 32, 64, 128 or 256 (the rest reads as zero);
 // 8 * NT rows per block.  JOINED: a chunk's pieces are a cluster, which joins them.
 template <int DP, int NT, bool JOINED, int MODE>
@@ -383,8 +357,74 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             }
         }
     __syncthreads();
-    const bool merges = MODE == kShared && !flat && p.merges;
-    if (merges) pdl_wait();
+    if (MODE == kShared && !flat && p.merges) {
+        // ---- all of a row's keys past the prefix are here: its pieces are joined to them,
+        // a row a warp, four channels a lane, eight pieces asked for before the sums
+        pdl_wait();
+        for (int n = warp; n < 8 * NT && row0 + n < rows; n += kWarps) {
+            const int head = h * p.G + (row0 + n) % p.G, token = (row0 + n) / p.G;
+            const int64_t part = (int64_t)(part0 + token) * p.Hq + head, at = (int64_t)(rq.q0 + token) * p.Hq + head;
+            const float2 *ml = p.ml + part * p.parts;
+            const float *po = p.po + part * p.parts * p.D;
+            constexpr int kAhead = 8;
+            float4 v[kAhead];
+#pragma unroll
+            for (int s = 0; s < kAhead; ++s)
+                if (s < p.first && 4 * lane < p.D) v[s] = *reinterpret_cast<const float4 *>(po + s * p.D + 4 * lane);
+            const float2 mine = lane < p.first ? ml[lane] : make_float2(neg_inf(), 0.f);  // of piece `lane`
+            float M = mine.x;
+            for (int s = lane + 32; s < p.first; s += 32) M = fmaxf(M, ml[s].x);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][n]);
+            const float ref = M == neg_inf() ? 0.f : M, f0 = exp2_fast(mine.x - ref);
+            float L = mine.y * f0, own[kWarps];
+            for (int s = lane + 32; s < p.first; s += 32) L += ml[s].y * exp2_fast(ml[s].x - ref);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                own[w] = exp2_fast(s_m[w][n] - ref);
+                L += s_l[w][n] * own[w];
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            for (int d = 4 * lane; d - 4 * lane < p.D; d += 128) {
+                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                auto add = [&](const float4 &x, float f) {
+                    acc.x = fmaf(f, x.x, acc.x);
+                    acc.y = fmaf(f, x.y, acc.y);
+                    acc.z = fmaf(f, x.z, acc.z);
+                    acc.w = fmaf(f, x.w, acc.w);
+                };
+                if (d < p.D) {
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w)
+                        add(*reinterpret_cast<const float4 *>(s_o + (w * 8 * NT + n) * kO + d), own[w]);
+                }
+                for (int b = 0; b < p.first; b += kAhead) {
+                    if (b > 0 || d >= 128) {
+#pragma unroll
+                        for (int s = 0; s < kAhead; ++s)
+                            if (b + s < p.first && d < p.D)
+                                v[s] = *reinterpret_cast<const float4 *>(po + (int64_t)(b + s) * p.D + d);
+                    }
+#pragma unroll
+                    for (int s = 0; s < kAhead; ++s) {
+                        float f = __shfl_sync(0xffffffffu, f0, (b + s) & 31);
+                        if (b + s >= 32) f = b + s < p.first ? exp2_fast(ml[b + s].x - ref) : 0.f;
+                        // (a piece without a visible key adds nothing: its output may be anything)
+                        if (b + s < p.first && d < p.D && f != 0.f) add(v[s], f);
+                    }
+                }
+                if (d < p.D)
+                    *reinterpret_cast<uint2 *>(p.out + (int64_t)(rq.q0 + token) * p.out_stride + (int64_t)head * p.D + d) =
+                        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+            }
+            if (p.lse && lane == 0) p.lse[at] = L == 0.f ? neg_inf() : (M + log2f(L)) * kLn2;
+        }
+        return;
+    }
     const int half = p.D / 2;
     for (int i = tid; i < 8 * NT * half; i += kWarps * 32) {
         const int n = i / half, d = (i % half) * 2, row = row0 + n;
@@ -406,8 +446,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
         const int64_t token = rq.q0 + row / p.G;
         const int head = h * p.G + row % p.G;
         const int64_t at = token * p.Hq + head;
-        if (merges) join_prefix(p, (int64_t)(part0 + row / p.G) * p.Hq + head, d, M, L, acc);
-        if (whole || merges) {
+        if (whole) {
             const float inv = L == 0.f ? 0.f : 1.f / L;
             *reinterpret_cast<uint32_t *>(p.out + token * p.out_stride + (int64_t)head * p.D + d) =
                 pack_bf16(acc.x * inv, acc.y * inv);
@@ -423,7 +462,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             if (d == 0) p.ml[part * parts + piece_no] = make_float2(M, L);
         }
     }
-    if (waits_last<MODE>(p) && !merges) pdl_wait();
+    if (waits_last<MODE>(p)) pdl_wait();
     if (!JOINED || whole) return;
     // ---- each block of the cluster that has keys joins a part of the channels
     cluster_sync();
@@ -832,10 +871,12 @@ kvi_status attend_shared(const PromptCall &c, int32_t shared)
                                                                      : plan_rows(a, 1, all, all, shared);
     PromptPlan rest = tiles_fit(a, c.R, c.max_q, own, blocks, B) ? plan_tiles(a, c.R, c.total_q, c.max_q, own)
                                                                  : plan_rows(a, c.R, c.total_q, c.max_q, own);
-    // About a wave of blocks: they take a request's keys whole, and join the prefix's
-    // pieces themselves (64 requests x 30 to 700 keys 45.8 us, in pieces and with a
-    // join 52.0; 8 x 20 to 200 keys 16.0, 14.5; 24 x 30 to 2000 keys 67, 42).
-    const bool merges = !rest.tiles && (int64_t)c.R * a.kv_heads * rest.chunks >= 400;
+    // Blocks that take a request's keys whole join the prefix's pieces to them
+    // themselves, without a third kernel.  Where the keys are few, or the blocks nearly
+    // a wave (us, in pieces and with a join, and so; 8 KV heads, prefix 1600: 8 requests
+    // x 20 to 200 keys 14.5, 12.3; 16 x 300 23.0, 16.3; 32 x 300 25.6, 23.9; 20 x 700 25.9,
+    // 31.3; 40 x 700 41.7, 36.3; 24 x 2000 41, 65; prefix 10240: 64 x 30 to 700 52.0, 45.3).
+    const bool merges = !rest.tiles && (own <= 384 || (int64_t)c.R * a.kv_heads * rest.chunks >= 300);
     if (merges) {
         rest.S = 1;
         rest.span = kLongest;

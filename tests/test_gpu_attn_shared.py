@@ -65,15 +65,20 @@ def test_lengths(Hq, H, D, B, shared, n_q, ctx):
     assert torch.equal(c.out, first)
 
 
-@pytest.mark.parametrize("more", [0, 3])
+@pytest.mark.parametrize("more,long", [(0, 0), (3, 0), (0, 1500), (3, 1500)])
 @pytest.mark.parametrize("Hq,H,D,B", LAYOUTS)
-def test_many(Hq, H, D, B, more):
-    """Enough requests that the prefix is read by itself: single tokens, and a few questions among them."""
+def test_many(Hq, H, D, B, more, long):
+    """Enough requests that the prefix is read by itself: single tokens, and a few questions among them; own keys
+    that are one piece, and several."""
     R = 90 if H * D > 64 else 200
+    if long:
+        R = min(R, 240 // H)
     n_q = [1 if i % 7 else 0 for i in range(R)]
     n_q[5:5 + more] = [9, 4, 13][:more]
     blocks = -(-(9 << 20) // ((R - 1) * H * D) // B) + 1
-    c = Case(Hq, H, D, B, n_q, [n + (37 * i) % 150 for i, n in enumerate(n_q)], blocks * B, seed=Hq * D + B)
+    ctx = [n + (37 * i) % 150 for i, n in enumerate(n_q)]
+    ctx[3] += long
+    c = Case(Hq, H, D, B, n_q, ctx, blocks * B, seed=Hq * D + B)
     c.run()
     c.check()
     first = c.out.clone()
