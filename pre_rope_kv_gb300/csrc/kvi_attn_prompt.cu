@@ -4,6 +4,12 @@
 // A KV head's query rows are its group's heads for every token, token first:
 // row = token * G + head, so the rows that read the same keys share a tile.
 //
+// Two more calls are forms of the same kernels: windows (kvi_attn_window; a row sees
+// the last keys and the first ones, and tiles that no row of a block sees are left
+// out) and batches with a shared prefix (kvi_attn_shared; the prefix is attended by
+// all rows of the batch as one request's, beside each request's other keys, and the
+// pieces joined).
+//
 // Long prompts run on the tensor cores' tiles (kvi_attn_tile.cu).  rows_kernel
 // here takes 8 or 16 rows a block, for few rows and for the page and head sizes
 // that the tiles do not take.  Its products are S^T = K Q^T (16 keys x 8 rows) and
@@ -13,7 +19,11 @@
 // block's warps join at the end, and blocks that share a request's keys through one
 // another's shared memory as a cluster, or in a second kernel.  Where a block's rows are all there are (decoding steps) the
 // cache's bytes bound it: 64 requests x 1.5 k keys, 8 KV heads of 128 channels,
-// 71 us, 5.3 TB/s.
+// 71 us, 5.3 TB/s; 64 windows of 1024 keys 50 us, 5.4 TB/s; 64 users' 30 to 700 keys
+// beside a prefix of 10240 for all 45 us.  (Slower: the keys of all requests in a row
+// cut into as many chunks of one length as there are blocks at a time, 64 windows of
+// 1024 keys 87 us and of 4096 keys 267 instead of 170: some SMs reach memory faster
+// than others, and blocks that are handed out as they end leave those more.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -869,8 +879,11 @@ kvi_status attend_shared(const PromptCall &c, int32_t shared)
     const int32_t all = (int32_t)tokens;
     const PromptPlan first = tiles_fit(a, 1, all, shared, blocks, B) ? plan_tiles(a, 1, all, all, shared)
                                                                      : plan_rows(a, 1, all, all, shared);
-    PromptPlan rest = tiles_fit(a, c.R, c.max_q, own, blocks, B) ? plan_tiles(a, c.R, c.total_q, c.max_q, own)
-                                                                 : plan_rows(a, c.R, c.total_q, c.max_q, own);
+    // (few keys of up to 32 rows take the rows form, whose blocks then join the prefix's
+    // pieces: 24 requests x 3 tokens 39.4, 34.1, x 5 42.4, 39.8, x 10 54.7, 56.2)
+    const bool few = own <= 384 && (int64_t)c.max_q * (a.q_heads / a.kv_heads) <= 32;
+    PromptPlan rest = !few && tiles_fit(a, c.R, c.max_q, own, blocks, B) ? plan_tiles(a, c.R, c.total_q, c.max_q, own)
+                                                                         : plan_rows(a, c.R, c.total_q, c.max_q, own);
     // Blocks that take a request's keys whole join the prefix's pieces to them
     // themselves, without a third kernel.  Where the keys are few, or the blocks nearly
     // a wave (us, in pieces and with a join, and so; 8 KV heads, prefix 1600: 8 requests

@@ -29,12 +29,20 @@
 // past the end become zero, and an infinity or NaN is replaced by zero and
 // added, at the end, to the rows that see it.
 //
+// With a window a block walks over the tiles of the first `sink` keys and those from
+// its first row's window on; masks are a bit a column, so that they cost two
+// instructions a score.  The keys that a batch shares are one request's, whose rows
+// are all the batch's and see all of them; each piece's results go to the join.
+//
 // What bounds it: the matrix products (4 D flops per pair of row and key) for
 // long prompts, and for ragged ones the 6 us or so that a block takes beside
 // them (Q and the first keys, the rows' results), which nothing overlaps as a
 // block fills its SM and its softmax warps store the results themselves.  32 heads over 8 of 128 channels: one prompt of 8192 tokens
 // 0.33 ms, 1670 TFLOP/s; 16 prompts of 1 to 2048 tokens and up to 1600 keys of
-// memory 0.19 ms, 1130 TFLOP/s.  No faster: blocks that stay and take several
+// memory 0.19 ms, 1130 TFLOP/s; with windows of 2048 keys 0.19 ms for 8192 tokens
+// (1.25 PFLOP/s), of 512 for the 16 prompts 0.092 ms (six tiles a block).  Of a
+// block's 16 us there 3.2 pass until its first scores (request, block table, Q and K),
+// 0.9 between the last P and O, 2.9 until the next block begins.  No faster: blocks that stay and take several
 // pairs of tiles, the softmax warps storing the results all the same (0.35 and
 // 0.19 ms), the pairs with the most keys first (0.34 and
 // 0.195 ms); slower: two warps issuing matrix instructions, copies by cp.async
