@@ -6,7 +6,9 @@ LLM Serving": exact top-k retrieval of memory facts by embedding similarity
 prompt positions they take (Section 5.1 / Theorem 6), and scatter-copy of K/V
 into a vLLM-style paged KV cache through a block table (Section 3.4); then the
 attention that reads the memory there: causal prompts, a 4-bit cache with its
-decoding step, and eviction from it by accumulated weight.
+decoding step, and eviction from it by accumulated weight; and a serving step
+around it: block tables from lengths, norms with rotation into the pages, windowed
+attention, and attention over a prefix that a batch shares.
 
 The compute is in ``libkvi.so`` (hand-written CUDA for sm_103a, C ABI in
 ``include/kvi.h``); this package is a ctypes binding with the same function
