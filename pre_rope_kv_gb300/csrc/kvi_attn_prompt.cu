@@ -867,8 +867,8 @@ kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t
 // MB, 14.4, 17.7; 2 x 10240, 42 MB, 19.1, 18.1; 64 x 256, 66 MB, 22.8, 25.8).
 bool shares(const kvi_attention &a, int32_t R, int64_t tokens, int32_t shared)
 {
-    const int64_t less = ((int64_t)R - 1) * shared * a.kv_heads * a.head_dim * 4;
-    return tokens * (a.q_heads / a.kv_heads) < 256 * (int64_t)R && less >= (32 << 20);
+    const double less = ((double)R - 1) * shared * a.kv_heads * a.head_dim * 4;
+    return tokens * (a.q_heads / a.kv_heads) < 256 * (int64_t)R && less >= (double)(32 << 20);
 }
 
 kvi_status attend_shared(const PromptCall &c, int32_t shared)
@@ -889,7 +889,8 @@ kvi_status attend_shared(const PromptCall &c, int32_t shared)
     // a wave (us, in pieces and with a join, and so; 8 KV heads, prefix 1600: 8 requests
     // x 20 to 200 keys 14.5, 12.3; 16 x 300 23.0, 16.3; 32 x 300 25.6, 23.9; 20 x 700 25.9,
     // 31.3; 40 x 700 41.7, 36.3; 24 x 2000 41, 65; prefix 10240: 64 x 30 to 700 52.0, 45.3).
-    const bool merges = !rest.tiles && (own <= 384 || (int64_t)c.R * a.kv_heads * rest.chunks >= 300);
+    const bool merges =
+        !rest.tiles && own <= kLongest && (own <= 384 || (int64_t)c.R * a.kv_heads * rest.chunks >= 300);
     if (merges) {
         rest.S = 1;
         rest.span = kLongest;

@@ -482,16 +482,19 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int seen0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
     // With a window the tiles are those of the first `sink` keys and those from the
-    // block's first window on: tile j from `from` on is at key from + 128 j, or
-    // `skip` keys further from tile `skip_at` on.
+    // block's first window on (from the copies' box that it begins in): tile j from
+    // `from` on is at key from + 128 j, or `skip` keys further from tile `skip_at` on.
     // Boxes before that window (no row sees them) are not read.
+    const int box_keys = kM >> box_shift;
     const int low = MODE == kWindow ? seen0 + tok0 - p.window + 1 : 0;
     int skip = 0, skip_at = 0;
     if (MODE == kWindow) {
-        const int start = max(0, low) / kM;
-        const int kept = min(start, (int)(((int64_t)p.sink + kM - 1) / kM));
-        skip = (start - kept) * kM;
-        skip_at = kept - from / kM;
+        const int64_t kept = ((int64_t)p.sink + kM - 1) / kM * kM;
+        const int start = max(0, low) / box_keys * box_keys;
+        if (start > kept) {
+            skip = start - (int)kept;
+            skip_at = (int)kept / kM - from / kM;
+        }
     }
     auto key_of = [&](int j) { return from + j * kM + (MODE == kWindow && j >= skip_at ? skip : 0); };
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
@@ -529,7 +532,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
     // two halves of 16 boxes.  A piece past the end, or of a block that is not
     // there, reads as zeros from past a page's last token.
-    const int half = lane >> box_shift, box = lane & ((1 << box_shift) - 1), box_keys = kM >> box_shift;
+    const int half = lane >> box_shift, box = lane & ((1 << box_shift) - 1);
     // (Its block is asked for a tile ahead.)
     int at_token = 0, at_block = 0;
     auto wanted = [&](int key) {
