@@ -92,7 +92,7 @@ struct TileTail {
     int32_t first[3][DP];   // first key whose value in a channel is +inf, -inf, NaN
     int32_t newest[3][DP];  // (windows) of the keys up to the block's first row, the last such
     int32_t part0;          // row of token 0 among the partial results
-    int32_t skip, skip_at;  // (windows) keys left out, and the tile from which on
+    int32_t skip, kept;     // (windows) keys left out, and the place from which on
 };
 
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -266,7 +266,7 @@ __device__ __forceinline__ void box3_out(const CUtensorMap *map, int x, int y, i
 // first key says who sees any, of the latter the last (the first `sink` keys
 // count as the latest of all).
 template <int DP, int MODE>
-__device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> &tl, int row0, int sink)
+__device__ __forceinline__ void check_values(uint8_t *v, int place0, TileTail<DP> &tl, int row0, int sink, int kept, int skip)
 {
     constexpr int kChunks = TileSmem<DP>::kTile / 16;
     const int lane = threadIdx.x & 31;
@@ -301,7 +301,7 @@ __device__ __forceinline__ void check_values(uint8_t *v, int key0, TileTail<DP> 
         for (int k = 0; k < 8; ++k) {
             const uint32_t b = e[8 * i + k];
             if ((b & 0x7f80u) != 0x7f80u) continue;
-            const int key = key0 + row, which = b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2, channel = 64 * half + 8 * chunk + k;
+            const int place = place0 + row, key = MODE == kWindow && place >= kept ? place + skip : place, which = b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2, channel = 64 * half + 8 * chunk + k;
             if (MODE == kWindow && key <= row0)
                 atomicMax(&tl.newest[which][channel], key < sink ? INT32_MAX : key);
             else
@@ -351,25 +351,32 @@ __device__ __forceinline__ uint32_t low_bits(int n)
     return m;
 }
 
-// Scores from column `vis` on are not seen, nor (windows) those from `past` on that
-// are below `low`.  A warp's rows are a few tokens, so few of its quarters of 32
-// columns are seen in part.
-template <int MODE>
-__device__ __forceinline__ void mask_scores(float *s, int vis, int past, int low)
+// Scores from column `vis` on are not seen.  A warp's rows are a few tokens, so few
+// of its quarters of 32 columns are seen in part.
+__device__ __forceinline__ void mask_scores(float *s, int vis)
 {
 #pragma unroll
     for (int q = 0; q < kM; q += 32) {
-        if (MODE == kWindow) {
-            // (a bit a column: three comparisons each take a tile 1.6 us longer)
-            const uint32_t seen = low_bits(vis - q) & (~low_bits(low - q) | low_bits(past - q));
-            if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) s[q + c] = (seen >> c) & 1u ? s[q + c] : neg_inf();
-            continue;
-        }
         if (!__any_sync(0xffffffffu, vis < q + 32)) continue;
 #pragma unroll
         for (int c = q; c < q + 32; ++c) s[c] = c < vis ? s[c] : neg_inf();
+    }
+}
+
+// With a window: nor those that are past the first `sink` and below `low`; from
+// column `kept` on a column's key is `skip` further.  (A bit a column: three
+// comparisons each take a tile 1.6 us longer.)
+__device__ __forceinline__ void mask_window(float *s, int vis, int sink, int low, int kept, int skip)
+{
+#pragma unroll
+    for (int q = 0; q < kM; q += 32) {
+        const uint32_t near = low_bits(kept - q);
+        const uint32_t first = low_bits(vis - q) & (~low_bits(low - q) | low_bits(sink - q));
+        const uint32_t rest = low_bits(vis - skip - q) & ~low_bits(low - skip - q);
+        const uint32_t seen = skip > 0 ? (first & near) | (rest & ~near) : first;
+        if (__all_sync(0xffffffffu, seen == 0xffffffffu)) continue;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[q + c] = (seen >> c) & 1u ? s[q + c] : neg_inf();
     }
 }
 
@@ -481,22 +488,24 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     const int seen0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
     const int from = split * p.span;    // a multiple of 128
-    // With a window the tiles are those of the first `sink` keys and those from the
-    // block's first window on (from the copies' box that it begins in): tile j from
-    // `from` on is at key from + 128 j, or `skip` keys further from tile `skip_at` on.
-    // Boxes before that window (no row sees them) are not read.
+    // With a window a block's keys are the first `sink` ones and those from its first
+    // window on, in whole boxes of the copies, one after the other: place u of them is
+    // key u, or u + skip from place `kept` on, and tile j has the places from from + 128 j
+    // on.  Boxes before that window (no row sees them) are not read.
     const int box_keys = kM >> box_shift;
     const int low = MODE == kWindow ? seen0 + tok0 - p.window + 1 : 0;
-    int skip = 0, skip_at = 0;
+    int skip = 0, kept = 0;
     if (MODE == kWindow) {
-        const int64_t kept = ((int64_t)p.sink + kM - 1) / kM * kM;
-        const int start = max(0, low) / box_keys * box_keys;
-        if (start > kept) {
-            skip = start - (int)kept;
-            skip_at = (int)kept / kM - from / kM;
+        const uint32_t first = ((uint32_t)p.sink + box_keys - 1) & ~(uint32_t)(box_keys - 1);
+        const uint32_t start = (uint32_t)max(0, low) & ~(uint32_t)(box_keys - 1);
+        if (start > first) {
+            // (the first keys fill up a tile of their own where sharing one saves none)
+            const uint32_t own = (first + kM - 1) & ~(uint32_t)(kM - 1), rest = seen0 + min(rq.n_q, tok0 + 2 * per) - start;
+            kept = (int)(start > own && (first + rest + kM - 1) / kM == (own + rest + kM - 1) / kM ? own : first);
+            skip = (int)start - kept;
         }
     }
-    auto key_of = [&](int j) { return from + j * kM + (MODE == kWindow && j >= skip_at ? skip : 0); };
+    auto key_at = [&](int u) { return MODE == kWindow && u >= kept ? u + skip : u; };
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
     int n_tiles[2];  // (indexed by constants alone: they stay in registers)
 #pragma unroll
@@ -516,7 +525,6 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (MODE == kWindow) {
         const int held = seen0 + min(rq.n_q, tok0 + 2 * per) - p.window;
         low_from = max(0, p.sink / kM - from / kM);
-        if (low_from >= skip_at && skip > 0) low_from = max(0, skip_at);
         low_end = held <= 0 ? 0 : max(0, (held - skip - from + kM - 1) / kM);
     }
     auto partly = [&](int j) { return j >= first_partly || (MODE == kWindow && j >= low_from && j < low_end); };
@@ -526,7 +534,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (tid == 0) {
         tl.part0 = MODE == kShared ? part0 : p.by_request ? r * p.max_q : rq.q0;
         tl.skip = skip;
-        tl.skip_at = skip_at;
+        tl.kept = kept;
     }
 
     // A tile of K (plane 0) or V (1) into a stage, a box a lane: 32 lanes cover
@@ -539,11 +547,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         return key < rq.ctx && (MODE != kWindow || key + box_keys > low || key < p.sink);
     };
     auto block_of = [&](int j) {
-        const int key = key_of(j) + box * box_keys;
+        const int key = key_at(from + j * kM + box * box_keys);
         return wanted(key) ? table[(uint32_t)key / (uint32_t)p.B] : -1;
     };
     auto look_up = [&](int j, int block) {
-        const int key = key_of(j) + box * box_keys;
+        const int key = key_at(from + j * kM + box * box_keys);
         const bool there = (uint32_t)block < (uint32_t)p.num_blocks;
         // (noted before the copy is asked for, so before its scores are looked at)
         if (warp == kCopyK && __any_sync(0xffffffffu, wanted(key) && !there) && lane == 0) {
@@ -643,7 +651,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 break;
             }
-            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, key_of(j), tl, sure - 1, p.sink);
+            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl, sure - 1, p.sink, kept, skip);
             if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
             __syncwarp();
         }
@@ -794,12 +802,18 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (in_part || lost) {
                 tmem_wait_ld(s + 64);
                 tmem_wait_ld(s + 96);
-                const int key0 = from + j * kM + (MODE == kWindow && j >= tl.skip_at ? tl.skip : 0);
-                mask_scores<MODE>(s, last + 1 - key0, p.sink - key0, last - p.window + 1 - key0);
+                const int place0 = from + j * kM;
+                if (MODE == kWindow)
+                    mask_window(s, last + 1 - place0, p.sink - place0, last - p.window + 1 - place0, tl.kept - place0, tl.skip);
+                else
+                    mask_scores(s, last + 1 - place0);
                 if (lost) {
                     uint32_t gone[4] = {0, 0, 0, 0};
-                    for (int c = 0; c < kM && key0 + c < rq.ctx; ++c)
-                        if ((uint32_t)table[(key0 + c) / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
+                    for (int c = 0; c < kM; ++c) {
+                        const int key = place0 + c + (MODE == kWindow && place0 + c >= tl.kept ? tl.skip : 0);
+                        if (key >= rq.ctx) break;
+                        if ((uint32_t)table[key / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
+                    }
 #pragma unroll
                     for (int c = 0; c < kM; ++c)
                         if ((gone[c >> 5] >> (c & 31)) & 1u) s[c] = neg_inf();
