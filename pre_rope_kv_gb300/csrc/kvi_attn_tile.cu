@@ -893,15 +893,16 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int parts = MODE == kShared ? p.parts : p.S, piece_no = MODE == kShared ? p.first + split : split;
             const float inv = whole ? (sum == 0.f ? 0.f : 1.f / sum) : 1.f;
             const bool odd = tl.odd != 0;
-            // 32 channels of the row
-            auto row_values = [&](int c, float *v) {
+            // 32 channels of the row: asked for, and as they are to be
+            auto ask_values = [&](int c, float *v) {
                 if (my > 0) {
                     tmem_load32(t_o + c, v);
-                    tmem_wait_ld(v);
                 } else {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) v[e] = 0.f;
                 }
+            };
+            auto take_values = [&](int c, float *v) {
                 if (odd) {
                     const float inf = __int_as_float(0x7f800000);
                     auto sees = [&](int which, int channel) {
@@ -917,16 +918,25 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     __syncwarp();
                 }
             };
+            auto row_values = [&](int c, float *v) {
+                ask_values(c, v);
+                tmem_wait_ld(v);
+                take_values(c, v);
+            };
             auto packed = [&](const float *v) {
                 return make_uint4(pack_bf16(v[0] * inv, v[1] * inv), pack_bf16(v[2] * inv, v[3] * inv),
                                   pack_bf16(v[4] * inv, v[5] * inv), pack_bf16(v[6] * inv, v[7] * inv));
             };
             if (full) {
                 uint8_t *to = base + Sm::kQ + i * Sm::kTile + row * 128;
-#pragma unroll 1
+                float both[2][32];  // (the next channels are on their way while these are stored)
+                ask_values(0, both[0]);
+#pragma unroll
                 for (int c = 0; c < DP; c += 32) {
-                    float v[32];
-                    row_values(c, v);
+                    float *v = both[(c >> 5) & 1];
+                    tmem_wait_ld(v);
+                    if (c + 32 < DP) ask_values(c + 32, both[((c >> 5) + 1) & 1]);
+                    take_values(c, v);
 #pragma unroll
                     for (int e = 0; e < 32; e += 8)
                         *reinterpret_cast<uint4 *>(to + (c >> 6) * kHalf + ((((c & 63) + e) / 8) ^ (row & 7)) * 16) = packed(v + e);
