@@ -294,7 +294,8 @@ def _stream(stream) -> int | None:
             # the handle itself, where this torch offers it: a Stream object
             # built for every call costs more than the call's launch
             raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-            _current = (torch.cuda.current_device,
+            torch.cuda.current_device()  # (which also makes sure that torch has its context)
+            _current = (getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device),
                         raw or (lambda device: torch.cuda.current_stream(device).cuda_stream))
         return _current[1](_current[0]())
     if isinstance(stream, int):
@@ -785,7 +786,7 @@ def kvi_attn_shared(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
 
 
 def _norm_weight(t, head_dim: int, name: str):
-    if t.dtype is not _types[0] or t.dim() != 1 or t.numel() != head_dim or not t.is_contiguous():
+    if t.dtype is not _types[0] or t.numel() != head_dim or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous bfloat16 [{head_dim}]")
     return t.data_ptr()
 
@@ -799,26 +800,33 @@ def kvi_norm_rope(a: Attention, spec: Rope, max_position: int, positions, q, k, 
     k_plain takes the keys before rotation.  q and q_out None: keys alone."""
     bf16, ints, longs, _ = _types or _dtypes()
     T, heads, kv, dim = positions.numel(), a.q_heads, a.kv_heads, a.head_dim
-    none = (None, 0)
     if cache is None:
         pool = None
     elif type(cache) is _Cache and (layer, kv, dim) in cache.fits:
         pool = cache.struct
     else:
         pool = _pool(a, cache, layer)
-    if positions.dtype is not ints or positions.dim() != 1 or not positions.is_contiguous():
+    if positions.dtype is not ints or not positions.is_contiguous():
         raise ValueError("positions must be contiguous int32")
-    if slots is not None and (slots.dtype is not longs or slots.dim() != 1 or not slots.is_contiguous() or slots.numel() < T):
+    if slots is not None and (slots.dtype is not longs or not slots.is_contiguous() or slots.numel() < T):
         raise ValueError(f"slots must be contiguous int64, at least {T} long")
+    qp = qs = qop = qos = kop = kos = kpp = kps = vp = vs = 0  # (0 is NULL)
+    if q is not None:
+        qp, qs = _rows(q, heads, dim, "q", T)
+    if q_out is not None:
+        qop, qos = _rows(q_out, heads, dim, "q_out", T)
+    kp, ks = _rows(k, kv, dim, "k", T)
+    if k_out is not None:
+        kop, kos = _rows(k_out, kv, dim, "k_out", T)
+    if k_plain is not None:
+        kpp, kps = _rows(k_plain, kv, dim, "k_plain", T)
+    if v is not None:
+        vp, vs = _rows(v, kv, dim, "v", T)
     _check(load_library().kvi_norm_rope(
-        a, spec, max_position, T, positions.data_ptr(), *(none if q is None else _rows(q, heads, dim, "q", T)),
-        *_rows(k, kv, dim, "k", T), None if q_weight is None else _norm_weight(q_weight, dim, "q_weight"),
-        None if k_weight is None else _norm_weight(k_weight, dim, "k_weight"), eps,
-        *(none if q_out is None else _rows(q_out, heads, dim, "q_out", T)),
-        *(none if k_out is None else _rows(k_out, kv, dim, "k_out", T)),
-        *(none if k_plain is None else _rows(k_plain, kv, dim, "k_plain", T)),
-        *(none if v is None else _rows(v, kv, dim, "v", T)), pool, layer, None if slots is None else slots.data_ptr(),
-        _word(status), _stream(stream)), "kvi_norm_rope")
+        a, spec, max_position, T, positions.data_ptr(), qp, qs, kp, ks,
+        None if q_weight is None else _norm_weight(q_weight, dim, "q_weight"),
+        None if k_weight is None else _norm_weight(k_weight, dim, "k_weight"), eps, qop, qos, kop, kos, kpp, kps, vp, vs, pool,
+        layer, None if slots is None else slots.data_ptr(), _word(status), _stream(stream)), "kvi_norm_rope")
 
 
 def _batch_fault(R, rows, ctx_lens, new_lens, block_tables, free, free_at, free_at_out, ctx_out, q_start, positions, slots):
