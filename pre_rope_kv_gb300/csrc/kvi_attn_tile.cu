@@ -23,35 +23,44 @@
 // and S of a tile is issued after the O of the tile before, so a tile's S
 // being there means that its O is at rest.
 //
+// A row tile's last keys are often few: where no row sees the second half of them,
+// its scores, weights and products are left out (37 tokens behind 1564 keys 14.8 to
+// 14.2 us, windows 1%; not of a batch's shared prefix, which is whole tiles and
+// took 3 us of 45 longer with it).
+//
 // Keys that only some rows see, or that lie past the end, are masked in S.
 // Their values must not reach the output either (0 * inf is NaN), so in the
 // few tiles that have such keys V is looked over in shared memory first: rows
 // past the end become zero, and an infinity or NaN is replaced by zero and
 // added, at the end, to the rows that see it.
 //
-// With a window a block walks over the tiles of the first `sink` keys and those from
-// its first row's window on; masks are a bit a column, so that they cost two
-// instructions a score.  The keys that a batch shares are one request's, whose rows
-// are all the batch's and see all of them; each piece's results go to the join.
+// With a window a block walks over the first `sink` keys and those from its first
+// row's window on, as if they lay one after the other; masks are a bit a column, so
+// that they cost two instructions a score.  The keys that a batch shares are one
+// request's, whose rows are all the batch's and see all of them; each piece's
+// results go to the join.
 //
 // What bounds it: the matrix products (4 D flops per pair of row and key) for
 // long prompts, and for ragged ones the 6 us or so that a block takes beside
 // them (Q and the first keys, the rows' results), which nothing overlaps as a
-// block fills its SM and its softmax warps store the results themselves.  32 heads over 8 of 128 channels: one prompt of 8192 tokens
-// 0.33 ms, 1670 TFLOP/s; 16 prompts of 1 to 2048 tokens and up to 1600 keys of
-// memory 0.19 ms, 1130 TFLOP/s; with windows of 2048 keys 0.19 ms for 8192 tokens
-// (1.25 PFLOP/s), of 512 for the 16 prompts 0.092 ms (six tiles a block).  Of a
-// block's 16 us there 3.2 pass until its first scores (request, block table, Q and K),
-// 0.9 between the last P and O, 2.9 until the next block begins.  No faster: blocks that stay and take several
-// pairs of tiles, the softmax warps storing the results all the same (0.35 and
-// 0.19 ms), the pairs with the most keys first (0.34 and
-// 0.195 ms); slower: two warps issuing matrix instructions, copies by cp.async
-// instead of the tensor map.
+// block fills its SM and its softmax warps store the results themselves.  32
+// heads over 8 of 128 channels: one prompt of 8192 tokens 0.33 ms, 1670 TFLOP/s;
+// 16 prompts of 1 to 2048 tokens and up to 1600 keys of memory 0.185 ms, 1150
+// TFLOP/s; with windows of 2048 keys 0.186 ms for 8192 tokens (1.29 PFLOP/s), of 512
+// for the 16 prompts 0.0856 ms (six tiles a block; 776 blocks are 5.1 for an SM, so
+// that some SMs take six).  Of a block's 15 us there 3.2 pass until its first scores (request,
+// block table, Q and K), 0.9 between the last P and O, 2.9 until the next block
+// begins.  No faster: blocks that stay and take several pairs of tiles, the softmax
+// warps storing the results all the same (0.35 and 0.19 ms), the pairs with the most
+// keys first (0.34 and 0.195 ms), a barrier for each row tile's end; slower: two warps
+// issuing matrix instructions, copies by cp.async instead of the tensor map, the
+// first K before the first V.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "kvi_attn.cuh"
 #include "kvi_sync.cuh"
@@ -353,10 +362,11 @@ __device__ __forceinline__ uint32_t low_bits(int n)
 
 // Scores from column `vis` on are not seen.  A warp's rows are a few tokens, so few
 // of its quarters of 32 columns are seen in part.
+template <int COLS>
 __device__ __forceinline__ void mask_scores(float *s, int vis)
 {
 #pragma unroll
-    for (int q = 0; q < kM; q += 32) {
+    for (int q = 0; q < COLS; q += 32) {
         if (!__any_sync(0xffffffffu, vis < q + 32)) continue;
 #pragma unroll
         for (int c = q; c < q + 32; ++c) s[c] = c < vis ? s[c] : neg_inf();
@@ -366,10 +376,11 @@ __device__ __forceinline__ void mask_scores(float *s, int vis)
 // With a window: nor those that are past the first `sink` and below `low`; from
 // column `kept` on a column's key is `skip` further.  (A bit a column: three
 // comparisons each take a tile 1.6 us longer.)
+template <int COLS>
 __device__ __forceinline__ void mask_window(float *s, int vis, int sink, int low, int kept, int skip)
 {
 #pragma unroll
-    for (int q = 0; q < kM; q += 32) {
+    for (int q = 0; q < COLS; q += 32) {
         const uint32_t near = low_bits(kept - q);
         const uint32_t first = low_bits(vis - q) & (~low_bits(low - q) | low_bits(sink - q));
         const uint32_t rest = low_bits(vis - skip - q) & ~low_bits(low - skip - q);
@@ -507,13 +518,16 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     }
     auto key_at = [&](int u) { return MODE == kWindow && u >= kept ? u + skip : u; };
     // tiles of keys that each row tile walks over; token t sees up to seen0 + t
-    int n_tiles[2];  // (indexed by constants alone: they stay in registers)
+    // (indexed by constants alone: they stay in registers)
+    int n_tiles[2];
+    bool half_last[2];  // no row sees the second half of the last one
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t0 = tok0 + i * per, t1 = min(rq.n_q, t0 + per);
         const int seen = (flat ? rq.ctx : seen0 + t1) - skip;
         const int end = t0 < rq.n_q ? min(seen, from + p.span) : 0;
         n_tiles[i] = max(0, (end - from + kM - 1) / kM);
+        half_last[i] = MODE != kShared && n_tiles[i] > 0 && end - from <= n_tiles[i] * kM - kM / 2;
     }
     const int n = max(n_tiles[0], n_tiles[1]);
     const int sure = seen0 + (flat ? 0 : tok0) + 1;  // keys below it are seen by every row
@@ -665,7 +679,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             // This warp's latencies set the pace of everything here, so between two
             // products there is little more than a wait, and what the next tile of
             // keys needs is looked after while products are queued.
-            constexpr uint32_t id_s = bf16_idesc(kM, false), id_o = bf16_idesc(DP, true);
+            constexpr uint32_t id_all = bf16_idesc(kM, false), id_half = bf16_idesc(kM / 2, false), id_o = bf16_idesc(DP, true);
             constexpr uint32_t kTileLo = Sm::kTile >> 4;
             const uint32_t q_lo = desc_lo(smem_u32(base + Sm::kQ)), ring_lo = desc_lo(smem_u32(base + Sm::kRing));
             const uint32_t full0 = smem_u32(&tl.full[0]), empty0 = smem_u32(&tl.empty[0]);
@@ -676,7 +690,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 fence_after();
                 return got;
             };
-            auto score_part = [&](int i, uint32_t stage, int k0, int k1) {
+            auto score_part = [&](int i, uint32_t stage, int k0, int k1, uint32_t id_s) {
 #pragma unroll
                 for (int k = k0; k < k1; ++k) {
                     const uint32_t at = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
@@ -693,6 +707,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                            add || half > 0 || k > 0);
             };
             const int n0 = n_tiles[0], n1 = n_tiles[1];
+            // the tile of each whose second half is left out
+            const int h0 = half_last[0] ? n0 - 1 : -1, h1 = half_last[1] ? n1 - 1 : -1;
             uint32_t fixes = 0;  // the phase of each v_fixed, a bit a stage
             // Tile j of the keys, V in stage `vs` and K of j + 1 in stage `ks`; V's
             // copy has been waited for.
@@ -707,28 +723,33 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                     if (!wait(p_bar, par)) return false;
                     values(0, vs, 0, j > 0);
                     if (more && !wait(full0 + 8 * ks, kph)) return false;
-                    if (!wait(p_bar + 8, par)) return false;
-                    values(0, vs, 1, j > 0);
+                    if (j != h0) {
+                        if (!wait(p_bar + 8, par)) return false;
+                        values(0, vs, 1, j > 0);
+                    }
                     if (!more0) mma_commit(lead, o_bar);
                 } else if (more && !wait(full0 + 8 * ks, kph)) {
                     return false;
                 }
                 if (more0) {
-                    score_part(0, ks, 0, kSteps);
+                    score_part(0, ks, 0, kSteps, j + 1 == h0 ? id_half : id_all);
                     mma_commit(lead, s_bar);
                 }
                 if (j < n1) {
                     if (!wait(p_bar + 16, par)) return false;
                     values(1, vs, 0, j > 0);
-                    if (!wait(p_bar + 24, par)) return false;
-                    values(1, vs, 1, j > 0);
+                    if (j != h1) {
+                        if (!wait(p_bar + 24, par)) return false;
+                        values(1, vs, 1, j > 0);
+                    }
                     if (!more1) mma_commit(lead, o_bar + 8);
                 }
-                if (more1) score_part(1, ks, 0, kSteps / 2);
+                const uint32_t id1 = j + 1 == h1 ? id_half : id_all;
+                if (more1) score_part(1, ks, 0, kSteps / 2, id1);
                 mma_commit(lead, empty0 + 8 * vs);
                 if (more && !wait(full0 + 8 * vnext, vnph)) return false;
                 if (more1) {
-                    score_part(1, ks, kSteps / 2, kSteps);
+                    score_part(1, ks, kSteps / 2, kSteps, id1);
                     mma_commit(lead, s_bar + 8);
                 }
                 if (more) mma_commit(lead, empty0 + 8 * ks);
@@ -737,11 +758,11 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             bool ok = wait(smem_u32(&tl.q_full), 0) && wait(full0, 0);
             if (ok) {
                 if (n0 > 0) {
-                    score_part(0, 0, 0, kSteps);
+                    score_part(0, 0, 0, kSteps, h0 == 0 ? id_half : id_all);
                     mma_commit(lead, s_bar);
                 }
                 if (n1 > 0) {
-                    score_part(1, 0, 0, kSteps);
+                    score_part(1, 0, 0, kSteps, h1 == 0 ? id_half : id_all);
                     mma_commit(lead, s_bar + 8);
                 }
                 mma_commit(lead, empty0);
@@ -778,52 +799,51 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         float m = neg_inf(), limit = real ? neg_inf() : __int_as_float(0x7f800000), ref = 0.f, sum = 0.f;
         const float lazy = kLazy / p.scale;
         bool ok = true;
-        for (int j = 0; j < my; ++j) {
-            const bool in_part = partly(j);
-            ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
-                ok = false;
-                __syncwarp();
-                break;
-            }
-            fence_after();
+        auto soften = [&](auto cols, int j, bool in_part) {
+            constexpr int kCols = decltype(cols)::value;  // that rows see any of
             // two loads of 64 scores; the first half's largest is found while the
             // second is on its way
-            float s[kM];
+            float s[kCols];
             tmem_load32(t_s, s);
             tmem_load32(t_s + 32, s + 32);
             tmem_wait_ld(s);
             tmem_wait_ld(s + 32);
-            tmem_load32(t_s + 64, s + 64);
-            tmem_load32(t_s + 96, s + 96);
+            if constexpr (kCols == kM) {
+                tmem_load32(t_s + 64, s + 64);
+                tmem_load32(t_s + 96, s + 96);
+            }
             float top;
             const bool lost = *reinterpret_cast<volatile int32_t *>(&tl.lost) != 0;
             if (in_part || lost) {
-                tmem_wait_ld(s + 64);
-                tmem_wait_ld(s + 96);
+                if constexpr (kCols == kM) {
+                    tmem_wait_ld(s + 64);
+                    tmem_wait_ld(s + 96);
+                }
                 const int place0 = from + j * kM;
                 if (MODE == kWindow)
-                    mask_window(s, last + 1 - place0, p.sink - place0, last - p.window + 1 - place0, tl.kept - place0, tl.skip);
+                    mask_window<kCols>(s, last + 1 - place0, p.sink - place0, last - p.window + 1 - place0, tl.kept - place0, tl.skip);
                 else
-                    mask_scores(s, last + 1 - place0);
+                    mask_scores<kCols>(s, last + 1 - place0);
                 if (lost) {
                     uint32_t gone[4] = {0, 0, 0, 0};
-                    for (int c = 0; c < kM; ++c) {
+                    for (int c = 0; c < kCols; ++c) {
                         const int key = place0 + c + (MODE == kWindow && place0 + c >= tl.kept ? tl.skip : 0);
                         if (key >= rq.ctx) break;
                         if ((uint32_t)table[key / p.B] >= (uint32_t)p.num_blocks) gone[c >> 5] |= 1u << (c & 31);
                     }
 #pragma unroll
-                    for (int c = 0; c < kM; ++c)
+                    for (int c = 0; c < kCols; ++c)
                         if ((gone[c >> 5] >> (c & 31)) & 1u) s[c] = neg_inf();
                 }
-                top = fmaxf(largest64(s), largest64(s + 64));
+                top = largest64(s);
+                if constexpr (kCols == kM) top = fmaxf(top, largest64(s + 64));
             } else {
                 top = largest64(s);
-                tmem_wait_ld(s + 64);
-                tmem_wait_ld(s + 96);
-                top = fmaxf(top, largest64(s + 64));
+                if constexpr (kCols == kM) {
+                    tmem_wait_ld(s + 64);
+                    tmem_wait_ld(s + 96);
+                    top = fmaxf(top, largest64(s + 64));
+                }
             }
             const bool move = top > limit;
             if (__any_sync(0xffffffffu, move)) {
@@ -850,7 +870,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const uint64_t scale2 = pair2(p.scale, p.scale), ref2 = pair2(-ref, -ref);
             uint64_t part[2] = {0, 0};  // sums of even and odd keys, twice
 #pragma unroll
-            for (int c = 0; c < kM; c += 32) {
+            for (int c = 0; c < kCols; c += 32) {
                 uint32_t w[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
@@ -869,7 +889,22 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             float a, b;
             split2(add2(part[0], part[1]), a, b);
             sum += a + b;
-            announce(tl.p_full[i][1]);
+            announce(tl.p_full[i][kCols == kM ? 1 : 0]);
+        };
+        for (int j = 0; j < my; ++j) {
+            const bool in_part = partly(j);
+            ok = ok && mbar_wait_brisk(smem_u32(&tl.s_full[i]), (uint32_t)(j & 1), kTileWaitNs);
+            if (!__all_sync(0xffffffffu, ok)) {
+                if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
+                ok = false;
+                __syncwarp();
+                break;
+            }
+            fence_after();
+            if (MODE != kShared && j + 1 == my && (i ? half_last[1] : half_last[0]))
+                soften(std::integral_constant<int, kM / 2>{}, j, in_part);
+            else
+                soften(std::integral_constant<int, kM>{}, j, in_part);
         }
         // ---- the rows' results; the values have been looked over
         asm volatile("bar.sync 1, 288;" ::: "memory");
