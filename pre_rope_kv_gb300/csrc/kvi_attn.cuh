@@ -314,11 +314,19 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 // A batch's own keys need nothing of the kernel before, which is that of its
 // shared prefix and began when all work before it had ended: they begin beside
-// it, and wait for it before they end, so that what follows finds both done.
+// it.  Blocks that join its results wait for it first; of the others one waits
+// before it ends, so that what follows finds both done, and the rest make room (24
+// questions over 10240 keys 67.2 to 66.3 us, 32 users' tokens 34.3 to 32.7).
 template <int MODE>
 __device__ __forceinline__ bool waits_last(const PromptParams &p)
 {
     return MODE == kShared && !p.flat;
+}
+
+template <int MODE>
+__device__ __forceinline__ void wait_at_end(const PromptParams &p)
+{
+    if (waits_last<MODE>(p) && blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
 }
 
 // The rows and keys of request r, or false when its lengths are not usable.

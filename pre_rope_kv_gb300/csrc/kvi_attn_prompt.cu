@@ -17,13 +17,14 @@
 // M.  Each warp streams its own tiles of 16 keys (16-byte asynchronous copies into
 // a ring of its own, so no block-wide wait) and keeps a softmax of its own; the
 // block's warps join at the end, and blocks that share a request's keys through one
-// another's shared memory as a cluster, or in a second kernel.  Where a block's rows are all there are (decoding steps) the
-// cache's bytes bound it: 64 requests x 1.5 k keys, 8 KV heads of 128 channels,
-// 71 us, 5.3 TB/s; 64 windows of 1024 keys 50 us, 5.4 TB/s; 64 users' 30 to 700 keys
-// beside a prefix of 10240 for all 45 us.  (Slower: the keys of all requests in a row
-// cut into as many chunks of one length as there are blocks at a time, 64 windows of
-// 1024 keys 87 us and of 4096 keys 267 instead of 170: some SMs reach memory faster
-// than others, and blocks that are handed out as they end leave those more.)
+// another's shared memory as a cluster, or in a second kernel.  Where a block's rows
+// are all there are (decoding steps) the cache's bytes bound it: 64 requests x 1.5 k
+// keys, 8 KV heads of 128 channels, 71 us, 5.3 TB/s; 64 windows of 1024 keys 50 us, 5.4
+// TB/s; 64 users' 30 to 700 keys beside a prefix of 10240 for all 41 us.  (Slower: the
+// keys of all requests in a row cut into as many chunks of one length as there are
+// blocks at a time, 64 windows of 1024 keys 87 us and of 4096 keys 267 instead of 170:
+// some SMs reach memory faster than others, and blocks that are handed out as they end
+// leave those more.)
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -111,12 +112,12 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
                                : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq) ||
                                      !sees_prefix(rq, p.shared)) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
-        if (waits_last<MODE>(p)) pdl_wait();
+        wait_at_end<MODE>(p);
         return;
     }
     const int rows = rq.n_q * p.G, row0 = chunk * 8 * NT;
     if (row0 >= rows) {
-        if (waits_last<MODE>(p)) pdl_wait();
+        wait_at_end<MODE>(p);
         return;
     }
     const int pieces = max(1, ((MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx) + p.span - 1) / p.span);
@@ -125,7 +126,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             cluster_sync();
             cluster_sync();
         }
-        if (waits_last<MODE>(p)) pdl_wait();
+        wait_at_end<MODE>(p);
         return;
     }
     const int seen_by_0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             if (d == 0) p.ml[part * parts + piece_no] = make_float2(M, L);
         }
     }
-    if (waits_last<MODE>(p)) pdl_wait();
+    wait_at_end<MODE>(p);
     if (!JOINED || whole) return;
     // ---- each block of the cluster that has keys joins a part of the channels
     cluster_sync();
@@ -871,29 +872,52 @@ bool shares(const kvi_attention &a, int32_t R, int64_t tokens, int32_t shared)
     return tokens * (a.q_heads / a.kv_heads) < 256 * (int64_t)R && less >= (double)(32 << 20);
 }
 
+// The prefix in fewer pieces than there are SMs, so that the other keys are read on the
+// rest of them meanwhile and a piece's fixed time is paid less often: as few as end with
+// all the work shared out, at a block's 8 us and 1.33 a tile of 128 keys (of 128
+// channels), and 35 KB a us of the others' keys for an SM, of which half of the most
+// there can be are taken to be there.  Not below 5 of 12, as they may be fewer still (us,
+// with a piece for every SM and so, single tokens; prefix 10240: 64 requests x 30 to 700
+// keys 48.6, 41.1, 40 x 30 to 700 41.1, 32.7, 64 x 30 to 2000 79.6, 69.3, 400 x 10 to 60
+// 103, 91; prefix 1600: 64 x 30 to 700 35.4, 32.4).
+void share_out(PromptPlan &first, const kvi_attention &a, int32_t R, int32_t shared, int32_t own)
+{
+    const double units = (double)first.chunks * a.kv_heads, tiles = 1.33 * ((shared + 127) / 128);
+    const double others = (double)R * own / 2 * a.kv_heads * a.head_dim * 4 / 35e3;
+    int S = (5 * first.S + 11) / 12;
+    while (S < first.S && 8 + tiles / S > (units * (8 * S + tiles) + others) / kPlanSms) ++S;
+    const int64_t span = ((int64_t)shared + S - 1) / S;
+    first.span = (int)std::max<int64_t>(first.span, std::min<int64_t>((span + 127) / 128 * 128, kLongest));
+    first.S = (int)(((int64_t)shared + first.span - 1) / first.span);
+}
+
 kvi_status attend_shared(const PromptCall &c, int32_t shared)
 {
     const kvi_attention &a = *c.a;
     const int32_t blocks = c.cache->num_blocks, B = c.cache->block_size, own = c.max_ctx - shared;
     const int64_t tokens = part_rows(c.R, c.total_q, c.max_q), rows = tokens * a.q_heads;
     const int32_t all = (int32_t)tokens;
-    const PromptPlan first = tiles_fit(a, 1, all, shared, blocks, B) ? plan_tiles(a, 1, all, all, shared)
-                                                                     : plan_rows(a, 1, all, all, shared);
-    // (few keys of up to 32 rows take the rows form, whose blocks then join the prefix's
-    // pieces: 24 requests x 3 tokens 39.4, 34.1, x 5 42.4, 39.8, x 10 54.7, 56.2)
-    const bool few = own <= 384 && (int64_t)c.max_q * (a.q_heads / a.kv_heads) <= 32;
+    PromptPlan first = tiles_fit(a, 1, all, shared, blocks, B) ? plan_tiles(a, 1, all, all, shared)
+                                                               : plan_rows(a, 1, all, all, shared);
+    // Few rows take the rows form, which reads the keys beside the prefix's tiles, several
+    // blocks to an SM (us, tiles and rows; prefix 10240, own keys up to: 24 requests x 3
+    // tokens, 900 48.9, 42.4, 2000 51.5, 44.6; 64 x 4, 2000 118, 94; 24 x 5, 100 42.3, 38.2,
+    // x 8, 100 45.0, 43.9, 600 x 6 49.1, 52.5, 2000 x 8 61.9, 70.1).
+    const int64_t most = (int64_t)c.max_q * (a.q_heads / a.kv_heads);
+    const bool few = most <= 16 || (own <= 384 && most <= 32);
     PromptPlan rest = !few && tiles_fit(a, c.R, c.max_q, own, blocks, B) ? plan_tiles(a, c.R, c.total_q, c.max_q, own)
                                                                          : plan_rows(a, c.R, c.total_q, c.max_q, own);
-    // Blocks that take a request's keys whole join the prefix's pieces to them
-    // themselves, without a third kernel.  Where the keys are few, or the blocks nearly
-    // a wave (us, in pieces and with a join, and so; 8 KV heads, prefix 1600: 8 requests
-    // x 20 to 200 keys 14.5, 12.3; 16 x 300 23.0, 16.3; 32 x 300 25.6, 23.9; 20 x 700 25.9,
-    // 31.3; 40 x 700 41.7, 36.3; 24 x 2000 41, 65; prefix 10240: 64 x 30 to 700 52.0, 45.3).
-    const bool merges =
-        !rest.tiles && own <= kLongest && (own <= 384 || (int64_t)c.R * a.kv_heads * rest.chunks >= 300);
+    // Blocks that take a request's keys whole may join the prefix's pieces to them
+    // themselves, without a third kernel, but hold their places until the prefix is done:
+    // where they all have places at once (us, with a join and so, one token; prefix 1600:
+    // 8 requests 14.3, 12.6, 16 17.0, 13.5, 24 21.9, 22.0, 32 19.2, 23.1; prefix 10240: 8
+    // 21.6, 19.6, 24 29.6, 28.4, 48 33.0, 33.1; 10 x 4 tokens 26.7, 33.5).
+    const bool merges = !rest.tiles && own <= 384 && most <= 8 && (int64_t)c.R * a.kv_heads * rest.chunks <= 200;
     if (merges) {
         rest.S = 1;
         rest.span = kLongest;
+    } else if (first.tiles && !rest.tiles) {
+        share_out(first, a, c.R, shared, own);
     }
     const int parts = first.S + (merges ? 0 : rest.S);
     const size_t ml = up256((size_t)rows * parts * a.head_dim * 4);

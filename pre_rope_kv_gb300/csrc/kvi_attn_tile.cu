@@ -487,14 +487,14 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         item -= __shfl_sync(0xffffffffu, sum, 31);
     }
     if (r < 0) {
-        if (waits_last<MODE>(p)) pdl_wait();
+        wait_at_end<MODE>(p);
         return;
     }
     const int tok0 = pair * 2 * per;  // the block's first token
     const int keys = MODE == kWindow ? min(rq.ctx, p.cap) : rq.ctx;  // that its pieces are for
     const bool whole = MODE != kShared && keys <= p.span;            // they are one piece
     if (split > 0 && (int64_t)split * p.span >= keys) {
-        if (waits_last<MODE>(p)) pdl_wait();
+        wait_at_end<MODE>(p);
         return;
     }
     const int seen0 = flat ? rq.ctx - 1 : rq.ctx - rq.n_q;  // last position that token 0 sees
@@ -1044,7 +1044,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
         }
     }
-    if (waits_last<MODE>(p)) pdl_wait();
+    wait_at_end<MODE>(p);
     fence_before();
     __syncthreads();
     if (warp == kMmaWarp) {

@@ -88,7 +88,7 @@ def test_many(Hq, H, D, B, more, long):
 
 @pytest.mark.parametrize("Hq,H,D,B", [(6, 1, 256, 8), (3, 1, 80, 5), (40, 2, 32, 16), (10, 2, 96, 24), (4, 1, 128, 16)])
 def test_a_wave_of_requests(Hq, H, D, B):
-    """So many that each block joins the prefix's pieces to its request's keys."""
+    """So many that their blocks are several waves, beside the prefix's."""
     R = 420
     n_q = [1 if i % 11 else 0 for i in range(R)]
     blocks = -(-(9 << 20) // ((R - 1) * H * D) // B) + 1
