@@ -664,8 +664,11 @@ KVI_API size_t kvi_attn_shared_workspace_bytes(const kvi_attention *a, int32_t R
  * rows are read).  shared is a multiple of block_size, in [0, max_ctx) and in the
  * tables (0: this is kvi_attn_prompt), and each request that has rows has ctx -
  * n >= shared, so that its rows see the whole prefix.  Rows, outputs and errors
- * are as for kvi_attn_prompt; also KVI_ERR_OUT_OF_RANGE for a request with fewer
- * keys before its rows than the prefix has (its outputs are not written). */
+ * are as for kvi_attn_prompt; with a prefix also KVI_ERR_OUT_OF_RANGE for a request
+ * with fewer keys before its rows than the prefix has (its outputs are not written),
+ * and, as the batch's rows go over the prefix together, for a batch whose rows
+ * d_q_start[0] .. d_q_start[R]-1 lie outside [0, total_q) or are more than R *
+ * max_q (no outputs are written) and for a request whose rows are not among them. */
 KVI_API kvi_status kvi_attn_shared(const kvi_attention *a, int32_t R, const void *d_q,
                                    int64_t q_row_stride, const int32_t *d_q_start, int32_t total_q,
                                    int32_t max_q, const int32_t *d_ctx_lens, int32_t max_ctx,
