@@ -345,38 +345,33 @@ __device__ __forceinline__ bool request_span(int r, const int32_t *q_start, int 
            (int64_t)o.ctx <= (int64_t)max_blocks * block_size;
 }
 
-// The rows of a batch, from its first request's to its last one's: whether they are
-// rows of q, and no more than its requests can have.
-__device__ __forceinline__ bool batch_span(const int32_t *q_start, int R, int total_q, int max_q, int &b0, int &b1)
+// Whether a batch's rows, b0 = q_start[0] .. b1 = q_start[R] - 1, are rows of q, and no
+// more than its requests can have.
+__device__ __forceinline__ bool batch_fits(int b0, int b1, int R, int total_q, int max_q)
 {
-    b0 = q_start[0];
-    b1 = q_start[R];
     return b0 >= 0 && b1 >= b0 && b1 <= total_q && (int64_t)b1 - b0 <= (int64_t)R * max_q;
 }
 
-// Whether a usable request may be attended in a batch with a shared prefix (0:
-// none): its rows are the batch's, and see all of the prefix.  The batch's rows are
-// attended over the prefix as one request's, or not at all, so every kernel goes by
-// this, those that read the prefix with each request's other keys included.
-__device__ __forceinline__ bool in_batch(const RequestSpan &o, const int32_t *q_start, int R, int total_q, int max_q,
-                                         int shared, int &part0)
+// Whether a usable request is attended in a batch with a shared prefix: its rows are
+// the batch's, and see all of the prefix.  The batch's rows are attended over the
+// prefix as one request's, or not at all, so every kernel goes by this, those that
+// read the prefix with each request's other keys included.
+__device__ __forceinline__ bool request_fits(const RequestSpan &o, int b0, int b1, int R, int total_q, int max_q, int shared)
 {
-    part0 = 0;
-    if (shared == 0) return true;
-    int b0, b1;
-    const bool good = batch_span(q_start, R, total_q, max_q, b0, b1);
-    part0 = good ? o.q0 - b0 : 0;
-    return good && o.q0 >= b0 && o.q0 + o.n_q <= b1 && (o.n_q == 0 || o.ctx - o.n_q >= shared);
+    return batch_fits(b0, b1, R, total_q, max_q) && o.q0 >= b0 && o.q0 + o.n_q <= b1 &&
+           (o.n_q == 0 || o.ctx - o.n_q >= shared);
 }
 
-// The rows and keys of request r in a batch with a shared prefix: its keys past
-// the prefix, and its first row's number in the batch.
+// The rows and keys of request r in a batch with a shared prefix: its keys past the
+// prefix, and its first row's number in the batch.
 __device__ __forceinline__ bool request_past_prefix(int r, const int32_t *q_start, int R, int total_q, int max_q,
                                                     const int32_t *ctx_lens, int max_ctx, int max_blocks,
                                                     int block_size, int shared, RequestSpan &o, int &part0)
 {
-    const bool good = request_span(r, q_start, total_q, max_q, ctx_lens, max_ctx, max_blocks, block_size, o) &&
-                      in_batch(o, q_start, R, total_q, max_q, shared, part0);
+    const int b0 = q_start[0], b1 = q_start[R];
+    bool good = request_span(r, q_start, total_q, max_q, ctx_lens, max_ctx, max_blocks, block_size, o);
+    good = good && request_fits(o, b0, b1, R, total_q, max_q, shared);
+    part0 = good ? o.q0 - b0 : 0;
     o.ctx = max(0, o.ctx - shared);
     return good;
 }
@@ -386,9 +381,8 @@ __device__ __forceinline__ bool request_past_prefix(int r, const int32_t *q_star
 // number; without any, no rows).  Every warp for itself.
 __device__ __forceinline__ int batch_rows(const PromptParams &p, RequestSpan &o)
 {
-    const int lane = threadIdx.x & 31;
-    int b0, b1;
-    const bool good = batch_span(p.q_start, p.R, p.total_q, p.max_q, b0, b1);
+    const int lane = threadIdx.x & 31, b0 = p.q_start[0], b1 = p.q_start[p.R];
+    const bool good = batch_fits(b0, b1, p.R, p.total_q, p.max_q);
     o = RequestSpan{b0, good ? b1 - b0 : 0, p.shared};
     for (int r0 = 0; r0 < p.R; r0 += 32) {
         const int r = r0 + lane;
@@ -414,7 +408,7 @@ __device__ __forceinline__ void join_rows(const JoinParams &p, int x, int r)
                                  p.shared, q, part0))
             return;
     } else if (!request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.block_size, q) ||
-               !in_batch(q, p.q_start, p.R, p.total_q, p.max_q, p.shared, part0)) {
+               (p.shared && !request_fits(q, p.q_start[0], p.q_start[p.R], p.R, p.total_q, p.max_q, p.shared))) {
         return;
     }
     const int pieces = p.first + (min(q.ctx, p.cap) + p.span - 1) / p.span;

@@ -110,7 +110,8 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
     } else if (MODE == kShared ? !request_past_prefix(r, p.q_start, p.R, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
                                                       p.max_blocks, p.B, p.shared, rq, part0)
                                : !request_span(r, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx, p.max_blocks, p.B, rq) ||
-                                     !in_batch(rq, p.q_start, p.R, p.total_q, p.max_q, p.shared, part0)) {
+                                     (MODE == kCausal && p.shared &&
+                                      !request_fits(rq, p.q_start[0], p.q_start[p.R], p.R, p.total_q, p.max_q, p.shared))) {
         if (tid == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         wait_at_end<MODE>(p);
         return;

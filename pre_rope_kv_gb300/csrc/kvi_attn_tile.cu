@@ -465,7 +465,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                                                               p.max_ctx, p.max_blocks, p.B, p.shared, c, c_part0)
                                         : request_span(r0 + lane, p.q_start, p.total_q, p.max_q, p.ctx_lens, p.max_ctx,
                                                        p.max_blocks, p.B, c) &&
-                                              in_batch(c, p.q_start, p.R, p.total_q, p.max_q, p.shared, c_part0));
+                                              (MODE != kCausal || p.shared == 0 ||
+                                               request_fits(c, p.q_start[0], p.q_start[p.R], p.R, p.total_q, p.max_q, p.shared)));
         if (asked && !good && h == 0 && split == 0 && warp == 0) record_status(p.status, KVI_ERR_OUT_OF_RANGE);
         const int pairs = good ? (c.n_q + 2 * per - 1) / (2 * per) : 0;
         int sum = pairs;
