@@ -291,11 +291,19 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
                 }
             __syncwarp();  // the next matrix instruction wants the warp as one
         }
-        // ---- P rounds to bf16 for the second product, whose operands are of one type
-        // and V's is bf16: each weight by up to 2^-8 of itself, which leaves the output
-        // 0.0023 off (mean square, of it) where its own rounding alone leaves 0.0017.  The
-        // sum takes P unrounded.
-        uint32_t b0[NT], b1[NT];
+        // ---- P in bf16 for the second product, whose operands are of one type and V's is
+        // bf16.  Rounded once, each weight is up to 2^-8 of itself off, which leaves the
+        // output 0.0023 off (mean square, of it) where its own rounding alone leaves
+        // 0.0017.  Windows over few rows, which HBM bounds, take P as a sum of two bf16
+        // numbers, 2^-16 of itself off at most, and are 0.0017 off (us, with two numbers
+        // and one: 64 windows of 1024 keys, 128 channels 51.1, 50.7, 64 channels 33.7, 32.0,
+        // 256 channels 69.7, 68.6).  Blocks of 16 rows, which issue bounds, do not (16
+        // prompts with windows of 32 keys 329, 313), nor do the users' own keys beside a
+        // shared prefix: its tiles round P all the same, so that the output would be 0.0023
+        // off with it too.  The plain calls have one rounding, as their tiles.  The sum
+        // takes P unrounded.
+        constexpr bool kTwoTerms = MODE == kWindow && NT == 1;
+        uint32_t b0[NT], b1[NT], rest0[NT], rest1[NT];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float m0 = m[nt][0] == neg_inf() ? 0.f : m[nt][0], m1 = m[nt][1] == neg_inf() ? 0.f : m[nt][1];
@@ -303,12 +311,18 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             const float p2 = exp2_fast(s[nt][2] - m0), p3 = exp2_fast(s[nt][3] - m1);
             l[nt][0] += p0 + p2;
             l[nt][1] += p1 + p3;
-            b0[nt] = transpose8x8(pack_bf16(p0, p1));
-            b1[nt] = transpose8x8(pack_bf16(p2, p3));
+            const uint32_t near0 = pack_bf16(p0, p1), near1 = pack_bf16(p2, p3);
+            b0[nt] = transpose8x8(near0);
+            b1[nt] = transpose8x8(near1);
+            if (kTwoTerms) {
+                rest0[nt] = transpose8x8(pack_bf16(p0 - bf16_lo(near0), p1 - bf16_hi(near0)));
+                rest1[nt] = transpose8x8(pack_bf16(p2 - bf16_lo(near1), p3 - bf16_hi(near1)));
+            }
         }
         // a tile that some row sees only in part: an infinity or NaN among its
         // values must not reach the rows that do not see it (0 * inf)
         const bool partly = key0 + 15 > least || (MODE == kWindow && key0 < held && key0 + 16 > p.sink);
+        uint32_t was[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             uint32_t a[4];
@@ -340,6 +354,15 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a[0], a[1], a[2], a[3], b0[nt], b1[nt]);
+            if (kTwoTerms) {  // a step behind, as a product waits for the last one to the same sums
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (i > 0) mma16816(o[nt][i > 0 ? i - 1 : 0], was[0], was[1], was[2], was[3], rest0[nt], rest1[nt]);
+                    if (i + 1 == KS) mma16816(o[nt][i], a[0], a[1], a[2], a[3], rest0[nt], rest1[nt]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) was[j] = a[j];
+            }
         }
         __syncwarp();  // the stage has been read
         stage = stage + 1 == kRowStages ? 0 : stage + 1;
