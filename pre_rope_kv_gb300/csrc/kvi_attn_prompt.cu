@@ -181,6 +181,14 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             qf[nt][k][1] = real ? *reinterpret_cast<const uint32_t *>(q + 16 * k + 8) : 0u;
         }
     }
+    // (of P's second numbers: an infinity among the values times a zero or less of them
+    // must not make it a NaN, so that these are added to what is finite at the end)
+    constexpr bool kTwoTerms = MODE == kWindow && NT == 1 && DP <= 128;
+    float rest[kTwoTerms ? KS : 1][4];
+#pragma unroll
+    for (int i = 0; i < (kTwoTerms ? KS : 1); ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) rest[i][j] = 0.f;
     float o[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -287,6 +295,10 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
                     for (int i = 0; i < KS; ++i) {
                         o[nt][i][c] *= f;
                         o[nt][i][c + 2] *= f;
+                        if (kTwoTerms) {
+                            rest[kTwoTerms ? i : 0][c] *= f;
+                            rest[kTwoTerms ? i : 0][c + 2] *= f;
+                        }
                     }
                 }
             __syncwarp();  // the next matrix instruction wants the warp as one
@@ -296,14 +308,13 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
         // output 0.0023 off (mean square, of it) where its own rounding alone leaves
         // 0.0017.  Windows over few rows, which HBM bounds, take P as a sum of two bf16
         // numbers, 2^-16 of itself off at most, and are 0.0017 off (us, with two numbers
-        // and one: 64 windows of 1024 keys, 128 channels 51.1, 50.7, 64 channels 33.7, 32.0,
-        // 256 channels 69.7, 68.6).  Blocks of 16 rows, which issue bounds, do not (16
-        // prompts with windows of 32 keys 329, 313), nor do the users' own keys beside a
-        // shared prefix: its tiles round P all the same, so that the output would be 0.0023
-        // off with it too.  The plain calls have one rounding, as their tiles.  The sum
-        // takes P unrounded.
-        constexpr bool kTwoTerms = MODE == kWindow && NT == 1;
-        uint32_t b0[NT], b1[NT], rest0[NT], rest1[NT];
+        // and one: 64 windows of 1024 keys, 128 channels 51.3, 50.7, 64 channels 29.7,
+        // 32.1).  The others do not: blocks of 16 rows, which issue bounds (16 prompts with
+        // windows of 32 keys 329, 313), heads of 256 channels, whose sums then do not find
+        // room (64 windows 106.7, 68.7), and the users' own keys beside a shared prefix,
+        // whose tiles round P all the same (the output would be 0.0023 off with it too).  The
+        // plain calls have one rounding, as their tiles.  The sum takes P unrounded.
+        uint32_t b0[NT], b1[NT], r0 = 0, r1 = 0;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float m0 = m[nt][0] == neg_inf() ? 0.f : m[nt][0], m1 = m[nt][1] == neg_inf() ? 0.f : m[nt][1];
@@ -315,14 +326,13 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             b0[nt] = transpose8x8(near0);
             b1[nt] = transpose8x8(near1);
             if (kTwoTerms) {
-                rest0[nt] = transpose8x8(pack_bf16(p0 - bf16_lo(near0), p1 - bf16_hi(near0)));
-                rest1[nt] = transpose8x8(pack_bf16(p2 - bf16_lo(near1), p3 - bf16_hi(near1)));
+                r0 = transpose8x8(pack_bf16(p0 - bf16_lo(near0), p1 - bf16_hi(near0)));
+                r1 = transpose8x8(pack_bf16(p2 - bf16_lo(near1), p3 - bf16_hi(near1)));
             }
         }
         // a tile that some row sees only in part: an infinity or NaN among its
         // values must not reach the rows that do not see it (0 * inf)
         const bool partly = key0 + 15 > least || (MODE == kWindow && key0 < held && key0 + 16 > p.sink);
-        uint32_t was[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             uint32_t a[4];
@@ -354,15 +364,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a[0], a[1], a[2], a[3], b0[nt], b1[nt]);
-            if (kTwoTerms) {  // a step behind, as a product waits for the last one to the same sums
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    if (i > 0) mma16816(o[nt][i > 0 ? i - 1 : 0], was[0], was[1], was[2], was[3], rest0[nt], rest1[nt]);
-                    if (i + 1 == KS) mma16816(o[nt][i], a[0], a[1], a[2], a[3], rest0[nt], rest1[nt]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) was[j] = a[j];
-            }
+            if (kTwoTerms) mma16816(rest[kTwoTerms ? i : 0], a[0], a[1], a[2], a[3], r0, r1);
         }
         __syncwarp();  // the stage has been read
         stage = stage + 1 == kRowStages ? 0 : stage + 1;
@@ -387,8 +389,13 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
             float *dst = s_o + (warp * 8 * NT + n) * kO + g;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
-                dst[16 * i] = o[nt][i][c];
-                dst[16 * i + 8] = o[nt][i][c + 2];
+                float a = o[nt][i][c], b = o[nt][i][c + 2];
+                if (kTwoTerms) {
+                    if (fabsf(a) <= 3.4028235e38f) a += rest[kTwoTerms ? i : 0][c];
+                    if (fabsf(b) <= 3.4028235e38f) b += rest[kTwoTerms ? i : 0][c + 2];
+                }
+                dst[16 * i] = a;
+                dst[16 * i + 8] = b;
             }
         }
     __syncthreads();
