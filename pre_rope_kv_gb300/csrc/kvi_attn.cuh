@@ -134,7 +134,8 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 // Every kernel of these calls may begin while the previous kernel of the
 // stream drains, waits for it before it touches memory (pdl_wait), and lets
 // the next one begin (pdl_launch_dependents): what a launch costs is hidden
-// behind the work before it.  What they read may thus be written during their
+// behind the work before it.  (One does not wait at its begin: see waits_last.)
+// What they read may thus be written during their
 // lifetime, so none of it goes through the read-only path (__ldg).  `blocks` > 1:
 // the blocks along x form clusters of so many.
 template <typename P, typename... Args>
@@ -312,15 +313,31 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 
 }  // namespace
 
-// A batch's own keys need nothing of the kernel before, which is that of its
-// shared prefix and began when all work before it had ended: they begin beside
-// it.  Blocks that join its results wait for it first; of the others one waits
-// before it ends, so that what follows finds both done, and the rest make room (24
-// questions over 10240 keys 67.2 to 66.3 us, 32 users' tokens 34.3 to 32.7).
+// A batch's own keys need nothing of the kernel before, which is that of its shared
+// prefix: they begin beside it.  That this is in order:
+//   - all blocks of the prefix's kernel wait for the work before it and only then let
+//     this one begin, so that all of what that work wrote has been made visible to the
+//     device by then; a fence takes the place of the wait here, so that nothing older is
+//     read;
+//   - blocks that join the prefix's pieces wait for its kernel first; of the others one
+//     waits before it ends (early ends included), so that what follows, and waits for
+//     this kernel, finds both done.  The rest make room (24 questions over 10240 keys
+//     67.2 to 66.3 us, 32 users' tokens 34.3 to 32.7);
+//   - a block that waits for the prefix's kernel holds up none of its blocks: they all
+//     had their places before.
 template <int MODE>
 __device__ __forceinline__ bool waits_last(const PromptParams &p)
 {
     return MODE == kShared && !p.flat;
+}
+
+template <int MODE>
+__device__ __forceinline__ void wait_at_begin(const PromptParams &p)
+{
+    if (waits_last<MODE>(p))
+        __threadfence();
+    else
+        pdl_wait();
 }
 
 template <int MODE>

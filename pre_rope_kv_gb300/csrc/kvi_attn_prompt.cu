@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int split = blockIdx.x % p.S, chunk = (blockIdx.x / p.S) % p.chunks, h = blockIdx.x / p.S / p.chunks;
     int r = blockIdx.y;
-    if (!waits_last<MODE>(p)) pdl_wait();
+    wait_at_begin<MODE>(p);
     pdl_launch_dependents();
     RequestSpan rq;
     int part0 = 0;

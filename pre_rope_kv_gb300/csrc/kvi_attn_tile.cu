@@ -442,7 +442,7 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     const int split = (int)(blockIdx.x - rest * (uint32_t)p.S);
     const int per = p.per;
     const bool flat = MODE == kShared && p.flat;
-    if (!waits_last<MODE>(p)) pdl_wait();
+    wait_at_begin<MODE>(p);
     pdl_launch_dependents();
     // Blocks are for the tile pairs that there are, numbered request after request
     // and from a request's end (its heaviest) to its start; a warp looks over 32
