@@ -786,7 +786,7 @@ def kvi_attn_shared(a: Attention, q, q_start, max_q: int, ctx_lens, max_ctx: int
 
 
 def _norm_weight(t, head_dim: int, name: str):
-    if t.dtype is not _types[0] or t.numel() != head_dim or not t.is_contiguous():
+    if t.dtype is not (_types or _dtypes())[0] or t.numel() != head_dim or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous bfloat16 [{head_dim}]")
     return t.data_ptr()
 
@@ -831,7 +831,7 @@ def kvi_norm_rope(a: Attention, spec: Rope, max_position: int, positions, q, k, 
 
 def _batch_fault(R, rows, ctx_lens, new_lens, block_tables, free, free_at, free_at_out, ctx_out, q_start, positions, slots):
     """Raise for the first tensor that kvi_batch_tables does not take."""
-    _, ints, longs, _ = _types
+    _, ints, longs, _ = _types or _dtypes()
     for t, name, kind, n in ((ctx_lens, "ctx_lens", ints, R), (new_lens, "new_lens", ints, R), (ctx_out, "ctx_out", ints, R),
                              (q_start, "q_start", ints, R + 1), (free, "free", ints, free.numel()),
                              (free_at, "free_at", longs, 2), (free_at_out, "free_at_out", longs, 2),

@@ -310,7 +310,8 @@ __device__ __forceinline__ void check_values(uint8_t *v, int place0, TileTail<DP
         for (int k = 0; k < 8; ++k) {
             const uint32_t b = e[8 * i + k];
             if ((b & 0x7f80u) != 0x7f80u) continue;
-            const int place = place0 + row, key = MODE == kWindow && place >= kept ? place + skip : place, which = b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2, channel = 64 * half + 8 * chunk + k;
+            const int place = place0 + row, key = MODE == kWindow && place >= kept ? place + skip : place;
+            const int which = b == 0x7f80u ? 0 : b == 0xff80u ? 1 : 2, channel = 64 * half + 8 * chunk + k;
             if (MODE == kWindow && key <= row0)
                 atomicMax(&tl.newest[which][channel], key < sink ? INT32_MAX : key);
             else
@@ -667,7 +668,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 if (lane == 0) record_status(p.status, KVI_ERR_TIMEOUT);
                 break;
             }
-            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl, sure - 1, p.sink, kept, skip);
+            check_values<DP, MODE>(base + Sm::kRing + (slot % Sm::kStages) * Sm::kTile, from + j * kM, tl, sure - 1, p.sink,
+                                   kept, skip);
             if (lane == 0) mbar_arrive(smem_u32(&tl.v_fixed[slot % Sm::kStages / 2]));
             __syncwarp();
         }
@@ -823,7 +825,8 @@ tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
                 }
                 const int place0 = from + j * kM;
                 if (MODE == kWindow)
-                    mask_window<kCols>(s, last + 1 - place0, p.sink - place0, last - p.window + 1 - place0, tl.kept - place0, tl.skip);
+                    mask_window<kCols>(s, last + 1 - place0, p.sink - place0, last - p.window + 1 - place0,
+                                       tl.kept - place0, tl.skip);
                 else
                     mask_scores<kCols>(s, last + 1 - place0);
                 if (lost) {
