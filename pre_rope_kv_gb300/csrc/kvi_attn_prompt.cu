@@ -19,8 +19,8 @@
 // block's warps join at the end, and blocks that share a request's keys through one
 // another's shared memory as a cluster, or in a second kernel.  Where a block's rows
 // are all there are (decoding steps) the cache's bytes bound it: 64 requests x 1.5 k
-// keys, 8 KV heads of 128 channels, 71 us, 5.3 TB/s; 64 windows of 1024 keys 50 us, 5.4
-// TB/s; 64 users' 30 to 700 keys beside a prefix of 10240 for all 41 us.  (Slower: the
+// keys, 8 KV heads of 128 channels, 71 us, 5.3 TB/s; 64 windows of 1024 keys 51 us, 5.3
+// TB/s; 64 users' 30 to 700 keys beside a prefix of 10240 for all 42 us.  (Slower: the
 // keys of all requests in a row cut into as many chunks of one length as there are
 // blocks at a time, 64 windows of 1024 keys 87 us and of 4096 keys 267 instead of 170:
 // some SMs reach memory faster than others, and blocks that are handed out as they end
@@ -896,7 +896,8 @@ kvi_status attend_prompts(const PromptCall &c, int mode, int32_t window, int32_t
 // requests x 37 tokens 67, 193; 8 x 37 58, 67; 4 x 64 51, 43; 16 x 128 274, 226),
 // nor below 32 MB less to read, which cost what a launch and a join do (single
 // tokens: 8 requests x 256 keys 12.0, 7.4; 4 x 1600, 20 MB, 13.3, 10.9; 16 x 512, 31
-// MB, 14.4, 17.7; 2 x 10240, 42 MB, 19.1, 18.1; 64 x 256, 66 MB, 22.8, 25.8).
+// MB, 14.4, 17.7; 2 x 10240, 42 MB, 19.1, 18.1; 64 x 256, 66 MB, 22.8, 25.8).  (Next to the
+// limit bytes alone do not tell: 16 x 512 and 2 x 10240 go the slower way.)
 bool shares(const kvi_attention &a, int32_t R, int64_t tokens, int32_t shared)
 {
     const double less = ((double)R - 1) * shared * a.kv_heads * a.head_dim * 4;

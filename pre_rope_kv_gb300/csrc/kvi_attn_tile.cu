@@ -11,7 +11,11 @@
 //                  as it lies in the cache (channels contiguous)
 // P rounds to bf16, as the instruction takes both operands in one type and V is
 // bf16; its sum takes it unrounded.  The output is 0.0023 off (mean square, of it),
-// where its own rounding to bf16 alone leaves 0.0017.
+// where its own rounding to bf16 alone leaves 0.0017.  P as a sum of two bf16 numbers,
+// which has room in tensor memory, leaves that too, and is not taken, as the second
+// product twice and the softmax's part of it cost a quarter or more: 16 prompts with
+// windows 106 us instead of 86, 8192 tokens 244 instead of 186, 64 users over a shared
+// prefix 49 instead of 41, 24 questions 76 instead of 67.
 // The two tiles alternate: while one tile's scores go through the softmax the
 // tensor cores work on the other's products.  Two warps copy, K and V (a box per
 // lane: a piece of a cache page, 64 channels wide), one looks over V where it has

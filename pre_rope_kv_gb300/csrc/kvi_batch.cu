@@ -9,7 +9,7 @@
 // request's last one, partly filled) or from the ring (a new one).
 //
 // A launch has as many blocks as rows want, and each scans the lengths of all
-// requests by itself (48 KB at most, from L2): no block waits for another, and a
+// requests by itself (32 KB at most, from L2): no block waits for another, and a
 // step is one launch without a workspace.  What bounds it is that chain of
 // latencies (lengths, scan, search, a block's number, a store): 64 requests of one
 // token 3.7 us, 16 prompts of 3 thousand rows 3.4 us, 1000 requests of 71 thousand

@@ -14,7 +14,7 @@
 // a weight a key gets the same bits as kvi_inject_paged gives it.
 //
 // What bounds it: HBM.  8192 rows of 32 + 8 + 8 heads of 128, to q, the pages and
-// plain keys, 40 us, 5.4 TB/s, 79 % of a copy: a warp stays with a part of the
+// plain keys, 40 us, 5.3 TB/s, 78 % of a copy: a warp stays with a part of the
 // rows, whose weights it keeps, and bulk copies fetch its next two meanwhile.  (A
 // warp per 4 units that loads, computes and ends, however many of them an SM
 // holds: 50 us and more; with a lane's table entries loaded directly, 52 us.)
