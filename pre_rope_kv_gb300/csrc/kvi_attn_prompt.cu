@@ -292,13 +292,14 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
                     m[nt][c] = top;
                     l[nt][c] *= f;
 #pragma unroll
+                    for (int i = 0; i < (kTwoTerms ? KS : 0); ++i) {
+                        rest[i][c] *= f;
+                        rest[i][c + 2] *= f;
+                    }
+#pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         o[nt][i][c] *= f;
                         o[nt][i][c + 2] *= f;
-                        if (kTwoTerms) {
-                            rest[kTwoTerms ? i : 0][c] *= f;
-                            rest[kTwoTerms ? i : 0][c + 2] *= f;
-                        }
                     }
                 }
             __syncwarp();  // the next matrix instruction wants the warp as one
@@ -309,7 +310,7 @@ __global__ void __launch_bounds__(kRowWarps<DP, MODE> * 32) rows_kernel(const __
         // 0.0017.  Windows over few rows, which HBM bounds, take P as a sum of two bf16
         // numbers, 2^-16 of itself off at most, and are 0.0017 off (us, with two numbers
         // and one: 64 windows of 1024 keys, 128 channels 51.3, 50.7, 64 channels 29.7,
-        // 32.1).  The others do not: blocks of 16 rows, which issue bounds (16 prompts with
+        // 32.1; 4 windows, 128 channels 12.1, 11.6).  The others do not: blocks of 16 rows, which issue bounds (16 prompts with
         // windows of 32 keys 329, 313), heads of 256 channels, whose sums then do not find
         // room (64 windows 106.7, 68.7), and the users' own keys beside a shared prefix,
         // whose tiles round P all the same (the output would be 0.0023 off with it too).  The
