@@ -132,12 +132,12 @@ kvi_status cuda_status(cudaError_t e, const char *where);
 #ifdef __CUDACC__
 
 // Every kernel of these calls may begin while the previous kernel of the
-// stream drains, waits for it before it touches memory (pdl_wait), and lets
-// the next one begin (pdl_launch_dependents): what a launch costs is hidden
-// behind the work before it.  (One does not wait at its begin: see waits_last.)
-// What they read may thus be written during their
-// lifetime, so none of it goes through the read-only path (__ldg).  `blocks` > 1:
-// the blocks along x form clusters of so many.
+// stream drains, waits for it before it touches memory (pdl_wait; the one kernel
+// that does not is described at waits_last), and lets the next one begin
+// (pdl_launch_dependents): what a launch costs is hidden behind the work before it.
+// What they read may thus be written during their lifetime, so none of it goes
+// through the read-only path (__ldg).  `blocks` > 1: the blocks along x form clusters
+// of so many.
 template <typename P, typename... Args>
 inline cudaError_t launch_chained_clusters(void (*kernel)(P, Args...), int blocks, dim3 grid, dim3 block, size_t smem,
                                            cudaStream_t s, const std::decay_t<P> &p, const std::decay_t<Args> &...args)
@@ -318,7 +318,7 @@ __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w 
 //   - all blocks of the prefix's kernel wait for the work before it and only then let
 //     this one begin, so that all of what that work wrote has been made visible to the
 //     device by then; a fence takes the place of the wait here, so that nothing older is
-//     read;
+//     read (24 questions 67.7 us, 66.6 without it, 64 users' tokens 41.9 and 41.6);
 //   - blocks that join the prefix's pieces wait for its kernel first; of the others one
 //     waits before it ends (early ends included), so that what follows, and waits for
 //     this kernel, finds both done.  The rest make room (24 questions over 10240 keys
